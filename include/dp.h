@@ -24,7 +24,7 @@
  *    cached driver entry point, four streams with their events per device
  *    for dp_all_gather_copy_engine (created on its first call), and the
  *    host-side bookkeeping (with their own streams and events) of the
- *    reducer and settle-pipe objects the caller creates and destroys.
+ *    reducer, settle-pipe and AdamW objects the caller creates and destroys.
  *  - Chunks: a rank buffer of N elements is split into K chunks of
  *    C = ceil(N/K) elements; chunk c is [c*C, min((c+1)*C, N)) (the page's
  *    "each worker splits its gradient into K chunks").
@@ -83,6 +83,9 @@ typedef enum {
 } dp_status_t;
 
 typedef enum { DP_FP32 = 0, DP_BF16 = 1 } dp_dtype_t;
+
+/* How an optimizer keeps its states. */
+typedef enum { DP_STATE_FP32 = 0, DP_STATE_8BIT = 1 } dp_state_t;
 
 #define DP_MAX_K 16
 #define DP_MAX_MICROBATCHES 16
@@ -556,6 +559,101 @@ DP_API dp_status_t dp_reducer_set_dry_run(dp_reducer_t* r, int on);
 DP_API int dp_reducer_launch_log(dp_reducer_t* r, int* buckets, int cap);
 DP_API dp_status_t dp_reducer_set_overlap(dp_reducer_t* r, int on);
 DP_API dp_status_t dp_reducer_wait(dp_reducer_t* r, dp_stream_t stream);
+
+/*
+ * The global norm of a list of gradients and the coefficient that clips it:
+ * the step between the gradient reduce-scatter and the optimizer ("CMU 11-868
+ * L14-L15 ...", "Intuition: data parallelism has only one thing to
+ * synchronize": the synchronised gradient then updates the parameters).
+ *
+ * grads: HOST array of n device pointers, numels[t] elements of grad_dtype
+ * each (a tensor of 0 elements takes no part; its pointer may be NULL).
+ *   norm = sqrt(sum over all elements of g^2)
+ *   coef = min(1, max_norm / (norm + 1e-6)), or NaN when norm is not finite
+ * norm and coef: one device float each; either may be NULL, not both.
+ * max_norm > 0 (infinity: coef is 1).  An empty list has norm 0.
+ * Squares are summed in fp32 over 32 elements and in double beyond; the
+ * order is fixed by the sizes alone, so a list gives the same bits under any
+ * CTA limit.  A gradient above 1.8e19 in magnitude overflows its square and
+ * makes the norm infinite.
+ *
+ * workspace: device memory of at least dp_grad_norm_workspace_size(n) bytes,
+ * 16-byte aligned, overlapping nothing; its first 4 bytes are zero before
+ * the first call, and every call leaves them zero.  Calls that may overlap
+ * on the GPU need separate workspaces.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ */
+DP_API dp_status_t dp_grad_norm(const void* const* grads, const size_t* numels, int n,
+                                dp_dtype_t grad_dtype, float max_norm, float* norm, float* coef,
+                                void* workspace, size_t workspace_bytes, dp_stream_t stream);
+DP_API dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes);
+
+/*
+ * AdamW (decoupled weight decay) over a list of tensors in one launch per
+ * 384 of them: the update of each rank's parameter shard from its reduced
+ * gradient shard ("Sharding and Parallelism", section "FSDP and ZeRO": the
+ * optimizer states b_o are sharded with the parameters and gradients).
+ *
+ * dp_adamw_create checks a list of tensors once and keeps it (host memory
+ * only); the buffers stay the caller's and are read and written by every
+ * step.  All pointers are device pointers:
+ *   param       numel elements of param_dtype, updated in place
+ *   grad        numel elements of grad_dtype
+ *   copy        NULL, or numel bf16: the new parameter rounded to bf16
+ *   exp_avg, exp_avg_sq
+ *               DP_STATE_FP32: numel floats each, m and v
+ *               DP_STATE_8BIT: numel bytes each, e4m3 codes of m and of
+ *               sqrt(v); with exp_avg_scale / exp_avg_sq_scale, ceil(numel /
+ *               DP_STATE_BLOCK) floats each: a value is its code times the
+ *               scale of its block of DP_STATE_BLOCK consecutive elements
+ *   weight_decay  this tensor's (0: none)
+ * All-zero states are those of a run's start.  A tensor of 0 elements takes
+ * no part.  Any element alignment; fastest where fp32 arrays are 32-byte,
+ * bf16 arrays 16-byte and code arrays 8-byte aligned.  No buffer that is
+ * written may overlap another buffer of the list.
+ *
+ * dp_adamw_step: step t >= 1, for every element, in fp32 with one rounding
+ * per operation:
+ *   g = grad * *grad_scale          (grad_scale NULL: 1)
+ *   m = m * beta1 + g * (1 - beta1)
+ *   v = v * beta2 + (g * g) * (1 - beta2)
+ *   p = p * (1 - lr * weight_decay)
+ *       - (lr / (1 - beta1^t)) * (m / (sqrt(v) * (1 / sqrt(1 - beta2^t)) + eps))
+ * the factors in t, lr and the betas alone in double, rounded once.  8-bit
+ * states: the step uses this step's unrounded m and v; then each block's m
+ * and sqrt(v) are stored as codes nearest (ties to even) to value * (448 /
+ * largest magnitude of the block), and a sqrt(v) above zero keeps at least
+ * the smallest code (2^-9).  Of a block whose largest magnitude is below
+ * 2^-110 m is dropped.
+ * grad_scale: NULL or a device float (dp_grad_norm's coef).  A NaN there
+ * leaves every buffer as it is.
+ * schedule: NULL, or 3 device floats (lr, 1 - beta1^t, 1 - beta2^t) that are
+ * read when the kernel runs in place of the call's values: a captured step
+ * is replayed with new ones.
+ * Requires 0 <= beta < 1, eps > 0, finite lr.  Steps of one object are
+ * serialised on the host; the caller orders them on the GPU.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ */
+#define DP_STATE_BLOCK 256
+typedef struct {
+  void* param;
+  const void* grad;
+  void* copy;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  size_t numel;
+  double weight_decay;
+} dp_adamw_tensor_t;
+typedef struct dp_adamw dp_adamw_t;
+DP_API dp_status_t dp_adamw_create(const dp_adamw_tensor_t* tensors, int n,
+                                   dp_dtype_t param_dtype, dp_dtype_t grad_dtype,
+                                   dp_state_t state, dp_adamw_t** out);
+DP_API dp_status_t dp_adamw_step(dp_adamw_t* o, double lr, double beta1, double beta2, double eps,
+                                 long long step, const float* grad_scale, const float* schedule,
+                                 dp_stream_t stream);
+DP_API void dp_adamw_destroy(dp_adamw_t* o);
 
 /*
  * The parameter all-gather on the GPU's copy engines instead of its SMs

@@ -17,6 +17,9 @@ DP_FP32 = 0
 DP_BF16 = 1
 DP_MAX_K = 16
 DP_MAX_MICROBATCHES = 16
+DP_STATE_FP32 = 0
+DP_STATE_8BIT = 1
+DP_STATE_BLOCK = 256  # elements that share one scale of an 8-bit state
 DP_WGRAD_NOALLOC_MAX_BYTES = 8 << 20  # the built-in scratch of the no-allocation call
 
 DP_OK = 0
@@ -31,6 +34,14 @@ LIB_PATH = os.path.join(_HERE, "libdp_gb300.so")
 
 _lock = threading.Lock()
 _lib = None
+
+
+class AdamwTensor(ctypes.Structure):
+    """dp_adamw_tensor_t"""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+                ("numel", ctypes.c_size_t), ("weight_decay", ctypes.c_double)]
 
 
 class DpError(RuntimeError):
@@ -95,6 +106,13 @@ def load() -> ctypes.CDLL:
             "dp_reducer_set_overlap": [vp, i32],
             "dp_reducer_wait": [vp, vp],
             "dp_all_gather_copy_engine": [pp, i32, sz, i32, pp, vp],
+            "dp_grad_norm": [pp, ctypes.POINTER(ctypes.c_size_t), i32, i32, f32, vp, vp, vp, sz,
+                             vp],
+            "dp_grad_norm_workspace_size": [i32, ctypes.POINTER(ctypes.c_size_t)],
+            "dp_adamw_create": [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32,
+                                ctypes.POINTER(ctypes.c_void_p)],
+            "dp_adamw_step": [vp, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                              ctypes.c_double, ctypes.c_longlong, vp, vp, vp],
             "dp_set_cta_limits": [i32, i32],
             "dp_set_collective_variant": [i32],
             "dp_get_collective_variant": [],
@@ -108,6 +126,8 @@ def load() -> ctypes.CDLL:
             fn.restype = i32
         lib.dp_reducer_destroy.argtypes = [vp]
         lib.dp_reducer_destroy.restype = None
+        lib.dp_adamw_destroy.argtypes = [vp]
+        lib.dp_adamw_destroy.restype = None
         lib.dp_status_string.argtypes = [i32]
         lib.dp_status_string.restype = ctypes.c_char_p
         lib.dp_version.argtypes = []
@@ -450,6 +470,56 @@ def dp_reducer_launch_log(h) -> list:
     buf = (ctypes.c_int * max(1, n))()
     lib.dp_reducer_launch_log(h, buf, n)
     return list(buf[:n])
+
+
+def _sizes(numels):
+    vals = [int(v) for v in numels]
+    return (ctypes.c_size_t * max(1, len(vals)))(*vals)
+
+
+def dp_grad_norm(grads, numels, n, grad_dtype, max_norm, norm, coef, workspace,
+                 workspace_bytes=None, stream=None, check=True) -> int:
+    """``grads`` / ``numels``: sequences, or the ctypes arrays of a list that is kept."""
+    wp, wb = _ws(workspace, workspace_bytes)
+    g = grads if isinstance(grads, ctypes.Array) else _parray(grads)
+    ne = numels if isinstance(numels, ctypes.Array) else _sizes(numels)
+    st = load().dp_grad_norm(g, ne, n, dtype_code(grad_dtype), max_norm, _ptr(norm), _ptr(coef),
+                             wp, wb, _stream(stream))
+    return _ret(st, "dp_grad_norm", check)
+
+
+def dp_grad_norm_workspace_size(n) -> int:
+    b = ctypes.c_size_t(0)
+    _ret(load().dp_grad_norm_workspace_size(n, ctypes.byref(b)), "dp_grad_norm_workspace_size",
+         True)
+    return int(b.value)
+
+
+def dp_adamw_create(tensors, n, param_dtype, grad_dtype, state, check=True):
+    """``tensors``: n dicts or tuples of AdamwTensor's fields (tensors, pointers
+    or None).  Returns (status, handle); handle is an opaque int (0 on failure)."""
+    names = [f[0] for f in AdamwTensor._fields_]
+    arr = (AdamwTensor * max(1, n))()
+    for i, row in enumerate(tensors):
+        vals = dict(row) if isinstance(row, dict) else dict(zip(names, row))
+        for k, v in vals.items():
+            setattr(arr[i], k, v if k in ("numel", "weight_decay") else _ptr(v))
+    h = ctypes.c_void_p()
+    st = load().dp_adamw_create(arr, n, dtype_code(param_dtype), dtype_code(grad_dtype),
+                                int(state), ctypes.byref(h))
+    _ret(st, "dp_adamw_create", check)
+    return st, (h.value or 0)
+
+
+def dp_adamw_step(h, lr, beta1, beta2, eps, step, grad_scale=None, schedule=None, stream=None,
+                  check=True) -> int:
+    st = load().dp_adamw_step(h, lr, beta1, beta2, eps, step, _ptr(grad_scale), _ptr(schedule),
+                              _stream(stream))
+    return _ret(st, "dp_adamw_step", check)
+
+
+def dp_adamw_destroy(h) -> None:
+    load().dp_adamw_destroy(h)
 
 
 def dp_all_gather_copy_engine(shards, K, shard_elems, dtype, out, stream=None,

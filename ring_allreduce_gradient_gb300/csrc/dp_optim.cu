@@ -1,0 +1,735 @@
+// dp_optim.cu -- the optimizer step on the reduced gradients: the global
+// gradient norm with its clip coefficient, and AdamW over a list of tensors
+// with 32-bit or 8-bit states.
+//
+// The mathematics (decoupled weight decay; t counts steps from 1):
+//   g' = c g                    c: the clip coefficient, min(1, max / (||g|| + 1e-6))
+//   m' = b1 m + (1 - b1) g'
+//   v' = b2 v + (1 - b2) g'^2
+//   p' = p (1 - lr wd) - lr / (1 - b1^t) * m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
+// in fp32, one rounding per operation (no contraction), with the factors that
+// depend on t alone formed in double on the host.
+//
+// 8-bit states: m and r = sqrt(v) are e4m3 codes with one fp32 scale for each
+// 256 consecutive elements, the block's largest magnitude at e4m3's largest
+// value (448).  The root of v is stored because the step divides by it: e4m3
+// spans 2^17.8 between its smallest and largest value, so the stored v spans
+// 2^35.  A root that would round to zero while v > 0 takes the smallest code
+// instead (a zero root under a nonzero m would make the next steps
+// unbounded).  The step itself uses the unrounded m' and v' of this step.
+//
+// Both kernels are bound by memory: AdamW moves 30 bytes an element (fp32
+// parameters, gradients and states, bf16 copy) for about 15 operations, the
+// 8-bit form 18, the norm 4.  A warp takes 256 consecutive elements of one
+// tensor at a time (an 8-bit block), each lane eight of them as one 32-byte
+// load per fp32 array, so every array's load is issued before any is used.
+// Tensors whose pointers are not aligned for that, and the last elements of a
+// tensor, go lane by lane over consecutive elements with the same arithmetic.
+
+#include "dp_launch.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <new>
+#include <vector>
+
+namespace {
+
+using namespace dpk;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnit = 256;         // elements a warp takes at once = an 8-bit block
+constexpr int kNormUnit = 1024;    // the norm's: four loads in flight per lane
+constexpr int kNormSlots = 608;    // partial sums of one norm launch: four CTAs on each of 152 SMs
+constexpr float kE4m3Max = 448.0f;
+constexpr float kE4m3Min = 0.001953125f;      // 2^-9, the smallest e4m3 value above zero
+constexpr float kTiny = 7.703719777548943e-34f;  // 2^-110: below it a block's reciprocal is left out
+
+// ---- eight consecutive elements --------------------------------------------
+
+__device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st8(float* p, const float (&v)[8]) {
+  asm volatile("st.global.cs.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld8(const uint16_t* p, float (&v)[8]) {
+  uint4 raw[1] = {ld_v4(p)};
+  Vec8<uint16_t>::widen(raw, v);
+}
+__device__ __forceinline__ void st8(uint16_t* p, const float (&v)[8]) { store8_bf16(p, v); }
+
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// e4m3 -> fp32 through fp16, which holds every e4m3 value.
+__device__ __forceinline__ void widen_e4m3x2(uint16_t c, float& lo, float& hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+}
+__device__ __forceinline__ void ld8_codes(const uint8_t* p, uint32_t (&c)[2]) {
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(c[0]), "=r"(c[1]) : "l"(p));
+}
+__device__ __forceinline__ void st8_codes(uint8_t* p, const uint32_t (&c)[2]) {
+  asm volatile("st.global.cs.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(c[0]), "r"(c[1]) : "memory");
+}
+__device__ __forceinline__ void widen_codes(const uint32_t (&c)[2], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    widen_e4m3x2((uint16_t)(c[i >> 1] >> (16 * (i & 1))), v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void pack_codes(const float (&v)[8], uint32_t (&c)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    c[i] = (uint32_t)e4m3x2(v[4 * i], v[4 * i + 1]) |
+           ((uint32_t)e4m3x2(v[4 * i + 2], v[4 * i + 3]) << 16);
+}
+
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(uint16_t* p, float v) { *p = bf16_rn(v); }
+
+// ---- AdamW -------------------------------------------------------------------
+
+template <int CAP>
+struct AdamwParams {
+  void* param[CAP];
+  const void* grad[CAP];
+  uint16_t* copy[CAP];
+  void* m[CAP];
+  void* v[CAP];
+  float* m_scale[CAP];
+  float* v_scale[CAP];
+  unsigned long long numel[CAP];
+  unsigned ustart[CAP + 1];  // prefix sums of units (kUnit elements) per tensor
+  double decay[CAP];
+  uint8_t vec_ok[CAP];
+  int n;
+  double lr;
+  float beta1, omb1, beta2, omb2, eps, step_size, inv_root;
+  const float* grad_scale;
+  const float* schedule;
+};
+
+struct Hyper {
+  float coef, beta1, omb1, beta2, omb2, eps, step_size, inv_root;
+};
+
+// One element: the new m, v and root of v, and the parameter's step.
+__device__ __forceinline__ float adamw_one(float p, float g, float& m, float& v, float& root,
+                                           float keep, const Hyper& h) {
+  g = __fmul_rn(g, h.coef);
+  m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.omb1));
+  v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, g), h.omb2));
+  root = __fsqrt_rn(v);
+  const float denom = __fadd_rn(__fmul_rn(root, h.inv_root), h.eps);
+  return __fsub_rn(__fmul_rn(p, keep), __fmul_rn(h.step_size, __fdiv_rn(m, denom)));
+}
+
+// A block's largest magnitude over the warp.  Magnitudes order as their bit
+// patterns; a NaN's is above every other, so it reaches the scale.
+__device__ __forceinline__ float warp_max_abs(const float (&v)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+}
+
+__device__ __forceinline__ float code_factor(float top) {
+  return top > kTiny ? __fmul_rn(__frcp_rn(top), kE4m3Max) : (top <= kTiny ? 0.0f : top);
+}
+
+template <typename PT, typename GT, bool S8, int CAP>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
+  const int lane = threadIdx.x & 31;
+  const unsigned units = a.ustart[a.n];
+  const unsigned stride = gridDim.x * kWarps;
+  unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= units) return;
+  Hyper h{1.0f, a.beta1, a.omb1, a.beta2, a.omb2, a.eps, a.step_size, a.inv_root};
+  double lr = a.lr;
+  if (a.grad_scale) h.coef = __ldg(a.grad_scale);
+  if (a.schedule) {
+    lr = (double)__ldg(a.schedule);
+    h.step_size = (float)(lr / (double)__ldg(a.schedule + 1));
+    h.inv_root = (float)(1.0 / sqrt((double)__ldg(a.schedule + 2)));
+  }
+  // the tensor of the first unit: the last t with ustart[t] <= u
+  int t = 0;
+  for (int hi = a.n - 1; t < hi;) {
+    const int mid = (t + hi + 1) >> 1;
+    if (a.ustart[mid] <= u) t = mid;
+    else hi = mid - 1;
+  }
+  for (; u < units; u += stride) {
+    while (a.ustart[t + 1] <= u) ++t;
+    const unsigned b = u - a.ustart[t];  // block of this tensor
+    const unsigned long long e0 = (unsigned long long)b * kUnit;
+    const unsigned long long left = a.numel[t] - e0;
+    PT* pp = static_cast<PT*>(a.param[t]) + e0;
+    const GT* gp = static_cast<const GT*>(a.grad[t]) + e0;
+    uint16_t* cp = a.copy[t] ? a.copy[t] + e0 : nullptr;
+    const bool vec = a.vec_ok[t] && left >= kUnit;
+    const int len = left < kUnit ? (int)left : kUnit;
+    float p[8], g[8], m[8], v[8], root[8];
+    uint32_t mc[2], rc[2];
+    float ms = 0.0f, rs = 0.0f;
+    float* mp = static_cast<float*>(a.m[t]) + (S8 ? 0 : e0);
+    float* vp = static_cast<float*>(a.v[t]) + (S8 ? 0 : e0);
+    uint8_t* m8 = static_cast<uint8_t*>(a.m[t]) + e0;
+    uint8_t* r8 = static_cast<uint8_t*>(a.v[t]) + e0;
+    if (vec) {
+      const int o = lane * 8;
+      ld8(pp + o, p);
+      ld8(gp + o, g);
+      if constexpr (S8) {
+        ld8_codes(m8 + o, mc);
+        ld8_codes(r8 + o, rc);
+        ms = a.m_scale[t][b];
+        rs = a.v_scale[t][b];
+        widen_codes(mc, m);
+        widen_codes(rc, v);
+      } else {
+        ld8(mp + o, m);
+        ld8(vp + o, v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int o = i * 32 + lane;
+        const bool in = o < len;
+        p[i] = in ? widen_scalar(pp, o) : 0.0f;
+        g[i] = in ? widen_scalar(gp, o) : 0.0f;
+        if constexpr (S8) {
+          float none;
+          widen_e4m3x2(in ? (uint16_t)m8[o] : (uint16_t)0, m[i], none);
+          widen_e4m3x2(in ? (uint16_t)r8[o] : (uint16_t)0, v[i], none);
+        } else {
+          m[i] = in ? mp[o] : 0.0f;
+          v[i] = in ? vp[o] : 0.0f;
+        }
+      }
+      if constexpr (S8) {
+        ms = a.m_scale[t][b];
+        rs = a.v_scale[t][b];
+      }
+    }
+    if (h.coef != h.coef) return;  // the norm was not finite: nothing is changed
+    const float keep = (float)(1.0 - lr * a.decay[t]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (S8) {
+        m[i] = __fmul_rn(m[i], ms);
+        v[i] = __fmul_rn(v[i], rs);
+        v[i] = __fmul_rn(v[i], v[i]);
+      }
+      p[i] = adamw_one(p[i], g[i], m[i], v[i], root[i], keep, h);
+    }
+    if constexpr (S8) {
+      if (!vec) {  // lanes past the end take no part in the block's largest value
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 32 + lane >= len) m[i] = v[i] = root[i] = 0.0f;
+      }
+      const float mt = warp_max_abs(m), rt = warp_max_abs(root);
+      const float mf = code_factor(mt), rf = code_factor(rt);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m[i] = __fmul_rn(m[i], mf);
+        root[i] = __fmul_rn(root[i], rf);
+        if (v[i] > 0.0f && root[i] < kE4m3Min) root[i] = kE4m3Min;
+      }
+      if (lane == 0) {
+        a.m_scale[t][b] = __fmul_rn(mt, 1.0f / kE4m3Max);
+        a.v_scale[t][b] = __fmul_rn(rt, 1.0f / kE4m3Max);
+      }
+    }
+    if (vec) {
+      const int o = lane * 8;
+      st8(pp + o, p);
+      if (cp) store8_bf16(cp + o, p);
+      if constexpr (S8) {
+        pack_codes(m, mc);
+        pack_codes(root, rc);
+        st8_codes(m8 + o, mc);
+        st8_codes(r8 + o, rc);
+      } else {
+        st8(mp + o, m);
+        st8(vp + o, v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int o = i * 32 + lane;
+        if (o >= len) continue;
+        put(pp + o, p[i]);
+        if (cp) cp[o] = bf16_rn(p[i]);
+        if constexpr (S8) {
+          m8[o] = (uint8_t)e4m3x2(m[i], 0.0f);
+          r8[o] = (uint8_t)e4m3x2(root[i], 0.0f);
+        } else {
+          mp[o] = m[i];
+          vp[o] = v[i];
+        }
+      }
+    }
+  }
+}
+
+template <typename KernelT>
+int resident_blocks(KernelT kernel, const dph::DeviceInfo& dev) {
+  const int b = dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kThreads, 0, dev.device);
+  long long r = (long long)dev.sm_count * (b < 1 ? 1 : b);
+  const int limit = dph::stream_cta_limit();
+  if (limit > 0 && r > limit) r = limit;
+  return (int)r;
+}
+
+int blocks_for(unsigned units, int resident) {
+  const long long want = ((long long)units + kWarps - 1) / kWarps;
+  return (int)std::max(1LL, std::min<long long>(want, resident));
+}
+
+// ---- the global norm -----------------------------------------------------------
+
+template <int CAP>
+struct NormParams {
+  const void* grad[CAP];
+  unsigned long long numel[CAP];
+  unsigned ustart[CAP + 1];  // prefix sums of units (kNormUnit elements)
+  uint8_t vec_ok[CAP];
+  int n;
+  int slots;         // this launch's partial sums
+  int slots_before;  // earlier launches' of the same call
+  int last;          // 1: this launch forms the norm
+  float max_norm;
+  unsigned* ticket;
+  double* part;
+  float* norm;
+  float* coef;
+};
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Squares are summed in fp32 over a lane's 32 elements of a unit and in double
+// beyond.  Partial sum s covers the units of virtual CTA s (s, s + slots, ...
+// by warps), whatever CTA computes it, and the last CTA to finish adds the
+// partial sums in order: the result depends neither on the grid nor on the
+// order in which CTAs finish.
+template <typename GT, int CAP>
+__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ NormParams<CAP> a) {
+  __shared__ double sums[kWarps];
+  __shared__ bool is_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned units = a.ustart[a.n];
+  for (int s = blockIdx.x; s < a.slots; s += gridDim.x) {
+    unsigned u = (unsigned)s * kWarps + warp;
+    double sum = 0.0;
+    int t = 0;
+    for (int hi = a.n - 1; t < hi;) {
+      const int mid = (t + hi + 1) >> 1;
+      if (a.ustart[mid] <= u) t = mid;
+      else hi = mid - 1;
+    }
+    for (; u < units; u += (unsigned)a.slots * kWarps) {
+      while (a.ustart[t + 1] <= u) ++t;
+      const unsigned long long e0 = (unsigned long long)(u - a.ustart[t]) * kNormUnit;
+      const unsigned long long left = a.numel[t] - e0;
+      const GT* gp = static_cast<const GT*>(a.grad[t]) + e0;
+      float acc = 0.0f;
+      if (a.vec_ok[t] && left >= kNormUnit) {
+        float g[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ld8(gp + j * 256 + lane * 8, g[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc = __fadd_rn(acc, __fmul_rn(g[j][i], g[j][i]));
+      } else {
+        const int len = left < kNormUnit ? (int)left : kNormUnit;
+#pragma unroll 8
+        for (int i = 0; i < kNormUnit / 32; ++i) {
+          const int o = i * 32 + lane;
+          const float g = o < len ? widen_scalar(gp, o) : 0.0f;
+          acc = __fadd_rn(acc, __fmul_rn(g, g));
+        }
+      }
+      sum += (double)acc;
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double all = 0.0;
+      for (int w = 0; w < kWarps; ++w) all += sums[w];
+      a.part[a.slots_before + s] = all;
+    }
+    __syncthreads();
+  }
+  if (!a.last) return;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    is_last = atomicInc(a.ticket, gridDim.x - 1) == gridDim.x - 1;  // wraps to 0 for the next call
+  }
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  const int total = a.slots_before + a.slots;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < total; i += kThreads) sum += __ldcg(a.part + i);
+  sum = warp_sum(sum);
+  if (lane == 0) sums[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double all = 0.0;
+    for (int w = 0; w < kWarps; ++w) all += sums[w];
+    const float norm = (float)sqrt(all);
+    const float c = __fmul_rn(__frcp_rn(__fadd_rn(norm, 1e-6f)), a.max_norm);
+    if (a.norm) *a.norm = norm;
+    if (a.coef)
+      *a.coef = isfinite(norm) ? fminf(c, 1.0f) : __uint_as_float(0x7fffffffu);
+  }
+}
+
+size_t esize(dp_dtype_t t) { return t == DP_FP32 ? 4u : 2u; }
+bool dtype_ok(dp_dtype_t t) { return t == DP_FP32 || t == DP_BF16; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+struct Span {
+  uintptr_t lo, hi;
+  bool written;
+};
+
+// True if a written range overlaps any other range.
+bool spans_clash(std::vector<Span>& s) {
+  std::sort(s.begin(), s.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t end_any = 0, end_written = 0;
+  for (const Span& x : s) {
+    if (x.lo >= x.hi) continue;
+    if (x.lo < end_written || (x.written && x.lo < end_any)) return true;
+    end_any = std::max(end_any, x.hi);
+    if (x.written) end_written = std::max(end_written, x.hi);
+  }
+  return false;
+}
+
+constexpr int kNormCap = 768;      // tensors per norm launch: 19 KB of kernel parameters
+constexpr int kNormCapSmall = 32;
+
+template <typename GT, int CAP>
+cudaError_t norm_launch(const void* const* grads, const size_t* numels, const std::vector<int>& at,
+                        size_t first, size_t count, int slots_before, int* slots, bool last,
+                        float max_norm, unsigned* ticket, double* part, float* norm, float* coef,
+                        const dph::DeviceInfo& dev, cudaStream_t s) {
+  NormParams<CAP> p;
+  unsigned units = 0;
+  for (size_t i = 0; i < count; ++i) {
+    const int t = at[first + i];
+    p.grad[i] = grads[t];
+    p.numel[i] = numels[t];
+    p.vec_ok[i] = aligned(grads[t], sizeof(GT) * 8);
+    p.ustart[i] = units;
+    units += (unsigned)((numels[t] + kNormUnit - 1) / kNormUnit);
+  }
+  p.n = (int)count;
+  p.ustart[count] = units;
+  *slots = (int)std::min<unsigned>(kNormSlots, std::max(1u, (units + kWarps - 1) / kWarps));
+  p.slots = *slots;
+  p.slots_before = slots_before;
+  p.last = last;
+  p.max_norm = max_norm;
+  p.ticket = ticket;
+  p.part = part;
+  p.norm = norm;
+  p.coef = coef;
+  const int grid = std::min(*slots, resident_blocks(norm_kernel<GT, CAP>, dev));
+  norm_kernel<GT, CAP><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+constexpr size_t kNormHead = 256;  // the ticket, ahead of the partial sums
+
+}  // namespace
+
+// ---- the AdamW object ----------------------------------------------------------
+
+struct dp_adamw {
+  static constexpr int kCap = 384;      // tensors per launch (30 KB of kernel parameters)
+  static constexpr int kCapSmall = 32;  // short lists: less to pass with each launch
+  dp_dtype_t param_dtype, grad_dtype;
+  dp_state_t state;
+  std::vector<AdamwParams<kCap>> tables;
+  std::mutex mu;
+};
+
+namespace {
+
+template <typename PT, typename GT, bool S8>
+cudaError_t adamw_launch(const AdamwParams<dp_adamw::kCap>& table, const dph::DeviceInfo& dev,
+                         cudaStream_t s) {
+  const unsigned units = table.ustart[table.n];
+  if (table.n > dp_adamw::kCapSmall) {
+    auto k = adamw_kernel<PT, GT, S8, dp_adamw::kCap>;
+    k<<<blocks_for(units, resident_blocks(k, dev)), kThreads, 0, s>>>(table);
+    return cudaGetLastError();
+  }
+  AdamwParams<dp_adamw::kCapSmall> p;
+  const size_t n = (size_t)table.n;
+  memcpy(p.param, table.param, n * 8);
+  memcpy(p.grad, table.grad, n * 8);
+  memcpy(p.copy, table.copy, n * 8);
+  memcpy(p.m, table.m, n * 8);
+  memcpy(p.v, table.v, n * 8);
+  memcpy(p.m_scale, table.m_scale, n * 8);
+  memcpy(p.v_scale, table.v_scale, n * 8);
+  memcpy(p.numel, table.numel, n * 8);
+  memcpy(p.ustart, table.ustart, (n + 1) * 4);
+  memcpy(p.decay, table.decay, n * 8);
+  memcpy(p.vec_ok, table.vec_ok, n);
+  p.n = table.n;
+  p.lr = table.lr;
+  p.beta1 = table.beta1;
+  p.omb1 = table.omb1;
+  p.beta2 = table.beta2;
+  p.omb2 = table.omb2;
+  p.eps = table.eps;
+  p.step_size = table.step_size;
+  p.inv_root = table.inv_root;
+  p.grad_scale = table.grad_scale;
+  p.schedule = table.schedule;
+  auto k = adamw_kernel<PT, GT, S8, dp_adamw::kCapSmall>;
+  k<<<blocks_for(units, resident_blocks(k, dev)), kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename PT, typename GT>
+cudaError_t adamw_launch_s(const dp_adamw& o, const AdamwParams<dp_adamw::kCap>& table,
+                           const dph::DeviceInfo& dev, cudaStream_t s) {
+  return o.state == DP_STATE_8BIT ? adamw_launch<PT, GT, true>(table, dev, s)
+                                  : adamw_launch<PT, GT, false>(table, dev, s);
+}
+
+cudaError_t adamw_dispatch(const dp_adamw& o, const AdamwParams<dp_adamw::kCap>& table,
+                           const dph::DeviceInfo& dev, cudaStream_t s) {
+  if (o.param_dtype == DP_FP32)
+    return o.grad_dtype == DP_FP32 ? adamw_launch_s<float, float>(o, table, dev, s)
+                                   : adamw_launch_s<float, uint16_t>(o, table, dev, s);
+  return o.grad_dtype == DP_FP32 ? adamw_launch_s<uint16_t, float>(o, table, dev, s)
+                                 : adamw_launch_s<uint16_t, uint16_t>(o, table, dev, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes) {
+  if (!bytes) return DP_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (n < 0) return DP_ERR_INVALID_ARG;
+  const size_t launches = ((size_t)n + kNormCap - 1) / kNormCap;
+  *bytes = kNormHead + std::max<size_t>(1, launches) * kNormSlots * sizeof(double);
+  return DP_OK;
+}
+
+dp_status_t dp_grad_norm(const void* const* grads, const size_t* numels, int n,
+                         dp_dtype_t grad_dtype, float max_norm, float* norm, float* coef,
+                         void* workspace, size_t workspace_bytes, dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_grad_norm");
+  if (n < 0 || (n > 0 && (!grads || !numels)) || (!norm && !coef) || !workspace)
+    return DP_ERR_INVALID_ARG;
+  if (!(max_norm > 0.0f)) return DP_ERR_INVALID_ARG;
+  if (!dtype_ok(grad_dtype)) return DP_ERR_UNSUPPORTED;
+  size_t need = 0;
+  dp_grad_norm_workspace_size(n, &need);
+  if (workspace_bytes < need) return DP_ERR_INVALID_ARG;
+  const size_t es = esize(grad_dtype);
+  if (!aligned(workspace, 16) || (norm && !aligned(norm, 4)) || (coef && !aligned(coef, 4)))
+    return DP_ERR_UNSUPPORTED;
+  try {
+    std::vector<int> at;  // tensors with elements
+    std::vector<Span> spans;
+    unsigned long long units = 0;
+    at.reserve((size_t)n);
+    spans.reserve((size_t)n + 3);
+    for (int t = 0; t < n; ++t) {
+      if (numels[t] == 0) continue;
+      if (!grads[t]) return DP_ERR_INVALID_ARG;
+      units += (numels[t] - 1) / kNormUnit + 1;
+      if (!aligned(grads[t], es) || units > 0x7fffffffull) return DP_ERR_UNSUPPORTED;
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[t]);
+      spans.push_back({lo, lo + numels[t] * es, false});
+      at.push_back(t);
+    }
+    const auto out = [&](const void* p, size_t b) {
+      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+      if (p) spans.push_back({lo, lo + b, true});
+    };
+    out(norm, 4);
+    out(coef, 4);
+    out(workspace, need);
+    if (spans_clash(spans)) return DP_ERR_ALIAS;
+    dph::DeviceInfo dev;
+    if (!dph::current_device(&dev)) return DP_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    unsigned* ticket = static_cast<unsigned*>(workspace);
+    double* part = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kNormHead);
+    int slots_before = 0;
+    size_t first = 0;
+    do {  // one launch at least: an empty list has norm 0
+      const size_t count = std::min<size_t>(at.size() - first, kNormCap);
+      const bool last = first + count == at.size();
+      int slots = 0;
+      cudaError_t e;
+      const bool small = count <= kNormCapSmall;
+#define DP_NORM(GT, CAP)                                                                        \
+  norm_launch<GT, CAP>(grads, numels, at, first, count, slots_before, &slots, last, max_norm,   \
+                       ticket, part, norm, coef, dev, s)
+      if (grad_dtype == DP_FP32)
+        e = small ? DP_NORM(float, kNormCapSmall) : DP_NORM(float, kNormCap);
+      else
+        e = small ? DP_NORM(uint16_t, kNormCapSmall) : DP_NORM(uint16_t, kNormCap);
+#undef DP_NORM
+      if (e != cudaSuccess) return DP_ERR_CUDA;
+      slots_before += slots;
+      first += count;
+    } while (first < at.size());
+  } catch (const std::bad_alloc&) {
+    return DP_ERR_INVALID_ARG;
+  }
+  return DP_OK;
+}
+
+dp_status_t dp_adamw_create(const dp_adamw_tensor_t* tensors, int n, dp_dtype_t param_dtype,
+                            dp_dtype_t grad_dtype, dp_state_t state, dp_adamw_t** out) {
+  if (!out) return DP_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (n < 0 || (n > 0 && !tensors)) return DP_ERR_INVALID_ARG;
+  if (!dtype_ok(param_dtype) || !dtype_ok(grad_dtype)) return DP_ERR_UNSUPPORTED;
+  if (state != DP_STATE_FP32 && state != DP_STATE_8BIT) return DP_ERR_UNSUPPORTED;
+  const bool s8 = state == DP_STATE_8BIT;
+  const size_t ps = esize(param_dtype), gs = esize(grad_dtype), ss = s8 ? 1 : 4;
+  dp_adamw* o = nullptr;
+  try {
+    o = new dp_adamw;
+    o->param_dtype = param_dtype;
+    o->grad_dtype = grad_dtype;
+    o->state = state;
+    std::vector<Span> spans;
+    spans.reserve((size_t)n * 7);
+    dp_status_t bad = DP_OK;
+    unsigned long long units = 0;
+    for (int t = 0; t < n && bad == DP_OK; ++t) {
+      const dp_adamw_tensor_t& x = tensors[t];
+      if (x.numel == 0) continue;
+      if (!x.param || !x.grad || !x.exp_avg || !x.exp_avg_sq ||
+          (s8 && (!x.exp_avg_scale || !x.exp_avg_sq_scale)) || !(x.weight_decay >= 0.0f) ||
+          std::isinf(x.weight_decay)) {
+        bad = DP_ERR_INVALID_ARG;
+        break;
+      }
+      const unsigned long long u = (x.numel - 1) / kUnit + 1;
+      if (!aligned(x.param, ps) || !aligned(x.grad, gs) || !aligned(x.copy, 2) ||
+          !aligned(x.exp_avg, ss) || !aligned(x.exp_avg_sq, ss) ||
+          (s8 && (!aligned(x.exp_avg_scale, 4) || !aligned(x.exp_avg_sq_scale, 4))) ||
+          u > 0x7fffffffull) {
+        bad = DP_ERR_UNSUPPORTED;
+        break;
+      }
+      const auto span = [&](const void* p, size_t bytes, bool written) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (p) spans.push_back({lo, lo + bytes, written});
+      };
+      span(x.param, x.numel * ps, true);
+      span(x.grad, x.numel * gs, false);
+      span(x.copy, x.numel * 2, true);
+      span(x.exp_avg, x.numel * ss, true);
+      span(x.exp_avg_sq, x.numel * ss, true);
+      if (s8) {
+        span(x.exp_avg_scale, (size_t)u * 4, true);
+        span(x.exp_avg_sq_scale, (size_t)u * 4, true);
+      }
+      if (o->tables.empty() || o->tables.back().n == dp_adamw::kCap || units + u > 0x7fffffffull) {
+        o->tables.emplace_back();
+        memset(&o->tables.back(), 0, sizeof o->tables.back());
+        units = 0;
+      }
+      auto& p = o->tables.back();
+      const int i = p.n++;
+      p.param[i] = x.param;
+      p.grad[i] = x.grad;
+      p.copy[i] = static_cast<uint16_t*>(x.copy);
+      p.m[i] = x.exp_avg;
+      p.v[i] = x.exp_avg_sq;
+      p.m_scale[i] = s8 ? x.exp_avg_scale : nullptr;
+      p.v_scale[i] = s8 ? x.exp_avg_sq_scale : nullptr;
+      p.numel[i] = x.numel;
+      p.decay[i] = x.weight_decay;
+      // eight elements of every array from an address that one load or store takes
+      p.vec_ok[i] = aligned(x.param, ps * 8) && aligned(x.grad, gs * 8) && aligned(x.copy, 16) &&
+                    aligned(x.exp_avg, ss * 8) && aligned(x.exp_avg_sq, ss * 8);
+      units += u;
+      p.ustart[i + 1] = (unsigned)units;
+    }
+    if (bad == DP_OK && spans_clash(spans)) bad = DP_ERR_ALIAS;
+    if (bad != DP_OK) {
+      delete o;
+      return bad;
+    }
+  } catch (const std::bad_alloc&) {
+    delete o;
+    return DP_ERR_INVALID_ARG;
+  }
+  *out = o;
+  return DP_OK;
+}
+
+void dp_adamw_destroy(dp_adamw_t* o) { delete o; }
+
+dp_status_t dp_adamw_step(dp_adamw_t* o, double lr, double beta1, double beta2, double eps,
+                          long long step, const float* grad_scale, const float* schedule,
+                          dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_adamw_step");
+  if (!o || step < 1 || !std::isfinite(lr)) return DP_ERR_INVALID_ARG;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return DP_ERR_INVALID_ARG;
+  if (!((float)eps > 0.0f) || std::isinf((float)eps)) return DP_ERR_INVALID_ARG;
+  if (!aligned(grad_scale, 4) || !aligned(schedule, 4)) return DP_ERR_UNSUPPORTED;
+  if (o->tables.empty()) return DP_OK;
+  dph::DeviceInfo dev;
+  if (!dph::current_device(&dev)) return DP_ERR_CUDA;
+  const double fix1 = 1.0 - std::pow(beta1, (double)step);
+  const double fix2 = 1.0 - std::pow(beta2, (double)step);
+  std::lock_guard<std::mutex> lock(o->mu);
+  for (auto& table : o->tables) {
+    table.lr = lr;
+    table.beta1 = (float)beta1;
+    table.omb1 = (float)(1.0 - beta1);
+    table.beta2 = (float)beta2;
+    table.omb2 = (float)(1.0 - beta2);
+    table.eps = (float)eps;
+    table.step_size = (float)(lr / fix1);
+    table.inv_root = (float)(1.0 / std::sqrt(fix2));
+    table.grad_scale = grad_scale;
+    table.schedule = schedule;
+    if (adamw_dispatch(*o, table, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return DP_ERR_CUDA;
+  }
+  return DP_OK;
+}
+
+}  // extern "C"
