@@ -84,6 +84,9 @@ typedef enum {
 
 typedef enum { DP_FP32 = 0, DP_BF16 = 1 } dp_dtype_t;
 
+/* Microscaled 4-bit formats (see dp_mx4_quantize). */
+typedef enum { DP_MXFP4 = 0, DP_NVFP4 = 1 } dp_mx4_format_t;
+
 /* How an optimizer keeps its states. */
 typedef enum { DP_STATE_FP32 = 0, DP_STATE_8BIT = 1 } dp_state_t;
 
@@ -654,6 +657,77 @@ DP_API dp_status_t dp_adamw_step(dp_adamw_t* o, double lr, double beta1, double 
                                  long long step, const float* grad_scale, const float* schedule,
                                  dp_stream_t stream);
 DP_API void dp_adamw_destroy(dp_adamw_t* o);
+
+/*
+ * Microscaled 4-bit matrices: the form in which a parameter shard is gathered
+ * into the GEMM that uses it ("Sharding and Parallelism", section
+ * "Communication predictions": a collective's bytes follow the element type).
+ *
+ * A matrix [rows, cols], cols a multiple of 32, has
+ *   codes    rows x cols/2 bytes: e2m1 values (0 0.5 1 1.5 2 3 4 6, bit 3 the
+ *            sign), two to a byte, the earlier column in the low half
+ *   scales   one byte for each block of consecutive columns:
+ *              DP_MXFP4  blocks of 32, 2^(byte - 127), 255 is NaN
+ *              DP_NVFP4  blocks of 16, e4m3; values are also times the
+ *                        tensor's fp32 scale (tensor_scale NULL: 1)
+ *            in tiles of 128 rows x 4 blocks, 512 bytes each: row r, block b
+ *            of a tile at (r % 32) * 16 + (r / 32) * 4 + b; the tiles of 128
+ *            rows one after another along the columns; zero where the matrix
+ *            has no row or block.  dp_mx4_scales_size gives the bytes.
+ * Both device buffers are 16-byte aligned.
+ *
+ * dp_mx4_quantize: x is a HOST array of K device pointers to row shards
+ * [rows, cols] of x_dtype, rows ld elements apart.  The matrix quantised is
+ * their row concatenation [K*rows, cols], or with transpose != 0 its
+ * transpose [cols, K*rows] (blocks along the concatenated rows: the operand
+ * of the backward products, gathered and transposed in one pass).  The
+ * blocked dimension must be a multiple of 32.  In fp32, with a the largest
+ * magnitude of a block:
+ *   DP_MXFP4  scale 2^(floor(log2 a) - 2), at least 2^-127; values x / scale
+ *   DP_NVFP4  scale s = e4m3(a * (1/6) / t), t = *tensor_scale (or 1);
+ *             values x / (s * t)
+ * rounded to the nearest e2m1, ties to even, saturating at 6.  A block of
+ * zeros has codes 0 and scale byte 0; a block with a NaN or an infinity has
+ * codes 0 and a NaN scale, so that it is NaN when used.
+ *
+ * dp_mx4_tensor_scale: *scale = (largest magnitude of n tensors of numels[t]
+ * elements) / 2688, the t that takes the largest block's scale to 448 and its
+ * values to 6.  NaN or infinity if an element is.  workspace as for
+ * dp_grad_norm (dp_grad_norm_workspace_size(n) bytes, zeroed once).
+ *
+ * dp_mx4_dequantize: out [rows, cols] of out_dtype, the values rounded once.
+ *
+ * dp_allgather_matmul_mx4: dp_allgather_matmul with both operands in 4 bits:
+ *   y[m, f] = sum_d x[m, d] * w[f, d]
+ * x [M, D] and K weight shards [F_shard, D]; block-scaled tensor-core
+ * products accumulated in fp32, the tensors' scales applied to the sum, one
+ * rounding to y_dtype.  y: row-major [M, K*F_shard].  Requires D % 32 == 0,
+ * F_shard % 16 == 0, 16-byte aligned buffers; y overlaps no operand.  The
+ * summation order over d follows from the sizes; under a CTA limit the result
+ * is the same.  D == 0 writes zeros.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA;
+ * DP_ERR_TIMEOUT later from dp_get_device_error if a pipeline wait expired.
+ */
+typedef struct {
+  const void* codes;
+  const void* scales;
+  const float* tensor_scale;  /* device float or NULL; DP_NVFP4 only */
+} dp_mx4_t;
+DP_API dp_status_t dp_mx4_scales_size(int rows, int cols, dp_mx4_format_t format, size_t* bytes);
+DP_API dp_status_t dp_mx4_quantize(const void* const* x, int K, int rows, int cols, long long ld,
+                                   dp_dtype_t x_dtype, dp_mx4_format_t format, int transpose,
+                                   const float* tensor_scale, void* codes, void* scales,
+                                   dp_stream_t stream);
+DP_API dp_status_t dp_mx4_tensor_scale(const void* const* x, const size_t* numels, int n,
+                                       dp_dtype_t x_dtype, float* scale, void* workspace,
+                                       size_t workspace_bytes, dp_stream_t stream);
+DP_API dp_status_t dp_mx4_dequantize(const void* codes, const void* scales, int rows, int cols,
+                                     dp_mx4_format_t format, const float* tensor_scale, void* out,
+                                     dp_dtype_t out_dtype, dp_stream_t stream);
+DP_API dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D,
+                                           const dp_mx4_t* w_shards, int K, int F_shard,
+                                           dp_mx4_format_t format, void* y, dp_dtype_t y_dtype,
+                                           dp_stream_t stream);
 
 /*
  * The parameter all-gather on the GPU's copy engines instead of its SMs

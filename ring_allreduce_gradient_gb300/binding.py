@@ -17,6 +17,8 @@ DP_FP32 = 0
 DP_BF16 = 1
 DP_MAX_K = 16
 DP_MAX_MICROBATCHES = 16
+DP_MXFP4 = 0
+DP_NVFP4 = 1
 DP_STATE_FP32 = 0
 DP_STATE_8BIT = 1
 DP_STATE_BLOCK = 256  # elements that share one scale of an 8-bit state
@@ -42,6 +44,12 @@ class AdamwTensor(ctypes.Structure):
                 ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
                 ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
                 ("numel", ctypes.c_size_t), ("weight_decay", ctypes.c_double)]
+
+
+class Mx4(ctypes.Structure):
+    """dp_mx4_t"""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("tensor_scale", ctypes.c_void_p)]
 
 
 class DpError(RuntimeError):
@@ -109,6 +117,14 @@ def load() -> ctypes.CDLL:
             "dp_grad_norm": [pp, ctypes.POINTER(ctypes.c_size_t), i32, i32, f32, vp, vp, vp, sz,
                              vp],
             "dp_grad_norm_workspace_size": [i32, ctypes.POINTER(ctypes.c_size_t)],
+            "dp_mx4_scales_size": [i32, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+            "dp_mx4_quantize": [pp, i32, i32, i32, ctypes.c_longlong, i32, i32, i32, vp, vp, vp,
+                                vp],
+            "dp_mx4_tensor_scale": [pp, ctypes.POINTER(ctypes.c_size_t), i32, i32, vp, vp, sz,
+                                    vp],
+            "dp_mx4_dequantize": [vp, vp, i32, i32, i32, vp, vp, i32, vp],
+            "dp_allgather_matmul_mx4": [ctypes.POINTER(Mx4), i32, i32, ctypes.POINTER(Mx4), i32,
+                                        i32, i32, vp, i32, vp],
             "dp_adamw_create": [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32,
                                 ctypes.POINTER(ctypes.c_void_p)],
             "dp_adamw_step": [vp, ctypes.c_double, ctypes.c_double, ctypes.c_double,
@@ -520,6 +536,50 @@ def dp_adamw_step(h, lr, beta1, beta2, eps, step, grad_scale=None, schedule=None
 
 def dp_adamw_destroy(h) -> None:
     load().dp_adamw_destroy(h)
+
+
+def dp_mx4_scales_size(rows, cols, fmt) -> int:
+    b = ctypes.c_size_t(0)
+    _ret(load().dp_mx4_scales_size(rows, cols, fmt, ctypes.byref(b)), "dp_mx4_scales_size", True)
+    return int(b.value)
+
+
+def dp_mx4_quantize(x, K, rows, cols, ld, x_dtype, fmt, transpose, tensor_scale, codes, scales,
+                    stream=None, check=True) -> int:
+    st = load().dp_mx4_quantize(_parray(x), K, rows, cols, ld, dtype_code(x_dtype), fmt,
+                                1 if transpose else 0, _ptr(tensor_scale), _ptr(codes),
+                                _ptr(scales), _stream(stream))
+    return _ret(st, "dp_mx4_quantize", check)
+
+
+def dp_mx4_tensor_scale(x, numels, n, x_dtype, scale, workspace, workspace_bytes=None,
+                        stream=None, check=True) -> int:
+    wp, wb = _ws(workspace, workspace_bytes)
+    st = load().dp_mx4_tensor_scale(_parray(x), _sizes(numels), n, dtype_code(x_dtype),
+                                    _ptr(scale), wp, wb, _stream(stream))
+    return _ret(st, "dp_mx4_tensor_scale", check)
+
+
+def dp_mx4_dequantize(codes, scales, rows, cols, fmt, tensor_scale, out, out_dtype, stream=None,
+                      check=True) -> int:
+    st = load().dp_mx4_dequantize(_ptr(codes), _ptr(scales), rows, cols, fmt, _ptr(tensor_scale),
+                                  _ptr(out), dtype_code(out_dtype), _stream(stream))
+    return _ret(st, "dp_mx4_dequantize", check)
+
+
+def _mx4_array(items):
+    """``items``: (codes, scales, tensor_scale) triples, or a kept ctypes array."""
+    if isinstance(items, ctypes.Array):
+        return items
+    return (Mx4 * max(1, len(items)))(*[Mx4(*[_ptr(v) for v in t]) for t in items])
+
+
+def dp_allgather_matmul_mx4(x, M, D, w_shards, K, F_shard, fmt, y, y_dtype, stream=None,
+                            check=True) -> int:
+    """``x``: a (codes, scales, tensor_scale) triple; ``w_shards``: K of them."""
+    st = load().dp_allgather_matmul_mx4(_mx4_array([x]), M, D, _mx4_array(w_shards), K, F_shard,
+                                        fmt, _ptr(y), dtype_code(y_dtype), _stream(stream))
+    return _ret(st, "dp_allgather_matmul_mx4", check)
 
 
 def dp_all_gather_copy_engine(shards, K, shard_elems, dtype, out, stream=None,

@@ -45,8 +45,8 @@
 // drains what it issued (bounded) and frees TMEM before returning.
 
 #include "dp_launch.h"
+#include "dp_tc.cuh"
 
-#include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <atomic>
@@ -194,15 +194,6 @@ __device__ __forceinline__ Item cta_item(const AgmmParams& p, int w) {
 
 // ---- PTX wrappers ---------------------------------------------------------
 
-__device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* bar, void* dst,
-                                            int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // A 3-D box: (64 elements, rows, blocks of 64) -- the MN-major operand tiles
 // of kShardT, viewed as (64 features, T tokens, features / 64).
 __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst,
@@ -267,26 +258,7 @@ __device__ __forceinline__ bool epi_any(bool v) {
   return r != 0;
 }
 
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// Shared-memory matrix descriptor (tcgen05 format): K-major operand laid out
-// by TMA with the 128-byte swizzle; 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);  // bits 0-13: start address >> 4
-  d |= (uint64_t)1u << 16;                   // bits 16-29: leading byte offset (unused here)
-  d |= (uint64_t)(1024u >> 4) << 32;         // bits 32-45: stride byte offset >> 4
-  d |= (uint64_t)1u << 46;                   // bits 46-48: fixed 0b001
-  d |= (uint64_t)2u << 61;                   // bits 61-63: 128-byte swizzle
-  return d;
-}
-
-// The same for an MN-major operand (kShardT): TMA writes each 64-wide block
+// The shared-memory descriptor of an MN-major operand (kShardT): TMA writes each 64-wide block
 // of the M (or N) dimension as rows of 128 bytes, one row per k, 128-byte
 // swizzled, the blocks 8 KiB apart (64 rows of k per stage).  Fields: the
 // offset between those 64-wide blocks (bits 16-29) and between 8-row groups
@@ -318,26 +290,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-
-#define DP_TMEM_LD_X16(taddr, r)                                                              \
-  asm volatile(                                                                               \
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13," \
-      "%14,%15}, [%16];"                                                                      \
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),   \
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),            \
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])                                                 \
-      : "r"(taddr))
-
-__device__ __forceinline__ void tmem_ld_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 #define DP_TMEM_ST_X16(taddr, r)                                                              \
@@ -892,6 +844,33 @@ bool encode_mnmajor3_bf16(CUtensorMap* map, const void* base, int rows, int cols
     return r == CUDA_SUCCESS;
   });
 }
+
+}  // namespace
+
+namespace dpl {
+
+// A K-major operand of packed 4-bit values: row-major [rows, row_bytes] bytes,
+// box [box_rows, 128 bytes], 128-byte swizzle.  Needs row_bytes % 16 == 0.
+bool encode_kmajor_bytes(CUtensorMap* map, const void* base, int rows, int row_bytes,
+                         int box_rows) {
+  if (!get_encoder()) return false;
+  const MapKey key{reinterpret_cast<uintptr_t>(base), rows, row_bytes, box_rows, 5};
+  return cached_map(map, key, [&](CUtensorMap* m) {
+    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+  });
+}
+
+}  // namespace dpl
+
+namespace {
 
 // Tile width along F.  A tile must never straddle a shard boundary partially:
 // either it lies inside one shard (F_shard % BN == 0, one TMA box) or it is a

@@ -1,0 +1,598 @@
+// dp_mx4mm.cu -- the FSDP forward's parameter all-gather fused into the local
+// matmul, with both operands in microscaled 4-bit form:
+//   y[m, f] = tx * tw * sum_d sx[m, b(d)] x[m, d] * sw[f, b(d)] w[f, d]
+// x, w: e2m1 values; sx, sw: their blocks' scales (b(d) = d / 32 for mxfp4,
+// d / 16 for nvfp4); tx, tw: the tensors' fp32 scales (nvfp4).  The tensor
+// cores multiply the scaled values exactly and accumulate in fp32
+// (tcgen05.mma with block_scale, 64 values of d at a time); tx tw multiplies
+// the fp32 sum once.  The gathered w is never materialised.
+//
+// The product runs transposed, y^T = w x^T: the 128 TMEM lanes are weight
+// rows f and the columns are tokens.  So a tile always lies inside one shard,
+// whatever F_shard is, few tokens make a narrow tile instead of an idle one
+// (one token: 16 of the instruction's columns), and a warp's store covers 32
+// consecutive f of a token.
+//
+// One CTA (384 threads) per SM, persistent over tiles of 128 f x BN tokens:
+//   warp 0      W producer: 128 rows x 256 values (128 bytes) by TMA, and the
+//               rows' scales, a contiguous copy of the 512-byte scale tiles
+//   warp 2      X producer: BN rows x 256 values; also allocates TMEM
+//   warp 3      X scales' producer
+//   warp 1      MMA issuer: copies a stage's scales into TMEM (tcgen05.cp,
+//               each 512-byte tile to four columns, for all four groups of 32
+//               lanes), then four MMAs of 64 values; a stage has its own scale
+//               columns, so they are overwritten only when the stage is
+//   warps 4-11  epilogue: a warp takes 32 f and half of the tokens, reads its
+//               accumulator columns into registers at once, releases TMEM and
+//               then scales, packs and stores while the next tile runs
+// TMEM: 256 accumulator columns (one tile) and 4 x 48 scale columns.  With
+// the scales two accumulators of 256 columns do not fit.
+//
+// Few tiles: the blocks of d are split over a cluster of 2, 4 or 8 CTAs,
+// whose fp32 partial sums meet in shared memory: each CTA adds a share of the
+// tokens over the cluster in rank order (no atomics, no workspace).
+//
+// Every mbarrier wait is bounded; on expiry a role flags the error word and
+// unwinds, and the cluster's barriers are still reached by every thread.
+
+#include "dp_launch.h"
+#include "dp_mx4.cuh"
+#include "dp_tc.cuh"
+
+#include <algorithm>
+#include <cstring>
+
+namespace {
+
+using namespace dpk;
+
+constexpr int BM = 128;          // weight rows of a tile
+constexpr int BK = 256;          // values of d per stage: one 128-byte swizzle row
+constexpr int kStep = 64;        // values of d per MMA
+constexpr int kMaxBN = 256;      // tokens of a tile
+constexpr int kStages = 4;
+constexpr uint32_t kStageW = BM * BK / 2;
+constexpr uint32_t kStageX = kMaxBN * BK / 2;
+constexpr uint32_t kStageSW = 4 * kScaleTile;      // 128 rows x 16 blocks (nvfp4)
+constexpr uint32_t kStageSX = 2 * 4 * kScaleTile;  // 256 rows
+constexpr size_t kBarBytes = 256;
+constexpr size_t kSmemBytes =
+    1024 + (size_t)kStages * (kStageW + kStageX + kStageSW + kStageSX) + kBarBytes;
+constexpr int kTmemCols = 512;
+constexpr int kScaleCol0 = kMaxBN;   // first scale column
+constexpr int kScaleCols = 48;       // per stage: 16 for W, 32 for X
+constexpr int kThreadsM = 384;
+constexpr int kEpiWarps = 8;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kMaxSplit = 8;
+
+struct Mx4mmParams {
+  CUtensorMap tmX;
+  CUtensorMap tmW[kMaxK];
+  const uint8_t* sx;
+  const uint8_t* sw[kMaxK];
+  const float* tx;
+  const float* tw[kMaxK];
+  void* y;
+  unsigned* err;
+  int M, D, F, F_shard;
+  int BN;
+  int tiles_m, tiles_f;   // tiles_f: of one shard
+  int tile0, tiles;       // this launch's tiles
+  int num_kb;
+  int col_tiles;          // scale tiles along d
+  int x_row_tiles;
+  int split;              // CTAs of a cluster that share a tile
+  int y_f32;
+};
+
+// ---- PTX wrappers ------------------------------------------------------------
+
+__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src,
+                                          uint32_t bytes) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A scale tile in shared memory: 32 rows of 16 bytes, unswizzled, 8-row groups
+// 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);  // bits 0-13: start address >> 4
+  d |= (uint64_t)(128u >> 4) << 32;          // bits 32-45: stride byte offset >> 4
+  d |= (uint64_t)1u << 46;                   // bits 46-48: fixed 0b001
+  return d;                                  // bits 61-63: no swizzle
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(scale_desc(saddr))
+               : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: A and B e2m1, both
+// K-major; scales ue8m0 (mxfp4) or e4m3.
+__device__ __forceinline__ uint32_t idesc_fp4(bool mx, int n) {
+  return (1u << 7)                      // A format: e2m1
+         | (1u << 10)                   // B format: e2m1
+         | ((uint32_t)(n >> 3) << 17)   // N >> 3
+         | (mx ? 1u << 23 : 0u)         // scale format: ue8m0 / ue4m3
+         | ((uint32_t)(BM >> 7) << 27); // M >> 7
+}
+
+template <bool MX>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                        uint32_t accumulate) {
+  if constexpr (MX)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_constant__ Mx4mmParams p) {
+  constexpr int BLOCK = MX ? kMxBlock : kNvBlock;
+  constexpr int kTilesKb = BK / (4 * BLOCK);          // scale tiles of a stage along d
+  constexpr uint32_t kScaleKb = kTilesKb * kScaleTile;  // bytes, of 128 rows
+  extern __shared__ unsigned char smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sW = smem;
+  uint8_t* sX = sW + kStages * kStageW;
+  uint8_t* sSW = sX + kStages * kStageX;
+  uint8_t* sSX = sSW + kStages * kStageSW;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sSX + kStages * kStageSX);
+  uint64_t* empty = full + kStages;
+  uint64_t* tmem_full = empty + kStages;
+  uint64_t* tmem_empty = tmem_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_empty + 1);
+  volatile int* aborted = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
+  const int first = p.split > 1 ? (int)blockIdx.x / p.split : (int)blockIdx.x;
+  const int stride = p.split > 1 ? p.tiles : (int)gridDim.x;  // a cluster runs one tile
+  const int kb_lo = (int)rank * p.num_kb / p.split;
+  const int kb_hi = ((int)rank + 1) * p.num_kb / p.split;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 3);  // three producers
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tmem_full, 1);
+    mbar_init(tmem_empty, kEpiWarps);
+    *aborted = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+            smem_u32(tmem_slot)),
+        "r"(kTmemCols)
+        : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------ producers ---------------------------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t armed_phase[kStages];
+      bool armed[kStages];
+      for (int s = 0; s < kStages; ++s) armed[s] = false;
+      for (int i = first; i < p.tiles && !*aborted; i += stride) {
+        const int tile = p.tile0 + i;
+        const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
+        const int shard = ft / p.tiles_f, f0 = (ft - shard * p.tiles_f) * BM;
+        const int m0 = mt * p.BN;
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs)) {
+            *aborted = 1;
+            break;
+          }
+          const int t0 = kb * kTilesKb;
+          const uint32_t sbytes =
+              (uint32_t)min(kTilesKb, p.col_tiles - t0) * kScaleTile;  // the last stage may end early
+          if (warp == 0) {
+            mbar_arrive_expect_tx(&full[stage], kStageW + sbytes);
+            tma_load_2d(&p.tmW[shard], &full[stage], sW + stage * kStageW, kb * (BK / 2), f0);
+            bulk_load(&full[stage], sSW + stage * kStageSW,
+                      p.sw[shard] + ((size_t)(f0 / kScaleRows) * p.col_tiles + t0) * kScaleTile,
+                      sbytes);
+          } else if (warp == 2) {
+            mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * (BK / 2));
+            tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), m0);
+          } else {
+            const int r0 = m0 / kScaleRows;
+            const int rows = min((p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
+            mbar_arrive_expect_tx(&full[stage], sbytes * (uint32_t)rows);
+            for (int r = 0; r < rows; ++r)
+              bulk_load(&full[stage], sSX + stage * kStageSX + r * kScaleKb,
+                        p.sx + ((size_t)(r0 + r) * p.col_tiles + t0) * kScaleTile, sbytes);
+          }
+          armed[stage] = true;
+          armed_phase[stage] = phase;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Drain: every load this thread issued has landed before the CTA exits.
+      for (int s = 0; s < kStages; ++s)
+        if (armed[s]) (void)mbar_wait_bounded(&full[s], armed_phase[s], p.err, kTimeoutNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer --------------------------------
+    if (lane == 0) {
+      const uint32_t idesc = idesc_fp4(MX, p.BN);
+      int stage = 0, w = 0;
+      uint32_t phase = 0;
+      bool issued = false;
+      for (int i = first; i < p.tiles && !*aborted; i += stride, ++w) {
+        if (!mbar_wait_bounded(tmem_empty, ((uint32_t)w & 1u) ^ 1u, p.err, kTimeoutNs)) {
+          *aborted = 1;
+          break;
+        }
+        tc_fence_after();
+        const int x_tiles = min((p.BN + kScaleRows - 1) / kScaleRows,
+                                p.x_row_tiles - (p.tile0 + i) % p.tiles_m * p.BN / kScaleRows);
+        bool ok = true;
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
+          if (!mbar_wait_bounded(&full[stage], phase, p.err, kTimeoutNs)) {
+            *aborted = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int steps = min(BK / kStep, (p.D - kb * BK + kStep - 1) / kStep);
+          const int stiles = min(kTilesKb, p.col_tiles - kb * kTilesKb);
+          const uint32_t tw = tmem_base + (uint32_t)(kScaleCol0 + stage * kScaleCols);
+          const uint32_t tx = tw + 16u;
+          const uint32_t aw = smem_u32(sSW + stage * kStageSW), ax = smem_u32(sSX + stage * kStageSX);
+          for (int t = 0; t < stiles; ++t) {
+            copy_scales(tw + 4u * t, aw + (uint32_t)t * kScaleTile);
+            for (int r = 0; r < x_tiles; ++r)
+              copy_scales(tx + 8u * t + 4u * r, ax + r * kScaleKb + (uint32_t)t * kScaleTile);
+          }
+          const uint32_t a0 = smem_u32(sW + stage * kStageW), b0 = smem_u32(sX + stage * kStageX);
+#pragma unroll
+          for (int k = 0; k < BK / kStep; ++k) {
+            if (k < steps) {
+              // nvfp4: a step's four scales are a tile's; mxfp4: its two are
+              // half of a tile's, chosen by the scale ids of the descriptor
+              const int t = MX ? k / 2 : k;
+              const uint32_t id = MX ? (uint32_t)(k & 1) * 2u : 0u;
+              mma_fp4<MX>(tmem_base, sw128_kmajor_desc(a0 + 32u * k), sw128_kmajor_desc(b0 + 32u * k),
+                          idesc | (id << 4) | (id << 29), tw + 4u * t, tx + 8u * t,
+                          (kb > kb_lo || k > 0) ? 1u : 0u);
+            }
+          }
+          mma_commit(&empty[stage]);
+          issued = true;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit(tmem_full);
+      }
+      // Drain: every MMA issued has completed before TMEM is freed.
+      if (issued) {
+        const int last = stage == 0 ? kStages - 1 : stage - 1;
+        const uint32_t last_phase = stage == 0 ? phase ^ 1u : phase;
+        (void)mbar_wait_bounded(&empty[last], last_phase, p.err, kTimeoutNs);
+      }
+    }
+  } else {
+    // ------------------------------ epilogue ----------------------------------
+    const int quarter = warp & 3;          // the TMEM lanes this warp may read
+    const int half = (warp - 4) >> 2;
+    const int chunks = p.BN / 16;
+    const int c0 = half ? (chunks + 1) / 2 : 0;
+    const int cn = half ? chunks / 2 : (chunks + 1) / 2;  // chunks of 16 tokens, at most 8
+    const int fl = quarter * 32 + lane;
+    int w = 0;
+    for (int i = first; i < p.tiles; i += stride, ++w) {
+      const int tile = p.tile0 + i;
+      const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
+      const int shard = ft / p.tiles_f, f0 = (ft - shard * p.tiles_f) * BM;
+      const int m0 = mt * p.BN;
+      float alpha = 1.0f;
+      if constexpr (!MX) {
+        if (p.tx) alpha = __ldg(p.tx);
+        if (p.tw[shard]) alpha = __fmul_rn(alpha, __ldg(p.tw[shard]));
+      }
+      const bool ok = mbar_wait_bounded(tmem_full, (uint32_t)w & 1u, p.err, kTimeoutNs);
+      if (!__all_sync(0xffffffffu, ok)) {  // the warp's lanes leave together
+        *aborted = 1;
+        break;
+      }
+      tc_fence_after();
+      uint32_t r[8][16];
+      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c0 * 16);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < cn) DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16), r[c]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tmem_empty);
+      if (p.split > 1) {
+        // the partial sums, [token][128 f], where the operands were: every
+        // MMA of this tile, the CTA's only one, has completed
+        float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < cn) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              red[((c0 + c) * 16 + q) * BM + fl] = __uint_as_float(r[c][q]);
+          }
+        continue;
+      }
+      const int f = f0 + fl;                       // inside the shard
+      const size_t yf = (size_t)shard * p.F_shard + f;
+      const bool f_in = f < p.F_shard;
+      if (p.y_f32) {
+        float* y = static_cast<float*>(p.y) + yf;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < cn) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const int m = m0 + (c0 + c) * 16 + q;
+              if (f_in && m < p.M) y[(size_t)m * p.F] = __fmul_rn(__uint_as_float(r[c][q]), alpha);
+            }
+          }
+      } else {
+        // neighbouring lanes trade values of two tokens, so that each lane
+        // stores two f of one token (F_shard is even)
+        uint16_t* y = static_cast<uint16_t*>(p.y) + (yf & ~(size_t)1);
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c < cn) {
+#pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+              const float a = __fmul_rn(__uint_as_float(r[c][q]), alpha);
+              const float b = __fmul_rn(__uint_as_float(r[c][q + 1]), alpha);
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+              const int m = m0 + (c0 + c) * 16 + q + (odd ? 1 : 0);
+              if (f_in && m < p.M)
+                *reinterpret_cast<uint32_t*>(y + (size_t)m * p.F) =
+                    odd ? pack_bf16x2_rn(got, b) : pack_bf16x2_rn(a, got);
+            }
+          }
+      }
+    }
+  }
+
+  __syncwarp();
+  if (p.split > 1) {
+    __syncthreads();
+    cluster_barrier();  // every CTA's partial sums are in its shared memory
+    const int tile = p.tile0 + first;
+    const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
+    const int shard = ft / p.tiles_f, f0 = (ft - shard * p.tiles_f) * BM;
+    const int m0 = mt * p.BN;
+    float alpha = 1.0f;
+    if constexpr (!MX) {
+      if (p.tx) alpha = __ldg(p.tx);
+      if (p.tw[shard]) alpha = __fmul_rn(alpha, __ldg(p.tw[shard]));
+    }
+    const int tokens = min(p.BN, p.M - m0);
+    const int share = (tokens + p.split - 1) / p.split;
+    const int lo = (int)rank * share, hi = min(tokens, lo + share);
+    const uint32_t red = smem_u32(smem);
+    for (int i = threadIdx.x; i < (hi - lo) * (BM / 2); i += kThreadsM) {
+      const int f = f0 + (i & (BM / 2 - 1)) * 2, m = lo + i / (BM / 2);
+      const uint32_t at = red + (uint32_t)(m * BM + (f - f0)) * 4u;
+      float2 sum = ld_peer2(peer_addr(at, 0));
+      for (int c = 1; c < p.split; ++c) {
+        const float2 v = ld_peer2(peer_addr(at, (uint32_t)c));
+        sum.x = __fadd_rn(sum.x, v.x);
+        sum.y = __fadd_rn(sum.y, v.y);
+      }
+      if (f < p.F_shard) {
+        const size_t o = (size_t)(m0 + m) * p.F + (size_t)shard * p.F_shard + f;
+        sum.x = __fmul_rn(sum.x, alpha);
+        sum.y = __fmul_rn(sum.y, alpha);
+        if (p.y_f32)
+          *reinterpret_cast<float2*>(static_cast<float*>(p.y) + o) = sum;
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + o) =
+              pack_bf16x2_rn(sum.x, sum.y);
+      }
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+template <bool MX>
+cudaError_t launch_mx4mm(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, cudaStream_t s) {
+  auto kernel = mx4mm_kernel<MX>;
+  if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kThreadsM, kSmemBytes,
+                          dev.device) < 1)
+    return cudaErrorInvalidConfiguration;
+  const int limit = dph::gemm_cta_limit();
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreadsM);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  if (p.split == 1) {
+    int grid = std::min(tiles, dev.sm_count);
+    if (limit > 0) grid = std::min(grid, limit);
+    p.tile0 = 0;
+    p.tiles = tiles;
+    cfg.gridDim = dim3((unsigned)grid);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)p.split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  // under a CTA limit the clusters go in several launches (one cluster each at least)
+  const int per = limit > 0 ? std::max(1, std::min(tiles, limit / p.split)) : tiles;
+  for (int t = 0; t < tiles; t += per) {
+    p.tile0 = t;
+    p.tiles = std::min(per, tiles - t);
+    cfg.gridDim = dim3((unsigned)(p.tiles * p.split));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span_of(const void* p, size_t n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Span{a, a + n};
+}
+bool clash(const Span& a, const Span& b) {
+  return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
+}
+
+}  // namespace
+
+extern "C" dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D,
+                                               const dp_mx4_t* w_shards, int K, int F_shard,
+                                               dp_mx4_format_t format, void* y,
+                                               dp_dtype_t y_dtype, dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_allgather_matmul_mx4");
+  if (!x || !w_shards || K < 1 || K > DP_MAX_K) return DP_ERR_INVALID_ARG;
+  if (M < 0 || D < 0 || F_shard < 0) return DP_ERR_INVALID_ARG;
+  if (format != DP_MXFP4 && format != DP_NVFP4) return DP_ERR_UNSUPPORTED;
+  if (y_dtype != DP_FP32 && y_dtype != DP_BF16) return DP_ERR_UNSUPPORTED;
+  if (D % 32 || F_shard % 16) return DP_ERR_UNSUPPORTED;
+  if ((long long)K * F_shard > 0x7fffff00ll || M > 0x7fffff00 || D > 0x7fffff00)
+    return DP_ERR_UNSUPPORTED;
+  if (!aligned(y, 16)) return DP_ERR_UNSUPPORTED;
+  const bool mx = format == DP_MXFP4;
+  const int F = K * F_shard, block = mx4_block(format);
+  const size_t ysz = (size_t)M * F * (y_dtype == DP_FP32 ? 4 : 2);
+  if (!y && ysz) return DP_ERR_INVALID_ARG;
+  const Span out = span_of(y, ysz);
+  const auto check = [&](const dp_mx4_t& a, int rows) -> dp_status_t {
+    if (mx && a.tensor_scale) return DP_ERR_INVALID_ARG;
+    if ((!a.codes || !a.scales) && rows && D) return DP_ERR_INVALID_ARG;
+    if (!aligned(a.codes, 16) || !aligned(a.scales, 16) || !aligned(a.tensor_scale, 4))
+      return DP_ERR_UNSUPPORTED;
+    size_t sbytes = 0;
+    dp_mx4_scales_size(rows, D, format, &sbytes);
+    if (clash(out, span_of(a.codes, (size_t)rows * (D / 2))) ||
+        clash(out, span_of(a.scales, sbytes)) ||
+        (a.tensor_scale && clash(out, span_of(a.tensor_scale, 4))))
+      return DP_ERR_ALIAS;
+    return DP_OK;
+  };
+  dp_status_t st = check(*x, M);
+  for (int k = 0; k < K && st == DP_OK; ++k) st = check(w_shards[k], F_shard);
+  if (st != DP_OK) return st;
+  if (M == 0 || F == 0) return DP_OK;
+  dph::DeviceInfo dev;
+  if (!dph::current_device(&dev)) return DP_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (D == 0) return cudaMemsetAsync(y, 0, ysz, s) == cudaSuccess ? DP_OK : DP_ERR_CUDA;
+  if (dev.cc_major != 10 || dev.cc_minor != 3 || dev.smem_optin < kSmemBytes)
+    return DP_ERR_UNSUPPORTED;
+
+  Mx4mmParams p;
+  memset(&p, 0, sizeof p);
+  p.M = M;
+  p.D = D;
+  p.F = F;
+  p.F_shard = F_shard;
+  p.tiles_f = (F_shard + BM - 1) / BM;
+  const int all_f = K * p.tiles_f;
+  // Tokens of a tile: up to 128 the call's own, rounded up to the
+  // instruction's 16; beyond, 256 where that still gives every SM a tile, else
+  // 128 (a tile starts on a 128-row scale tile).
+  p.BN = M <= 128 ? (M + 15) / 16 * 16
+                  : ((long long)all_f * ((M + 255) / 256) >= dev.sm_count ? 256 : 128);
+  p.tiles_m = (M + p.BN - 1) / p.BN;
+  p.num_kb = (D + BK - 1) / BK;
+  p.col_tiles = mx4_col_tiles(D, block);
+  p.x_row_tiles = (M + kScaleRows - 1) / kScaleRows;
+  if ((long long)all_f * p.tiles_m > 0x3fffffffll) return DP_ERR_UNSUPPORTED;
+  const int tiles = all_f * p.tiles_m;
+  // CTAs of a cluster that share a tile's blocks of d: as many as keep the
+  // launch on the SMs and leave each a block.
+  p.split = 1;
+  while (p.split < kMaxSplit && tiles * p.split * 2 <= dev.sm_count && p.num_kb >= p.split * 2)
+    p.split *= 2;
+  p.sx = static_cast<const uint8_t*>(x->scales);
+  p.tx = x->tensor_scale;
+  p.y = y;
+  p.y_f32 = y_dtype == DP_FP32;
+  p.err = dev.err_word;
+  if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, D / 2, p.BN)) return DP_ERR_UNSUPPORTED;
+  for (int k = 0; k < K; ++k) {
+    if (!dpl::encode_kmajor_bytes(&p.tmW[k], w_shards[k].codes, F_shard, D / 2, BM))
+      return DP_ERR_UNSUPPORTED;
+    p.sw[k] = static_cast<const uint8_t*>(w_shards[k].scales);
+    p.tw[k] = w_shards[k].tensor_scale;
+  }
+  const cudaError_t e = mx ? launch_mx4mm<true>(p, tiles, dev, s)
+                           : launch_mx4mm<false>(p, tiles, dev, s);
+  return e == cudaSuccess ? DP_OK : DP_ERR_CUDA;
+}

@@ -45,6 +45,7 @@ constexpr int kUnit = 256;         // elements a warp takes at once = an 8-bit b
 constexpr int kNormUnit = 1024;    // the norm's: four loads in flight per lane
 constexpr int kNormSlots = 608;    // partial sums of one norm launch: four CTAs on each of 152 SMs
 constexpr float kE4m3Max = 448.0f;
+constexpr float kTopFp4 = 1.0f / 2688.0f;     // e2m1's largest value (6) times e4m3's
 constexpr float kE4m3Min = 0.001953125f;      // 2^-9, the smallest e4m3 value above zero
 constexpr float kTiny = 7.703719777548943e-34f;  // 2^-110: below it a block's reciprocal is left out
 
@@ -327,12 +328,31 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
+// What is gathered over a list: the sum of squares, or the largest magnitude
+// (kept as its bit pattern, which orders as the magnitude does with NaN above
+// all, and is exact in fp32's and double's place alike).
+enum { kSumSquares = 0, kMaxAbs = 1 };
+
+__device__ __forceinline__ double warp_max(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_down_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int OP>
+__device__ __forceinline__ double joined(double a, double b) {
+  return OP == kSumSquares ? a + b : fmax(a, b);
+}
+template <int OP>
+__device__ __forceinline__ double warp_joined(double v) {
+  return OP == kSumSquares ? warp_sum(v) : warp_max(v);
+}
+
 // Squares are summed in fp32 over a lane's 32 elements of a unit and in double
 // beyond.  Partial sum s covers the units of virtual CTA s (s, s + slots, ...
 // by warps), whatever CTA computes it, and the last CTA to finish adds the
 // partial sums in order: the result depends neither on the grid nor on the
 // order in which CTAs finish.
-template <typename GT, int CAP>
+template <typename GT, int OP, int CAP>
 __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ NormParams<CAP> a) {
   __shared__ double sums[kWarps];
   __shared__ bool is_last;
@@ -353,6 +373,13 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
       const unsigned long long left = a.numel[t] - e0;
       const GT* gp = static_cast<const GT*>(a.grad[t]) + e0;
       float acc = 0.0f;
+      uint32_t top = 0;
+      const auto take = [&](float g) {
+        if constexpr (OP == kSumSquares)
+          acc = __fadd_rn(acc, __fmul_rn(g, g));
+        else
+          top = max(top, __float_as_uint(g) & 0x7fffffffu);
+      };
       if (a.vec_ok[t] && left >= kNormUnit) {
         float g[4][8];
 #pragma unroll
@@ -360,24 +387,23 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc = __fadd_rn(acc, __fmul_rn(g[j][i], g[j][i]));
+          for (int i = 0; i < 8; ++i) take(g[j][i]);
       } else {
         const int len = left < kNormUnit ? (int)left : kNormUnit;
 #pragma unroll 8
         for (int i = 0; i < kNormUnit / 32; ++i) {
           const int o = i * 32 + lane;
-          const float g = o < len ? widen_scalar(gp, o) : 0.0f;
-          acc = __fadd_rn(acc, __fmul_rn(g, g));
+          take(o < len ? widen_scalar(gp, o) : 0.0f);
         }
       }
-      sum += (double)acc;
+      sum = joined<OP>(sum, OP == kSumSquares ? (double)acc : (double)top);
     }
-    sum = warp_sum(sum);
+    sum = warp_joined<OP>(sum);
     if (lane == 0) sums[warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
       double all = 0.0;
-      for (int w = 0; w < kWarps; ++w) all += sums[w];
+      for (int w = 0; w < kWarps; ++w) all = joined<OP>(all, sums[w]);
       a.part[a.slots_before + s] = all;
     }
     __syncthreads();
@@ -392,13 +418,17 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
   __threadfence();
   const int total = a.slots_before + a.slots;
   double sum = 0.0;
-  for (int i = threadIdx.x; i < total; i += kThreads) sum += __ldcg(a.part + i);
-  sum = warp_sum(sum);
+  for (int i = threadIdx.x; i < total; i += kThreads) sum = joined<OP>(sum, __ldcg(a.part + i));
+  sum = warp_joined<OP>(sum);
   if (lane == 0) sums[warp] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     double all = 0.0;
-    for (int w = 0; w < kWarps; ++w) all += sums[w];
+    for (int w = 0; w < kWarps; ++w) all = joined<OP>(all, sums[w]);
+    if constexpr (OP == kMaxAbs) {
+      *a.norm = __fmul_rn(__uint_as_float((uint32_t)all), kTopFp4);
+      return;
+    }
     const float norm = (float)sqrt(all);
     const float c = __fmul_rn(__frcp_rn(__fadd_rn(norm, 1e-6f)), a.max_norm);
     if (a.norm) *a.norm = norm;
@@ -432,7 +462,7 @@ bool spans_clash(std::vector<Span>& s) {
 constexpr int kNormCap = 768;      // tensors per norm launch: 19 KB of kernel parameters
 constexpr int kNormCapSmall = 32;
 
-template <typename GT, int CAP>
+template <typename GT, int OP, int CAP>
 cudaError_t norm_launch(const void* const* grads, const size_t* numels, const std::vector<int>& at,
                         size_t first, size_t count, int slots_before, int* slots, bool last,
                         float max_norm, unsigned* ticket, double* part, float* norm, float* coef,
@@ -458,8 +488,8 @@ cudaError_t norm_launch(const void* const* grads, const size_t* numels, const st
   p.part = part;
   p.norm = norm;
   p.coef = coef;
-  const int grid = std::min(*slots, resident_blocks(norm_kernel<GT, CAP>, dev));
-  norm_kernel<GT, CAP><<<grid, kThreads, 0, s>>>(p);
+  const int grid = std::min(*slots, resident_blocks(norm_kernel<GT, OP, CAP>, dev));
+  norm_kernel<GT, OP, CAP><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -534,26 +564,12 @@ cudaError_t adamw_dispatch(const dp_adamw& o, const AdamwParams<dp_adamw::kCap>&
                                  : adamw_launch_s<uint16_t, uint16_t>(o, table, dev, s);
 }
 
-}  // namespace
-
-extern "C" {
-
-dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes) {
-  if (!bytes) return DP_ERR_INVALID_ARG;
-  *bytes = 0;
-  if (n < 0) return DP_ERR_INVALID_ARG;
-  const size_t launches = ((size_t)n + kNormCap - 1) / kNormCap;
-  *bytes = kNormHead + std::max<size_t>(1, launches) * kNormSlots * sizeof(double);
-  return DP_OK;
-}
-
-dp_status_t dp_grad_norm(const void* const* grads, const size_t* numels, int n,
-                         dp_dtype_t grad_dtype, float max_norm, float* norm, float* coef,
-                         void* workspace, size_t workspace_bytes, dp_stream_t stream) {
-  dph::NvtxRange nvtx_range("dp_grad_norm");
-  if (n < 0 || (n > 0 && (!grads || !numels)) || (!norm && !coef) || !workspace)
-    return DP_ERR_INVALID_ARG;
-  if (!(max_norm > 0.0f)) return DP_ERR_INVALID_ARG;
+// One pass over a list: the checks, and as many launches as the list needs.
+template <int OP>
+dp_status_t gather_list(const void* const* grads, const size_t* numels, int n,
+                        dp_dtype_t grad_dtype, float max_norm, float* norm, float* coef,
+                        void* workspace, size_t workspace_bytes, cudaStream_t s) {
+  if (n < 0 || (n > 0 && (!grads || !numels)) || !workspace) return DP_ERR_INVALID_ARG;
   if (!dtype_ok(grad_dtype)) return DP_ERR_UNSUPPORTED;
   size_t need = 0;
   dp_grad_norm_workspace_size(n, &need);
@@ -586,7 +602,6 @@ dp_status_t dp_grad_norm(const void* const* grads, const size_t* numels, int n,
     if (spans_clash(spans)) return DP_ERR_ALIAS;
     dph::DeviceInfo dev;
     if (!dph::current_device(&dev)) return DP_ERR_CUDA;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     unsigned* ticket = static_cast<unsigned*>(workspace);
     double* part = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + kNormHead);
     int slots_before = 0;
@@ -598,7 +613,7 @@ dp_status_t dp_grad_norm(const void* const* grads, const size_t* numels, int n,
       cudaError_t e;
       const bool small = count <= kNormCapSmall;
 #define DP_NORM(GT, CAP)                                                                        \
-  norm_launch<GT, CAP>(grads, numels, at, first, count, slots_before, &slots, last, max_norm,   \
+  norm_launch<GT, OP, CAP>(grads, numels, at, first, count, slots_before, &slots, last, max_norm,   \
                        ticket, part, norm, coef, dev, s)
       if (grad_dtype == DP_FP32)
         e = small ? DP_NORM(float, kNormCapSmall) : DP_NORM(float, kNormCap);
@@ -613,6 +628,37 @@ dp_status_t dp_grad_norm(const void* const* grads, const size_t* numels, int n,
     return DP_ERR_INVALID_ARG;
   }
   return DP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes) {
+  if (!bytes) return DP_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (n < 0) return DP_ERR_INVALID_ARG;
+  const size_t launches = ((size_t)n + kNormCap - 1) / kNormCap;
+  *bytes = kNormHead + std::max<size_t>(1, launches) * kNormSlots * sizeof(double);
+  return DP_OK;
+}
+
+dp_status_t dp_grad_norm(const void* const* grads, const size_t* numels, int n,
+                         dp_dtype_t grad_dtype, float max_norm, float* norm, float* coef,
+                         void* workspace, size_t workspace_bytes, dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_grad_norm");
+  if ((!norm && !coef) || !(max_norm > 0.0f)) return DP_ERR_INVALID_ARG;
+  return gather_list<kSumSquares>(grads, numels, n, grad_dtype, max_norm, norm, coef, workspace,
+                                  workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dp_status_t dp_mx4_tensor_scale(const void* const* x, const size_t* numels, int n,
+                                dp_dtype_t x_dtype, float* scale, void* workspace,
+                                size_t workspace_bytes, dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_mx4_tensor_scale");
+  if (!scale) return DP_ERR_INVALID_ARG;
+  return gather_list<kMaxAbs>(x, numels, n, x_dtype, 1.0f, scale, nullptr, workspace,
+                              workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 dp_status_t dp_adamw_create(const dp_adamw_tensor_t* tensors, int n, dp_dtype_t param_dtype,
