@@ -292,19 +292,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
-#define DP_TMEM_ST_X16(taddr, r)                                                              \
-  asm volatile(                                                                               \
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"  \
-      "%13,%14,%15,%16};" ::"r"(taddr),                                                       \
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),  \
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),        \
-      "r"(r[15])                                                                              \
-      : "memory")
-
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
 // Partial accumulators go through L2 only (.cg): another SM wrote them.
 __device__ __forceinline__ uint4 ld_cg_v4(const void* ptr) {
   uint4 v;

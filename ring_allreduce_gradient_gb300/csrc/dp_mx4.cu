@@ -14,12 +14,14 @@
 // an infinity has a NaN scale.
 //
 // Bound by memory: 2 bytes read and 0.53 / 0.56 written for each bf16 value.
-// Rows form: a warp takes 256 columns of a row, a lane eight of them, so a
-// block is 2 or 4 neighbouring lanes.  Transposed form: blocks run down the
-// columns, so a lane takes two neighbouring columns and reads 64 rows of
-// them (a warp reads 128 contiguous bytes of each bf16 row): a block's
-// largest value needs no exchange, and a lane ends with 32 contiguous bytes
-// of each of its two output rows.  Neither goes through shared memory.
+// Rows form: a warp takes up to 1024 columns of a row with all its loads
+// issued first, a lane eight columns of each 256, so a block is 2 or 4
+// neighbouring lanes.  Transposed form: blocks run down the columns, so a lane
+// takes two neighbouring columns and reads 64 rows of them (a warp reads 128
+// contiguous bytes of each bf16 row): a block's largest value needs no
+// exchange, a lane ends with 32 contiguous bytes of each of its two output
+// rows, and the four warps of a CTA, one below the other, with a 128-byte
+// line.  Neither goes through shared memory.
 
 #include "dp_launch.h"
 #include "dp_mx4.cuh"
@@ -37,10 +39,9 @@ constexpr int kWarps = kThreads / 32;
 struct QuantParams {
   const void* x[kMaxK];
   int rows;        // of one shard
-  int in_rows;     // of all
-  int cols;
   long long ld;    // elements between rows of a shard
-  int vec_ok;
+  int vec_ok;      // the loads of several elements are aligned
+  int whole;       // each 32 concatenated rows lie in one shard
   int R, L;        // the output: R rows of L values (blocks run along L)
   int col_tiles;
   const float* tscale;
@@ -48,10 +49,10 @@ struct QuantParams {
   uint8_t* scales;
 };
 
-__device__ __forceinline__ const void* row_at(const QuantParams& p, int r, int esz) {
+template <typename T>
+__device__ __forceinline__ const T* row_at(const QuantParams& p, int r) {
   const int k = r < p.rows ? 0 : r / p.rows;
-  return static_cast<const uint8_t*>(p.x[k]) +
-         (long long)(r - k * p.rows) * p.ld * esz;
+  return static_cast<const T*>(p.x[k]) + (long long)(r - k * p.rows) * p.ld;
 }
 
 // Eight fp32 values to eight e2m1 codes, the first in the lowest half byte.
@@ -95,34 +96,75 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   return lo;
 }
 
-// A block's scale byte from its largest magnitude, and what its values are
-// divided by (nvfp4) or multiplied by (mxfp4); `zero`: every code is zero.
-template <int BLOCK>
-__device__ __forceinline__ uint32_t block_scale(float amax, float t, float& f, bool& zero) {
-  const uint32_t bits = __float_as_uint(amax);
-  const bool finite = bits < 0x7f800000u;
-  if constexpr (BLOCK == kMxBlock) {
-    const int e = (int)(bits >> 23) - 2;
-    const uint32_t byte = finite ? (uint32_t)max(e, 0) : 255u;
-    f = __uint_as_float((254u - byte) << 23);
-    zero = !finite;
-    return byte;
-  } else {
-    uint16_t c;
-    const float s = amax > 0.0f ? __fdiv_rn(__fmul_rn(amax, 1.0f / 6.0f), t) : 0.0f;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(s));
-    const uint32_t byte = finite ? (uint32_t)c & 0xffu : 0x7fu;
-    f = __fmul_rn(e4m3_value(byte), t);
-    zero = !(f > 0.0f);
-    return byte;
+// Division by a value that many others are divided by, as a product with its
+// reciprocal in two words (hi + lo, relative error below 2^-46): x hi is
+// rounded once, together with x lo, so the result is the rounded quotient
+// unless the quotient lies within 2^-46 of a midpoint between two fp32 values;
+// a quotient that is an fp32 value, a tie between two codes among them, comes
+// out exactly.  Measured against __fdiv_rn for every value: 8192 x 4096 bf16 to
+// nvfp4 43.9 us with it.  Divisors too far from 1 for the two words take the
+// division.
+struct Divisor {
+  float d, hi, lo;
+  bool near;
+  __device__ __forceinline__ explicit Divisor(float v) : d(v) {
+    near = v > 1e-30f && v < 1e30f;
+    hi = __frcp_rn(v);
+    lo = __fmul_rn(__fmaf_rn(-hi, v, 1.0f), hi);
   }
-}
+  __device__ __forceinline__ float of(float x) const {
+    return near ? __fmaf_rn(x, hi, __fmul_rn(x, lo)) : __fdiv_rn(x, d);
+  }
+};
 
+// The tensor's scale, and a block's: its byte from the block's largest
+// magnitude, and eight of its values to codes.
 template <int BLOCK>
-__device__ __forceinline__ float scaled(float x, float f, bool zero) {
-  if (zero) return 0.0f;
-  return BLOCK == kMxBlock ? __fmul_rn(x, f) : __fdiv_rn(x, f);
-}
+struct Scale;
+
+template <>
+struct Scale<kMxBlock> {
+  uint32_t byte;
+  float f;
+  bool zero;
+  __device__ __forceinline__ Scale(float amax, float, const Divisor&) {
+    const uint32_t bits = __float_as_uint(amax);
+    zero = bits >= 0x7f800000u;
+    byte = zero ? 255u : (uint32_t)max((int)(bits >> 23) - 2, 0);
+    f = __uint_as_float((254u - byte) << 23);
+  }
+  __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __fmul_rn(v[i], f);
+    return zero ? 0u : pack_e2m1(w);
+  }
+};
+
+template <>
+struct Scale<kNvBlock> {
+  uint32_t byte;
+  float step;
+  __device__ __forceinline__ Scale(float amax, float t, const Divisor& by_t) {
+    uint16_t c;
+    const float s = amax > 0.0f ? by_t.of(__fmul_rn(amax, 1.0f / 6.0f)) : 0.0f;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(s));
+    byte = __float_as_uint(amax) < 0x7f800000u ? (uint32_t)c & 0xffu : 0x7fu;
+    step = __fmul_rn(e4m3_value(byte), t);
+  }
+  __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
+    const Divisor by(step);
+    float w[8];
+    if (by.near) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __fmaf_rn(v[i], by.hi, __fmul_rn(v[i], by.lo));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __fdiv_rn(v[i], step);
+    }
+    return step > 0.0f ? pack_e2m1(w) : 0u;  // also where the step is NaN
+  }
+};
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -144,43 +186,38 @@ __device__ __forceinline__ size_t scale_at(int row, int tile, int col_tiles) {
 
 // ---- rows form ---------------------------------------------------------------
 
-template <typename T, int BLOCK>
-__global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_constant__ QuantParams p) {
+// One row's G x 256 columns from e0 on, by a warp.
+template <typename T, int BLOCK, int G>
+__device__ __forceinline__ void quant_row(const QuantParams& p, int r, int e0, bool vec, float t,
+                                          const Divisor& by_t) {
   constexpr int kLanes = BLOCK / 8;  // lanes of a block
   const int lane = threadIdx.x & 31;
-  const int segs = (p.col_tiles * 4 * BLOCK + 255) / 256;
-  const long long units = (long long)((p.R + kScaleRows - 1) / kScaleRows * kScaleRows) * segs;
-  const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
-  for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * kWarps) {
-    const int r = (int)(u / segs);
-    const int e = (int)(u - (long long)r * segs) * 256 + lane * 8;
-    const bool in = r < p.R && e < p.L;
-    float v[8];
+  float v[G][8];
+  const T* x = r < p.R ? row_at<T>(p, r) : nullptr;
+  if (x && vec && e0 + G * 256 <= p.L) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (in) {
-      const T* x = static_cast<const T*>(row_at(p, r, sizeof(T))) + e;
-      if (p.vec_ok) {
-        load8(x, v);
-      } else {
+    for (int g = 0; g < G; ++g) load8(x + e0 + g * 256 + lane * 8, v[g]);
+  } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = widen_scalar(x, i);
-      }
+    for (int g = 0; g < G; ++g) {
+      const int e = e0 + g * 256 + lane * 8;
+      const bool in = x && e < p.L;  // L is a multiple of 32: all eight are inside or none
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[g][i] = in ? widen_scalar(x, e + i) : 0.0f;
     }
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int e = e0 + g * 256 + lane * 8;
     uint32_t top = 0;  // magnitudes order as their bits, NaN above all
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[g][i]) & 0x7fffffffu);
 #pragma unroll
     for (int o = 1; o < kLanes; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float f;
-    bool zero;
-    uint32_t byte = block_scale<BLOCK>(__uint_as_float(top), t, f, zero);
-    if (!in) byte = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = scaled<BLOCK>(v[i], f, zero);
-    if (in)
-      *reinterpret_cast<uint32_t*>(p.codes + (size_t)r * (p.L / 2) + e / 2) = pack_e2m1(v);
+    const Scale<BLOCK> s(__uint_as_float(top), t, by_t);
+    if (x && e < p.L)
+      *reinterpret_cast<uint32_t*>(p.codes + (size_t)r * (p.L / 2) + e / 2) = s.codes(v[g]);
+    const uint32_t byte = x && e < p.L ? s.byte : 0u;
     uint32_t four = byte;
 #pragma unroll
     for (int i = 1; i < 4; ++i)
@@ -191,75 +228,97 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_const
   }
 }
 
+template <typename T, int BLOCK, int G>
+__global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_constant__ QuantParams p) {
+  const unsigned groups = ((unsigned)p.col_tiles * 4 * BLOCK + G * 256 - 1) / (G * 256);
+  const unsigned blocks = ((unsigned)p.R + kScaleRows - 1) / kScaleRows * (kScaleRows / kWarps) * groups;
+  const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
+  const Divisor by_t(t);
+  for (unsigned b = blockIdx.x; b < blocks; b += gridDim.x) {
+    const unsigned q = b / groups;
+    quant_row<T, BLOCK, G>(p, (int)(q * kWarps + (threadIdx.x >> 5)), (int)((b - q * groups) * G * 256),
+                           p.vec_ok, t, by_t);
+  }
+}
+
 // ---- transposed form ----------------------------------------------------------
 
-__device__ __forceinline__ void load2(const float* p, bool vec, bool two, float& a, float& b) {
-  if (vec) {
-    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
-    a = v.x;
-    b = v.y;
-  } else {
-    a = __ldg(p);
-    b = two ? __ldg(p + 1) : 0.0f;
-  }
+// Two neighbouring columns of a row.
+template <bool FAST>
+__device__ __forceinline__ float2 load2(const float* x, int c, int last) {
+  if constexpr (FAST) return __ldg(reinterpret_cast<const float2*>(x + c));
+  return make_float2(__ldg(x + c), __ldg(x + min(c + 1, last)));
 }
-__device__ __forceinline__ void load2(const uint16_t* p, bool vec, bool two, float& a, float& b) {
-  if (vec) {
-    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p));
-    a = bf16lo(v);
-    b = bf16hi(v);
-  } else {
-    a = widen_scalar(p, 0);
-    b = two ? widen_scalar(p, 1) : 0.0f;
-  }
+template <bool FAST>
+__device__ __forceinline__ uint32_t load2(const uint16_t* x, int c, int last) {
+  if constexpr (FAST) return __ldg(reinterpret_cast<const uint32_t*>(x + c));
+  return (uint32_t)__ldg(x + c) | (uint32_t)__ldg(x + min(c + 1, last)) << 16;
 }
+__device__ __forceinline__ float part(float2 v, int j) { return j ? v.y : v.x; }
+__device__ __forceinline__ float part(uint32_t v, int j) { return j ? bf16hi(v) : bf16lo(v); }
+
+template <typename T>
+struct Pair;
+template <>
+struct Pair<float> {
+  using type = float2;
+};
+template <>
+struct Pair<uint16_t> {
+  using type = uint32_t;
+};
 
 constexpr int kTRows = 64;  // input rows a warp takes at once: 32 bytes of each output row
 
-template <typename T, int BLOCK>
+// FAST: two columns are one aligned load, R is even and 32 rows lie in one
+// shard.  Otherwise columns past the last are read as the last (and dropped),
+// so that no load hangs on a branch.
+template <typename T, int BLOCK, bool FAST>
 __global__ void __launch_bounds__(kThreads) quant_cols_kernel(const __grid_constant__ QuantParams p) {
   constexpr int kBlocks = kTRows / BLOCK;
   const int lane = threadIdx.x & 31;
-  const int cgroups = (p.R + kScaleRows - 1) / kScaleRows * 2;  // 64 columns each
-  const long long units = (long long)cgroups * ((p.col_tiles * 4 * BLOCK + kTRows - 1) / kTRows);
+  const unsigned cgroups = ((unsigned)p.R + kScaleRows - 1) / kScaleRows * 2;  // 64 columns each
+  const unsigned rgroups = ((unsigned)p.col_tiles * 4 * BLOCK + kTRows * kWarps - 1) / (kTRows * kWarps);
   const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
-  for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * kWarps) {
-    const int g = (int)(u / cgroups);
-    const int c = (int)(u - (long long)g * cgroups) * 64 + lane * 2;  // input column = output row
-    const int l0 = g * kTRows;
-    const bool in = c < p.R, two = c + 1 < p.R;
+  const Divisor by_t(t);
+  for (unsigned u = blockIdx.x; u < cgroups * rgroups; u += gridDim.x) {
+    const unsigned q = u / cgroups;
+    const int c = (int)(u - q * cgroups) * 64 + lane * 2;  // input column = output row
+    const int l0 = (int)(q * kWarps + (threadIdx.x >> 5)) * kTRows;
+    if (l0 >= p.col_tiles * 4 * BLOCK) continue;
+    const int cl = min(c, FAST ? p.R - 2 : p.R - 1);
     uint32_t code[2][kTRows / 8];
     uint32_t sc[2] = {0, 0};
 #pragma unroll
-    for (int b = 0; b < kBlocks; ++b) {
-      const int l = l0 + b * BLOCK;  // L is a multiple of 32: a block is inside or outside
-      float v[2][BLOCK];
-      const bool inside = in && l < p.L;
+    for (int h = 0; h < 2; ++h) {
+      const int l = l0 + 32 * h;
+      if (l >= p.L) continue;  // L is a multiple of 32
+      typename Pair<T>::type v[32];
+      const T* x = row_at<T>(p, l);
 #pragma unroll
-      for (int i = 0; i < BLOCK; ++i) {
-        v[0][i] = v[1][i] = 0.0f;
-        if (inside)
-          load2(static_cast<const T*>(row_at(p, l + i, sizeof(T))) + c, p.vec_ok && two, two,
-                v[0][i], v[1][i]);
+      for (int i = 0; i < 32; ++i) {
+        if (!FAST && !p.whole && i) x = row_at<T>(p, l + i);
+        v[i] = load2<FAST>(x, cl, p.R - 1);
+        if (FAST || p.whole) x += p.ld;
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t top = 0;
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < BLOCK; ++i) top = max(top, __float_as_uint(v[j][i]) & 0x7fffffffu);
-        float f;
-        bool zero;
-        const uint32_t byte = block_scale<BLOCK>(__uint_as_float(top), t, f, zero);
-        if (inside && (j == 0 || two)) sc[j] |= byte << (8 * b);
+        for (int b = 0; b < 32 / BLOCK; ++b) {
+          uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < BLOCK / 8; ++i) {
-          float w[8];
+          for (int i = 0; i < BLOCK; ++i)
+            top = max(top, __float_as_uint(part(v[b * BLOCK + i], j)) & 0x7fffffffu);
+          const Scale<BLOCK> s(__uint_as_float(top), t, by_t);
+          if (c + j < p.R) sc[j] |= s.byte << (8 * (h * (32 / BLOCK) + b));
 #pragma unroll
-          for (int q = 0; q < 8; ++q) w[q] = scaled<BLOCK>(v[j][8 * i + q], f, zero);
-          code[j][b * (BLOCK / 8) + i] = pack_e2m1(w);
+          for (int i = 0; i < BLOCK / 8; ++i) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = part(v[b * BLOCK + 8 * i + e], j);
+            code[j][4 * h + b * (BLOCK / 8) + i] = s.codes(w);
+          }
         }
-      }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -272,14 +331,11 @@ __global__ void __launch_bounds__(kThreads) quant_cols_kernel(const __grid_const
                 code[j][4 * h], code[j][4 * h + 1], code[j][4 * h + 2], code[j][4 * h + 3]);
       }
       // the scales of 64 rows: a tile's four (nvfp4) or half of them (mxfp4)
-      const int tile = l0 / (4 * BLOCK);
-      uint8_t* s = p.scales + scale_at(c + j, tile, p.col_tiles);
-      if (tile < p.col_tiles) {
-        if constexpr (kBlocks == 4)
-          *reinterpret_cast<uint32_t*>(s) = sc[j];
-        else
-          *reinterpret_cast<uint16_t*>(s + (l0 / BLOCK) % 4) = (uint16_t)sc[j];
-      }
+      uint8_t* s = p.scales + scale_at(c + j, l0 / (4 * BLOCK), p.col_tiles);
+      if constexpr (kBlocks == 4)
+        *reinterpret_cast<uint32_t*>(s) = sc[j];
+      else
+        *reinterpret_cast<uint16_t*>(s + (l0 / BLOCK) % 4) = (uint16_t)sc[j];
     }
   }
 }
@@ -297,54 +353,84 @@ struct DecodeParams {
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) { store8_f32(p, v); }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) { store8_bf16(p, v); }
 
-template <typename T, int BLOCK>
+template <int BLOCK>
+__device__ __forceinline__ float step_of(uint32_t byte, float t) {
+  if constexpr (BLOCK == kNvBlock) return __fmul_rn(e4m3_value(byte), t);
+  if (byte == 255u) return __uint_as_float(0x7fffffffu);
+  return __uint_as_float(byte ? byte << 23 : 0x00400000u);  // 2^-127 is subnormal
+}
+
+// A warp takes G x 256 columns of a row, a lane eight of each 256.
+template <typename T, int BLOCK, int G>
 __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant__ DecodeParams p) {
   const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
   const int lane = threadIdx.x & 31;
-  const int segs = (p.L + 255) / 256;
-  const long long units = (long long)p.R * segs;
-  for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * kWarps) {
-    const int r = (int)(u / segs);
-    const int e = (int)(u - (long long)r * segs) * 256 + lane * 8;
-    if (e >= p.L) continue;
-    const int b = e / BLOCK;
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.codes + (size_t)r * (p.L / 2) + e / 2));
-    const uint32_t byte = __ldg(p.scales + scale_at(r, b / 4, p.col_tiles) + b % 4);
-    float step;
-    if constexpr (BLOCK == kMxBlock)  // 2^(byte - 127): a subnormal at 0
-      step = byte == 255 ? __uint_as_float(0x7fffffffu)
-                         : (byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u));
-    else
-      step = __fmul_rn(e4m3_value(byte), t);
-    float v[8];
-    unpack_e2m1(c, v);
+  const unsigned groups = ((unsigned)p.L + G * 256 - 1) / (G * 256);
+  const unsigned blocks = ((unsigned)p.R + kWarps - 1) / kWarps * groups;
+  for (unsigned u = blockIdx.x; u < blocks; u += gridDim.x) {
+    const unsigned q = u / groups;
+    const int r = (int)(q * kWarps + (threadIdx.x >> 5));
+    const int e0 = (int)((u - q * groups) * G * 256) + lane * 8;
+    if (r >= p.R) continue;
+    const uint8_t* codes = p.codes + (size_t)r * (p.L / 2);
+    uint32_t c[G], byte[G];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], step);
-    store8(static_cast<T*>(p.out) + (size_t)r * p.L + e, v);
+    for (int g = 0; g < G; ++g) {
+      const int e = min(e0 + g * 256, p.L - 8);  // past the end: the last, and dropped
+      const int b = e / BLOCK;
+      c[g] = __ldg(reinterpret_cast<const uint32_t*>(codes + e / 2));
+      byte[g] = __ldg(p.scales + scale_at(r, b / 4, p.col_tiles) + b % 4);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int e = e0 + g * 256;
+      const float step = step_of<BLOCK>(byte[g], t);
+      float v[8];
+      unpack_e2m1(c[g], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], step);
+      if (e < p.L) store8(static_cast<T*>(p.out) + (size_t)r * p.L + e, v);
+    }
   }
 }
 
+// One CTA for each share of the work, which the hardware hands out as SMs
+// become free; under a CTA limit the CTAs go over the shares.
 template <typename KernelT, typename P>
-cudaError_t launch(KernelT kernel, const P& p, long long units, const dph::DeviceInfo& dev,
-                   cudaStream_t s) {
-  const int b = dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kThreads, 0, dev.device);
-  long long resident = (long long)dev.sm_count * (b < 1 ? 1 : b);
+cudaError_t launch(KernelT kernel, const P& p, long long blocks, cudaStream_t s) {
   const int limit = dph::stream_cta_limit();
-  if (limit > 0 && resident > limit) resident = limit;
-  const long long grid = std::max(1LL, std::min(resident, (units + kWarps - 1) / kWarps));
-  kernel<<<(unsigned)grid, kThreads, 0, s>>>(p);
+  if (limit > 0) blocks = std::min<long long>(blocks, limit);
+  kernel<<<(unsigned)std::min<long long>(blocks, 0x7fffffffll), kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Columns a warp takes at once in the rows form and in decoding: all its loads
+// are in flight together, so 1024 where rows are that long and enough of them
+// to fill the GPU; short calls spread wider with 256.
+bool wide(long long rows, long long cols) { return cols >= 1024 && rows * cols >= (1ll << 21); }
+
 template <typename T, int BLOCK>
-cudaError_t quantize(const QuantParams& p, bool transpose, const dph::DeviceInfo& dev,
-                     cudaStream_t s) {
-  const long long rows = (p.R + kScaleRows - 1) / kScaleRows * kScaleRows;
+cudaError_t quantize(const QuantParams& p, bool transpose, cudaStream_t s) {
+  const long long rows = ceil_div(p.R, kScaleRows) * kScaleRows;
   const long long cols = (long long)p.col_tiles * 4 * BLOCK;
-  if (transpose)
-    return launch(quant_cols_kernel<T, BLOCK>, p, rows / 64 * ((cols + kTRows - 1) / kTRows), dev, s);
-  return launch(quant_rows_kernel<T, BLOCK>, p, rows * ((cols + 255) / 256), dev, s);
+  if (transpose) {
+    const long long blocks = rows / 64 * ceil_div(cols, kTRows * kWarps);
+    if (p.vec_ok && p.whole && p.R % 2 == 0)
+      return launch(quant_cols_kernel<T, BLOCK, true>, p, blocks, s);
+    return launch(quant_cols_kernel<T, BLOCK, false>, p, blocks, s);
+  }
+  if (wide(p.R, p.L))
+    return launch(quant_rows_kernel<T, BLOCK, 4>, p, rows / kWarps * ceil_div(cols, 1024), s);
+  return launch(quant_rows_kernel<T, BLOCK, 1>, p, rows / kWarps * ceil_div(cols, 256), s);
+}
+
+template <typename T, int BLOCK>
+cudaError_t decode(const DecodeParams& p, cudaStream_t s) {
+  if (wide(p.R, p.L))
+    return launch(decode_kernel<T, BLOCK, 4>, p, ceil_div(p.R, kWarps) * ceil_div(p.L, 1024), s);
+  return launch(decode_kernel<T, BLOCK, 1>, p, ceil_div(p.R, kWarps) * ceil_div(p.L, 256), s);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -412,8 +498,7 @@ dp_status_t dp_mx4_quantize(const void* const* x, int K, int rows, int cols, lon
     if (clash(in, out[0]) || clash(in, out[1])) return DP_ERR_ALIAS;
   }
   p.rows = rows;
-  p.in_rows = (int)all;
-  p.cols = cols;
+  p.whole = K == 1 || rows % 32 == 0;
   p.ld = ld;
   p.vec_ok = vec && ld % (transpose ? 2 : 8) == 0;
   p.R = R;
@@ -427,11 +512,11 @@ dp_status_t dp_mx4_quantize(const void* const* x, int K, int rows, int cols, lon
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (x_dtype == DP_FP32)
-    e = format == DP_NVFP4 ? quantize<float, kNvBlock>(p, transpose, dev, s)
-                           : quantize<float, kMxBlock>(p, transpose, dev, s);
+    e = format == DP_NVFP4 ? quantize<float, kNvBlock>(p, transpose, s)
+                           : quantize<float, kMxBlock>(p, transpose, s);
   else
-    e = format == DP_NVFP4 ? quantize<uint16_t, kNvBlock>(p, transpose, dev, s)
-                           : quantize<uint16_t, kMxBlock>(p, transpose, dev, s);
+    e = format == DP_NVFP4 ? quantize<uint16_t, kNvBlock>(p, transpose, s)
+                           : quantize<uint16_t, kMxBlock>(p, transpose, s);
   return e == cudaSuccess ? DP_OK : DP_ERR_CUDA;
 }
 
@@ -459,14 +544,13 @@ dp_status_t dp_mx4_dequantize(const void* codes, const void* scales, int rows, i
   dph::DeviceInfo dev;
   if (!dph::current_device(&dev)) return DP_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const long long units = (long long)rows * ((cols + 255) / 256);
   cudaError_t e;
   if (out_dtype == DP_FP32)
-    e = format == DP_NVFP4 ? launch(decode_kernel<float, kNvBlock>, p, units, dev, s)
-                           : launch(decode_kernel<float, kMxBlock>, p, units, dev, s);
+    e = format == DP_NVFP4 ? decode<float, kNvBlock>(p, s)
+                           : decode<float, kMxBlock>(p, s);
   else
-    e = format == DP_NVFP4 ? launch(decode_kernel<uint16_t, kNvBlock>, p, units, dev, s)
-                           : launch(decode_kernel<uint16_t, kMxBlock>, p, units, dev, s);
+    e = format == DP_NVFP4 ? decode<uint16_t, kNvBlock>(p, s)
+                           : decode<uint16_t, kMxBlock>(p, s);
   return e == cudaSuccess ? DP_OK : DP_ERR_CUDA;
 }
 

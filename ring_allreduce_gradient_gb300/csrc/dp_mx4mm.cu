@@ -13,20 +13,25 @@
 // (one token: 16 of the instruction's columns), and a warp's store covers 32
 // consecutive f of a token.
 //
-// One CTA (384 threads) per SM, persistent over tiles of 128 f x BN tokens:
-//   warp 0      W producer: 128 rows x 256 values (128 bytes) by TMA, and the
-//               rows' scales, a contiguous copy of the 512-byte scale tiles
+// One CTA (512 threads) per SM, persistent over tiles of 128 f x BN tokens:
+//   warp 0      W producer: 128 rows x 256 values (128 bytes) by TMA
 //   warp 2      X producer: BN rows x 256 values; also allocates TMEM
-//   warp 3      X scales' producer
-//   warp 1      MMA issuer: copies a stage's scales into TMEM (tcgen05.cp,
-//               each 512-byte tile to four columns, for all four groups of 32
-//               lanes), then four MMAs of 64 values; a stage has its own scale
-//               columns, so they are overwritten only when the stage is
-//   warps 4-11  epilogue: a warp takes 32 f and half of the tokens, reads its
-//               accumulator columns into registers at once, releases TMEM and
-//               then scales, packs and stores while the next tile runs
-// TMEM: 256 accumulator columns (one tile) and 4 x 48 scale columns.  With
-// the scales two accumulators of 256 columns do not fit.
+//   warp 3      scales' producer: the rows' 512-byte scale tiles, contiguous copies
+//   warps 12-15 scales into TMEM: lane l of each 32-lane quarter takes row l of a
+//               scale tile (16 bytes: four columns), tcgen05.st
+//   warp 1      MMA issuer: four MMAs of 64 values a stage
+//   warps 4-11  epilogue: a warp takes 32 f and half of the tokens, packs its
+//               accumulator columns into registers, releases TMEM and stores
+//               while the next tile runs
+// TMEM: 256 accumulator columns (one tile) and 4 x 48 scale columns: a stage
+// has its own, so they are overwritten only when the stage is.  With the
+// scales two accumulators of 256 columns do not fit.
+//
+// The scales go through registers because tcgen05.cp, which copies a scale
+// tile straight from shared memory, takes its turn with the MMAs: x[8192,8192]
+// . w[8192,8192]^T took 500 us (nvfp4, 12 copies a stage) and 348 us (mxfp4, 6)
+// with it, and 208 / 202 us with the copies of all stages but the first left
+// out, where operand intake (54 KiB a stage) is the limit.
 //
 // Few tiles: the blocks of d are split over a cluster of 2, 4 or 8 CTAs,
 // whose fp32 partial sums meet in shared memory: each CTA adds a share of the
@@ -61,7 +66,7 @@ constexpr size_t kSmemBytes =
 constexpr int kTmemCols = 512;
 constexpr int kScaleCol0 = kMaxBN;   // first scale column
 constexpr int kScaleCols = 48;       // per stage: 16 for W, 32 for X
-constexpr int kThreadsM = 384;
+constexpr int kThreadsM = 512;
 constexpr int kEpiWarps = 8;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kMaxSplit = 8;
@@ -95,21 +100,6 @@ __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* 
           "r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
-}
-
-// A scale tile in shared memory: 32 rows of 16 bytes, unswizzled, 8-row groups
-// 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);  // bits 0-13: start address >> 4
-  d |= (uint64_t)(128u >> 4) << 32;          // bits 32-45: stride byte offset >> 4
-  d |= (uint64_t)1u << 46;                   // bits 46-48: fixed 0b001
-  return d;                                  // bits 61-63: no swizzle
-}
-
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t saddr) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(scale_desc(saddr))
-               : "memory");
 }
 
 // Instruction descriptor of the block-scaled kinds: A and B e2m1, both
@@ -179,7 +169,9 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   uint8_t* sSX = sSW + kStages * kStageSW;
   uint64_t* full = reinterpret_cast<uint64_t*>(sSX + kStages * kStageSX);
   uint64_t* empty = full + kStages;
-  uint64_t* tmem_full = empty + kStages;
+  uint64_t* sfull = empty + kStages;    // a stage's scales are in shared memory
+  uint64_t* sready = sfull + kStages;   // ... and in TMEM
+  uint64_t* tmem_full = sready + kStages;
   uint64_t* tmem_empty = tmem_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_empty + 1);
   volatile int* aborted = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -194,8 +186,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 3);  // three producers
+      mbar_init(&full[s], 2);  // W and X
       mbar_init(&empty[s], 1);
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sready[s], 4);  // one arrival per scale warp
     }
     mbar_init(tmem_full, 1);
     mbar_init(tmem_empty, kEpiWarps);
@@ -237,20 +231,20 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           const uint32_t sbytes =
               (uint32_t)min(kTilesKb, p.col_tiles - t0) * kScaleTile;  // the last stage may end early
           if (warp == 0) {
-            mbar_arrive_expect_tx(&full[stage], kStageW + sbytes);
+            mbar_arrive_expect_tx(&full[stage], kStageW);
             tma_load_2d(&p.tmW[shard], &full[stage], sW + stage * kStageW, kb * (BK / 2), f0);
-            bulk_load(&full[stage], sSW + stage * kStageSW,
-                      p.sw[shard] + ((size_t)(f0 / kScaleRows) * p.col_tiles + t0) * kScaleTile,
-                      sbytes);
           } else if (warp == 2) {
             mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * (BK / 2));
             tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), m0);
           } else {
             const int r0 = m0 / kScaleRows;
             const int rows = min((p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
-            mbar_arrive_expect_tx(&full[stage], sbytes * (uint32_t)rows);
+            mbar_arrive_expect_tx(&sfull[stage], sbytes * (uint32_t)(rows + 1));
+            bulk_load(&sfull[stage], sSW + stage * kStageSW,
+                      p.sw[shard] + ((size_t)(f0 / kScaleRows) * p.col_tiles + t0) * kScaleTile,
+                      sbytes);
             for (int r = 0; r < rows; ++r)
-              bulk_load(&full[stage], sSX + stage * kStageSX + r * kScaleKb,
+              bulk_load(&sfull[stage], sSX + stage * kStageSX + r * kScaleKb,
                         p.sx + ((size_t)(r0 + r) * p.col_tiles + t0) * kScaleTile, sbytes);
           }
           armed[stage] = true;
@@ -263,7 +257,9 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       }
       // Drain: every load this thread issued has landed before the CTA exits.
       for (int s = 0; s < kStages; ++s)
-        if (armed[s]) (void)mbar_wait_bounded(&full[s], armed_phase[s], p.err, kTimeoutNs);
+        if (armed[s])
+          (void)mbar_wait_bounded(warp == 3 ? &sfull[s] : &full[s], armed_phase[s], p.err,
+                                  kTimeoutNs);
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer --------------------------------
@@ -278,26 +274,18 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           break;
         }
         tc_fence_after();
-        const int x_tiles = min((p.BN + kScaleRows - 1) / kScaleRows,
-                                p.x_row_tiles - (p.tile0 + i) % p.tiles_m * p.BN / kScaleRows);
         bool ok = true;
         for (int kb = kb_lo; kb < kb_hi; ++kb) {
-          if (!mbar_wait_bounded(&full[stage], phase, p.err, kTimeoutNs)) {
+          if (!mbar_wait_bounded(&full[stage], phase, p.err, kTimeoutNs) ||
+              !mbar_wait_bounded(&sready[stage], phase, p.err, kTimeoutNs)) {
             *aborted = 1;
             ok = false;
             break;
           }
           tc_fence_after();
           const int steps = min(BK / kStep, (p.D - kb * BK + kStep - 1) / kStep);
-          const int stiles = min(kTilesKb, p.col_tiles - kb * kTilesKb);
           const uint32_t tw = tmem_base + (uint32_t)(kScaleCol0 + stage * kScaleCols);
           const uint32_t tx = tw + 16u;
-          const uint32_t aw = smem_u32(sSW + stage * kStageSW), ax = smem_u32(sSX + stage * kStageSX);
-          for (int t = 0; t < stiles; ++t) {
-            copy_scales(tw + 4u * t, aw + (uint32_t)t * kScaleTile);
-            for (int r = 0; r < x_tiles; ++r)
-              copy_scales(tx + 8u * t + 4u * r, ax + r * kScaleKb + (uint32_t)t * kScaleTile);
-          }
           const uint32_t a0 = smem_u32(sW + stage * kStageW), b0 = smem_u32(sX + stage * kStageX);
 #pragma unroll
           for (int k = 0; k < BK / kStep; ++k) {
@@ -328,6 +316,56 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         (void)mbar_wait_bounded(&empty[last], last_phase, p.err, kTimeoutNs);
       }
     }
+  } else if (warp >= 12) {
+    // ------------------------------ scales into TMEM --------------------------
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = first; i < p.tiles && !*aborted; i += stride) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        const bool ok = mbar_wait_bounded(&sfull[stage], phase, p.err, kTimeoutNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          *aborted = 1;
+          break;
+        }
+        tc_fence_after();
+        // this quarter's copy of each tile; a tile that the last stage lacks,
+        // or a second row tile that X lacks, is stale and belongs to no step or
+        // to no token
+        const uint8_t* gw = sSW + stage * kStageSW + lane * 16;
+        const uint8_t* gx = sSX + stage * kStageSX + lane * 16;
+        const uint32_t tw = tmem_base + lanes + (uint32_t)(kScaleCol0 + stage * kScaleCols);
+        uint32_t w[4 * kTilesKb], x[8 * kTilesKb];
+#pragma unroll
+        for (int t = 0; t < kTilesKb; ++t) {
+          const uint4 a = *reinterpret_cast<const uint4*>(gw + t * kScaleTile);
+          w[4 * t] = a.x, w[4 * t + 1] = a.y, w[4 * t + 2] = a.z, w[4 * t + 3] = a.w;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint4 b = *reinterpret_cast<const uint4*>(gx + r * kScaleKb + t * kScaleTile);
+            const int o = 8 * t + 4 * r;
+            x[o] = b.x, x[o + 1] = b.y, x[o + 2] = b.z, x[o + 3] = b.w;
+          }
+        }
+        if constexpr (MX) {
+          DP_TMEM_ST_X8(tw, w);
+          DP_TMEM_ST_X16(tw + 16u, x);
+        } else {
+          DP_TMEM_ST_X16(tw, w);
+          DP_TMEM_ST_X16(tw + 16u, x);
+          const uint32_t* hi = x + 16;
+          DP_TMEM_ST_X16(tw + 32u, hi);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sready[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
   } else {
     // ------------------------------ epilogue ----------------------------------
     const int quarter = warp & 3;          // the TMEM lanes this warp may read
@@ -341,7 +379,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       const int tile = p.tile0 + i;
       const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
       const int shard = ft / p.tiles_f, f0 = (ft - shard * p.tiles_f) * BM;
-      const int m0 = mt * p.BN;
+      const int m0 = mt * p.BN + c0 * 16;
       float alpha = 1.0f;
       if constexpr (!MX) {
         if (p.tx) alpha = __ldg(p.tx);
@@ -353,62 +391,70 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         break;
       }
       tc_fence_after();
-      uint32_t r[8][16];
       const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c0 * 16);
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (c < cn) DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16), r[c]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tmem_empty);
-      if (p.split > 1) {
-        // the partial sums, [token][128 f], where the operands were: every
-        // MMA of this tile, the CTA's only one, has completed
-        float* red = reinterpret_cast<float*>(smem);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c < cn) {
-#pragma unroll
-            for (int q = 0; q < 16; ++q)
-              red[((c0 + c) * 16 + q) * BM + fl] = __uint_as_float(r[c][q]);
-          }
-        continue;
-      }
       const int f = f0 + fl;                       // inside the shard
       const size_t yf = (size_t)shard * p.F_shard + f;
       const bool f_in = f < p.F_shard;
-      if (p.y_f32) {
+      if (p.split > 1 || p.y_f32) {
+        // 32-bit values leave chunk by chunk: the partial sums of a split tile
+        // as [token][128 f] to where the operands were (every MMA of this tile,
+        // the CTA's only one, has completed), or y
+        float* red = reinterpret_cast<float*>(smem) + c0 * 16 * BM + fl;
         float* y = static_cast<float*>(p.y) + yf;
+        for (int c = 0; c < cn; ++c) {
+          uint32_t r[16];
+          DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16), r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c < cn) {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const int m = m0 + (c0 + c) * 16 + q;
-              if (f_in && m < p.M) y[(size_t)m * p.F] = __fmul_rn(__uint_as_float(r[c][q]), alpha);
-            }
+          for (int q = 0; q < 16; ++q) {
+            const int m = m0 + c * 16 + q;
+            if (p.split > 1)
+              red[(c * 16 + q) * BM] = __uint_as_float(r[q]);
+            else if (f_in && m < p.M)
+              y[(size_t)m * p.F] = __fmul_rn(__uint_as_float(r[q]), alpha);
           }
-      } else {
-        // neighbouring lanes trade values of two tokens, so that each lane
-        // stores two f of one token (F_shard is even)
-        uint16_t* y = static_cast<uint16_t*>(p.y) + (yf & ~(size_t)1);
-        const bool odd = lane & 1;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c < cn) {
-#pragma unroll
-            for (int q = 0; q < 16; q += 2) {
-              const float a = __fmul_rn(__uint_as_float(r[c][q]), alpha);
-              const float b = __fmul_rn(__uint_as_float(r[c][q + 1]), alpha);
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-              const int m = m0 + (c0 + c) * 16 + q + (odd ? 1 : 0);
-              if (f_in && m < p.M)
-                *reinterpret_cast<uint32_t*>(y + (size_t)m * p.F) =
-                    odd ? pack_bf16x2_rn(got, b) : pack_bf16x2_rn(a, got);
-            }
-          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tmem_empty);
+        continue;
       }
+      // bf16: pairs of tokens are packed into a register as they are read, so
+      // the accumulator is free again before the first store
+      uint32_t h[8][8];
+#pragma unroll
+      for (int c = 0; c < 8; c += 2) {
+        uint32_t r[2][16];
+        if (c < cn) DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16), r[0]);
+        if (c + 1 < cn) DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16 + 16), r[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (c + e < cn)
+              h[c + e][q] = pack_bf16x2_rn(__fmul_rn(__uint_as_float(r[e][2 * q]), alpha),
+                                           __fmul_rn(__uint_as_float(r[e][2 * q + 1]), alpha));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tmem_empty);
+      // neighbouring lanes trade halves, so that each stores two f of one
+      // token (F_shard is even)
+      const bool odd = lane & 1;
+      uint16_t* y = static_cast<uint16_t*>(p.y) + (yf & ~(size_t)1);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < cn) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, h[c][q], 1);
+            const int m = m0 + c * 16 + 2 * q + (odd ? 1 : 0);
+            if (f_in && m < p.M)
+              *reinterpret_cast<uint32_t*>(y + (size_t)m * p.F) =
+                  odd ? __byte_perm(got, h[c][q], 0x7632) : __byte_perm(h[c][q], got, 0x5410);
+          }
+        }
     }
   }
 
