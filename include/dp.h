@@ -705,6 +705,12 @@ DP_API void dp_adamw_destroy(dp_adamw_t* o);
  * F_shard % 16 == 0, 16-byte aligned buffers; y overlaps no operand.  The
  * summation order over d follows from the sizes; under a CTA limit the result
  * is the same.  D == 0 writes zeros.
+ *
+ * dp_allgather_linear_mx4: the same with x [M, D] of x_dtype, rows ld elements
+ * apart, quantised on the way (dp_mx4_quantize with tensor scale x_scale) into
+ * workspace: device memory of dp_allgather_linear_mx4_workspace_size(M, D)
+ * bytes, 16-byte aligned, any contents, overlapping nothing else; free again
+ * in stream order.  All arguments are checked before anything is enqueued.
  * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA;
  * DP_ERR_TIMEOUT later from dp_get_device_error if a pipeline wait expired.
  */
@@ -728,6 +734,14 @@ DP_API dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D,
                                            const dp_mx4_t* w_shards, int K, int F_shard,
                                            dp_mx4_format_t format, void* y, dp_dtype_t y_dtype,
                                            dp_stream_t stream);
+DP_API dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long long ld,
+                                           dp_dtype_t x_dtype, const float* x_scale,
+                                           const dp_mx4_t* w_shards, int K, int F_shard,
+                                           dp_mx4_format_t format, void* y, dp_dtype_t y_dtype,
+                                           void* workspace, size_t workspace_bytes,
+                                           dp_stream_t stream);
+DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_format_t format,
+                                                          size_t* bytes);
 
 /*
  * The parameter all-gather on the GPU's copy engines instead of its SMs

@@ -61,6 +61,8 @@ class DpError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load libdp_gb300.so (built in-tree by ``build.py``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -125,6 +127,10 @@ def load() -> ctypes.CDLL:
             "dp_mx4_dequantize": [vp, vp, i32, i32, i32, vp, vp, i32, vp],
             "dp_allgather_matmul_mx4": [ctypes.POINTER(Mx4), i32, i32, ctypes.POINTER(Mx4), i32,
                                         i32, i32, vp, i32, vp],
+            "dp_allgather_linear_mx4": [vp, i32, i32, ctypes.c_longlong, i32, vp,
+                                        ctypes.POINTER(Mx4), i32, i32, i32, vp, i32, vp, sz, vp],
+            "dp_allgather_linear_mx4_workspace_size": [i32, i32, i32,
+                                                       ctypes.POINTER(ctypes.c_size_t)],
             "dp_adamw_create": [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32,
                                 ctypes.POINTER(ctypes.c_void_p)],
             "dp_adamw_step": [vp, ctypes.c_double, ctypes.c_double, ctypes.c_double,
@@ -168,15 +174,19 @@ def _parray(items) -> ctypes.Array:
 
 
 _raw_stream = None  # torch's current-stream query without building a Stream object
+_current_device = None  # ... and its current-device query, set with it
 
 
 def _stream(stream) -> int | None:
-    global _raw_stream
+    global _raw_stream, _current_device
     if stream is None:
+        if _raw_stream:
+            return _raw_stream(_current_device())
         import torch
         if not torch.cuda.is_available():
             return None  # nothing can be launched; host-only validation paths
         if _raw_stream is None:
+            _current_device = torch.cuda.current_device
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
         if _raw_stream:
             return _raw_stream(torch.cuda.current_device())
@@ -568,10 +578,11 @@ def dp_mx4_dequantize(codes, scales, rows, cols, fmt, tensor_scale, out, out_dty
 
 
 def _mx4_array(items):
-    """``items``: (codes, scales, tensor_scale) triples, or a kept ctypes array."""
+    """``items``: Mx4 structures, (codes, scales, tensor_scale) triples, or a ctypes array."""
     if isinstance(items, ctypes.Array):
         return items
-    return (Mx4 * max(1, len(items)))(*[Mx4(*[_ptr(v) for v in t]) for t in items])
+    return (Mx4 * max(1, len(items)))(*[t if type(t) is Mx4 else Mx4(*[_ptr(v) for v in t])
+                                        for t in items])
 
 
 def dp_allgather_matmul_mx4(x, M, D, w_shards, K, F_shard, fmt, y, y_dtype, stream=None,
@@ -580,6 +591,22 @@ def dp_allgather_matmul_mx4(x, M, D, w_shards, K, F_shard, fmt, y, y_dtype, stre
     st = load().dp_allgather_matmul_mx4(_mx4_array([x]), M, D, _mx4_array(w_shards), K, F_shard,
                                         fmt, _ptr(y), dtype_code(y_dtype), _stream(stream))
     return _ret(st, "dp_allgather_matmul_mx4", check)
+
+
+def dp_allgather_linear_mx4(x, M, D, ld, x_dtype, x_scale, w_shards, K, F_shard, fmt, y, y_dtype,
+                            workspace, workspace_bytes=None, stream=None, check=True) -> int:
+    wp, wb = _ws(workspace, workspace_bytes)
+    st = load().dp_allgather_linear_mx4(_ptr(x), M, D, ld, dtype_code(x_dtype), _ptr(x_scale),
+                                        _mx4_array(w_shards), K, F_shard, fmt, _ptr(y),
+                                        dtype_code(y_dtype), wp, wb, _stream(stream))
+    return _ret(st, "dp_allgather_linear_mx4", check)
+
+
+def dp_allgather_linear_mx4_workspace_size(M, D, fmt) -> int:
+    b = ctypes.c_size_t(0)
+    _ret(load().dp_allgather_linear_mx4_workspace_size(M, D, fmt, ctypes.byref(b)),
+         "dp_allgather_linear_mx4_workspace_size", True)
+    return int(b.value)
 
 
 def dp_all_gather_copy_engine(shards, K, shard_elems, dtype, out, stream=None,

@@ -560,11 +560,15 @@ bool clash(const Span& a, const Span& b) {
 
 }  // namespace
 
-extern "C" dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D,
-                                               const dp_mx4_t* w_shards, int K, int F_shard,
-                                               dp_mx4_format_t format, void* y,
-                                               dp_dtype_t y_dtype, dp_stream_t stream) {
-  dph::NvtxRange nvtx_range("dp_allgather_matmul_mx4");
+namespace {
+
+// The product's checks and launch parameters; nothing is enqueued.  *tiles is
+// 0 where there is nothing to multiply (then *zero_bytes of y are to be zeroed).
+dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, int K, int F_shard,
+                    dp_mx4_format_t format, void* y, dp_dtype_t y_dtype, dph::DeviceInfo* devp,
+                    Mx4mmParams* pp, int* tilesp, size_t* zero_bytes) {
+  *tilesp = 0;
+  *zero_bytes = 0;
   if (!x || !w_shards || K < 1 || K > DP_MAX_K) return DP_ERR_INVALID_ARG;
   if (M < 0 || D < 0 || F_shard < 0) return DP_ERR_INVALID_ARG;
   if (format != DP_MXFP4 && format != DP_NVFP4) return DP_ERR_UNSUPPORTED;
@@ -595,14 +599,16 @@ extern "C" dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D,
   for (int k = 0; k < K && st == DP_OK; ++k) st = check(w_shards[k], F_shard);
   if (st != DP_OK) return st;
   if (M == 0 || F == 0) return DP_OK;
-  dph::DeviceInfo dev;
+  dph::DeviceInfo& dev = *devp;
   if (!dph::current_device(&dev)) return DP_ERR_CUDA;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 0) return cudaMemsetAsync(y, 0, ysz, s) == cudaSuccess ? DP_OK : DP_ERR_CUDA;
+  if (D == 0) {
+    *zero_bytes = ysz;
+    return DP_OK;
+  }
   if (dev.cc_major != 10 || dev.cc_minor != 3 || dev.smem_optin < kSmemBytes)
     return DP_ERR_UNSUPPORTED;
 
-  Mx4mmParams p;
+  Mx4mmParams& p = *pp;
   memset(&p, 0, sizeof p);
   p.M = M;
   p.D = D;
@@ -638,7 +644,91 @@ extern "C" dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D,
     p.sw[k] = static_cast<const uint8_t*>(w_shards[k].scales);
     p.tw[k] = w_shards[k].tensor_scale;
   }
-  const cudaError_t e = mx ? launch_mx4mm<true>(p, tiles, dev, s)
+  *tilesp = tiles;
+  return DP_OK;
+}
+
+dp_status_t enqueue(const Mx4mmParams& p, int tiles, size_t zero_bytes, dp_mx4_format_t format,
+                    const dph::DeviceInfo& dev, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (zero_bytes)
+    e = cudaMemsetAsync(p.y, 0, zero_bytes, s);
+  else if (tiles)
+    e = format == DP_MXFP4 ? launch_mx4mm<true>(p, tiles, dev, s)
                            : launch_mx4mm<false>(p, tiles, dev, s);
   return e == cudaSuccess ? DP_OK : DP_ERR_CUDA;
 }
+
+// The scratch of the call that quantises x: its codes, then its scales.
+size_t codes_bytes(int M, int D) { return ((size_t)M * (D / 2) + 255) / 256 * 256; }
+
+}  // namespace
+
+extern "C" {
+
+dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards,
+                                    int K, int F_shard, dp_mx4_format_t format, void* y,
+                                    dp_dtype_t y_dtype, dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_allgather_matmul_mx4");
+  dph::DeviceInfo dev;
+  Mx4mmParams p;
+  int tiles;
+  size_t zero;
+  const dp_status_t st =
+      prepare(x, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
+  if (st != DP_OK) return st;
+  p.y = y;
+  return enqueue(p, tiles, zero, format, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_format_t format,
+                                                   size_t* bytes) {
+  if (!bytes) return DP_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (M < 0 || D < 0) return DP_ERR_INVALID_ARG;
+  size_t scales = 0;
+  const dp_status_t st = dp_mx4_scales_size(M, D, format, &scales);
+  if (st != DP_OK) return st;
+  *bytes = codes_bytes(M, D) + scales;
+  return DP_OK;
+}
+
+dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long long ld, dp_dtype_t x_dtype,
+                                    const float* x_scale, const dp_mx4_t* w_shards, int K,
+                                    int F_shard, dp_mx4_format_t format, void* y,
+                                    dp_dtype_t y_dtype, void* workspace, size_t workspace_bytes,
+                                    dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_allgather_linear_mx4");
+  size_t need = 0;
+  dp_status_t st = dp_allgather_linear_mx4_workspace_size(M, D, format, &need);
+  if (st != DP_OK) return st;
+  if (workspace_bytes < need || (!workspace && need)) return DP_ERR_INVALID_ARG;
+  const dp_mx4_t q{workspace, static_cast<uint8_t*>(workspace) + codes_bytes(M, D), x_scale};
+  dph::DeviceInfo dev;
+  Mx4mmParams p;
+  int tiles;
+  size_t zero;
+  // everything is checked before the first launch; the workspace, written by
+  // the quantisation, must leave the weights alone too
+  st = prepare(&q, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
+  if (st != DP_OK) return st;
+  const Span ws = span_of(workspace, need);
+  size_t sbytes = 0;
+  dp_mx4_scales_size(F_shard, D, format, &sbytes);
+  for (int k = 0; k < K; ++k)
+    if (clash(ws, span_of(w_shards[k].codes, (size_t)F_shard * (D / 2))) ||
+        clash(ws, span_of(w_shards[k].scales, sbytes)) ||
+        (w_shards[k].tensor_scale && clash(ws, span_of(w_shards[k].tensor_scale, 4))))
+      return DP_ERR_ALIAS;
+  if (M > 0 && D > 0 && x &&
+      clash(span_of(x, ((size_t)(M - 1) * (size_t)(ld > 0 ? ld : 0) + D) * (x_dtype == DP_FP32 ? 4 : 2)),
+            span_of(y, (size_t)M * K * F_shard * (y_dtype == DP_FP32 ? 4 : 2))))
+    return DP_ERR_ALIAS;
+  st = dp_mx4_quantize(&x, 1, M, D, ld, x_dtype, format, 0, x_scale, workspace,
+                       const_cast<void*>(q.scales), stream);
+  if (st != DP_OK) return st;
+  p.y = y;
+  return enqueue(p, tiles, zero, format, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

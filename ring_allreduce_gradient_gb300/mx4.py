@@ -12,15 +12,13 @@ No arithmetic happens here: it allocates with PyTorch and calls the binding.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
-from typing import Optional
-
 import torch
 
 from . import binding as B
 from .collectives import _DT, _code
 
 FORMATS = {"mxfp4": B.DP_MXFP4, "nvfp4": B.DP_NVFP4}
+_BLOCK = {"mxfp4": 32, "nvfp4": 16}
 
 
 def _format(name) -> int:
@@ -29,38 +27,61 @@ def _format(name) -> int:
     return FORMATS[name]
 
 
-@dataclass
+def _scale_bytes(rows: int, cols: int, format: str) -> int:
+    """dp_mx4_scales_size."""
+    return -(-rows // 128) * -(-cols // (4 * _BLOCK[format])) * 512
+
+
 class Mx4Tensor:
-    """A [rows, cols] matrix in 4 bits (layout: ``include/dp.h``).
+    """A [rows, cols] matrix in 4 bits (layout: ``include/dp.h``), read-only
+    once made: it keeps its buffers and their addresses for the calls.
 
     ``codes``: uint8, rows x cols/2 bytes; ``scales``: uint8 tiles;
     ``tensor_scale``: one fp32 device value or None (nvfp4 only).
     """
 
-    codes: torch.Tensor
-    scales: torch.Tensor
-    rows: int
-    cols: int
-    format: str
-    tensor_scale: Optional[torch.Tensor] = None
+    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_format", "_tensor_scale", "_c")
 
-    def __post_init__(self):
-        need = B.dp_mx4_scales_size(self.rows, self.cols, _format(self.format))
-        for name, t, n in (("codes", self.codes, self.rows * (self.cols // 2)),
-                           ("scales", self.scales, need)):
+    def __init__(self, codes, scales, rows: int, cols: int, format: str, tensor_scale=None):
+        _format(format)
+        for name, t, n in (("codes", codes, rows * (cols // 2)),
+                           ("scales", scales, _scale_bytes(rows, cols, format))):
             if t.dtype != torch.uint8 or t.numel() != n or not t.is_contiguous():
-                raise ValueError(f"{name}: {n} contiguous bytes for a {self.format} matrix of "
-                                 f"{self.rows} x {self.cols}")
-        _check_scale(self.tensor_scale, self.codes.device)
+                raise ValueError(f"{name}: {n} contiguous bytes for a {format} matrix of "
+                                 f"{rows} x {cols}")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales on one device")
+        _check_scale(tensor_scale, codes.device)
+        self._set(codes, scales, rows, cols, format, tensor_scale)
 
-    def _triple(self):
-        return (self.codes, self.scales, self.tensor_scale)
+    def _set(self, codes, scales, rows, cols, format, tensor_scale):
+        self._codes, self._scales, self._tensor_scale = codes, scales, tensor_scale
+        self._rows, self._cols, self._format = rows, cols, format
+        self._c = B.Mx4(codes.data_ptr(), scales.data_ptr(),
+                        None if tensor_scale is None else tensor_scale.data_ptr())
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    format = property(lambda self: self._format)
+    tensor_scale = property(lambda self: self._tensor_scale)
+
+    def __repr__(self):
+        return f"Mx4Tensor({self._rows} x {self._cols}, {self._format})"
 
 
 def _check_scale(scale, device):
     if scale is not None and (scale.dtype != torch.float32 or scale.numel() != 1 or
                               scale.device != device):
         raise ValueError(f"tensor_scale: one fp32 value on {device}")
+
+
+def _on(stream, device):
+    """A context in which allocations, fills and calls belong to ``stream``."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
 
 
 def tensor_scale(x, out=None, stream=None) -> torch.Tensor:
@@ -71,21 +92,14 @@ def tensor_scale(x, out=None, stream=None) -> torch.Tensor:
                      not t.is_contiguous() for t in xs):
         raise ValueError("need contiguous tensors of one dtype and device")
     dev = xs[0].device
+    if stream is not None:
+        with _on(stream, dev):
+            return tensor_scale(xs, out)
     out = torch.empty(1, dtype=torch.float32, device=dev) if out is None else out
     _check_scale(out, dev)
-    with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else _same():
-        ws = torch.zeros(B.dp_grad_norm_workspace_size(len(xs)), dtype=torch.uint8, device=dev)
-    B.dp_mx4_tensor_scale(xs, [t.numel() for t in xs], len(xs), _code(xs[0]), out, ws,
-                          stream=stream)
+    ws = torch.zeros(B.dp_grad_norm_workspace_size(len(xs)), dtype=torch.uint8, device=dev)
+    B.dp_mx4_tensor_scale(xs, [t.numel() for t in xs], len(xs), _code(xs[0]), out, ws)
     return out
-
-
-class _same:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *a):
-        return False
 
 
 def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = False,
@@ -98,6 +112,9 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
     xs = [x] if isinstance(x, torch.Tensor) else list(x)
     if not xs:
         raise ValueError("need at least one shard")
+    if stream is not None:
+        with _on(stream, xs[0].device):
+            return quantize(xs, format, tensor_scale, transpose)
     x0 = xs[0]
     for t in xs:
         if t.dim() != 2 or t.shape != x0.shape or t.dtype != x0.dtype or t.device != x0.device \
@@ -105,45 +122,81 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
             raise ValueError("need matrices of one shape, dtype, device and row stride, with unit "
                              "stride along the rows")
     rows, cols = x0.shape
-    ld = x0.stride(0) if rows > 1 else cols
     _check_scale(tensor_scale, x0.device)
     K = len(xs)
     R, L = (cols, K * rows) if transpose else (K * rows, cols)
     codes = torch.empty(R, L // 2, dtype=torch.uint8, device=x0.device)
-    scales = torch.empty(B.dp_mx4_scales_size(R, L, fmt), dtype=torch.uint8, device=x0.device)
-    B.dp_mx4_quantize(xs, K, rows, cols, max(ld, cols), _code(x0), fmt, transpose, tensor_scale,
-                      codes, scales, stream)
-    return Mx4Tensor(codes, scales, R, L, format, tensor_scale)
+    scales = torch.empty(_scale_bytes(R, L, format), dtype=torch.uint8, device=x0.device)
+    B.dp_mx4_quantize(xs, K, rows, cols, _row_stride(x0), _code(x0), fmt, transpose, tensor_scale,
+                      codes, scales)
+    q = Mx4Tensor.__new__(Mx4Tensor)
+    q._set(codes, scales, R, L, format, tensor_scale)
+    return q
+
+
+def _row_stride(x) -> int:
+    return max(x.stride(0), x.shape[1]) if x.shape[0] > 1 else x.shape[1]
 
 
 def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values a 4-bit matrix stands for."""
-    out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.codes.device)
-    B.dp_mx4_dequantize(q.codes, q.scales, q.rows, q.cols, _format(q.format), q.tensor_scale, out,
-                        _code(out), stream)
+    if stream is not None:
+        with _on(stream, q._codes.device):
+            return dequantize(q, dtype)
+    out = torch.empty(q._rows, q._cols, dtype=dtype, device=q._codes.device)
+    B.dp_mx4_dequantize(q._codes, q._scales, q._rows, q._cols, FORMATS[q._format],
+                        q._tensor_scale, out, _code(out))
     return out
+
+
+def _shards(w_shards, cols, format, device):
+    """The shards' structures, after checking that they make one matrix for this operand."""
+    w0 = w_shards[0]
+    rows = w0._rows
+    if w0._cols != cols or w0._format != format:
+        raise ValueError(f"x is {format} with {cols} columns, the shards {w0._format} with "
+                         f"{w0._cols}")
+    for w in w_shards:
+        if w._rows != rows or w._cols != cols or w._format != format or \
+                w._codes.device != device:
+            raise ValueError("need shards of one shape, format and device")
+    return (B.Mx4 * len(w_shards))(*[w._c for w in w_shards])
 
 
 def matmul(x: Mx4Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = x . w^T with w the row concatenation of the 4-bit shards."""
-    w0 = w_shards[0]
-    for w in w_shards:
-        if (w.rows, w.cols, w.format) != (w0.rows, w0.cols, w0.format) or \
-                w.codes.device != x.codes.device:
-            raise ValueError("need shards of one shape, format and device")
-    if w0.cols != x.cols or w0.format != x.format:
-        raise ValueError(f"x is {x.format} with {x.cols} columns, the shards {w0.format} "
-                         f"with {w0.cols}")
+    if stream is not None:
+        with _on(stream, x._codes.device):
+            return matmul(x, w_shards, y_dtype)
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
-    y = torch.empty(x.rows, len(w_shards) * w0.rows, dtype=y_dtype, device=x.codes.device)
-    B.dp_allgather_matmul_mx4(x._triple(), x.rows, x.cols, [w._triple() for w in w_shards],
-                              len(w_shards), w0.rows, _format(x.format), y, _DT[y_dtype], stream)
+    dev, K = x._codes.device, len(w_shards)
+    arr = _shards(w_shards, x._cols, x._format, dev)
+    y = torch.empty(x._rows, K * w_shards[0]._rows, dtype=y_dtype, device=dev)
+    B.dp_allgather_matmul_mx4(x._c, x._rows, x._cols, arr, K, w_shards[0]._rows,
+                              FORMATS[x._format], y, _DT[y_dtype])
     return y
 
 
 def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
            stream=None) -> torch.Tensor:
-    """y = x . w^T with x [M, D] quantised to the shards' format on the way."""
-    return matmul(quantize(x, w_shards[0].format, x_scale, stream=stream), w_shards, y_dtype,
-                  stream)
+    """y = x . w^T with x [M, D] quantised to the shards' format on the way
+    (``x_scale``: its nvfp4 tensor scale), in one call."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return linear(x, w_shards, x_scale, y_dtype)
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x: a matrix with unit stride along its rows")
+    if y_dtype not in _DT:
+        raise TypeError(f"unsupported dtype {y_dtype}")
+    M, D = x.shape
+    dev, K, w0 = x.device, len(w_shards), w_shards[0]
+    arr = _shards(w_shards, D, w0._format, dev)
+    _check_scale(x_scale, dev)
+    # scratch of this call alone: the allocator hands it on in stream order
+    ws = torch.empty(-(-M * (D // 2) // 256) * 256 + _scale_bytes(M, D, w0._format),
+                     dtype=torch.uint8, device=dev)
+    y = torch.empty(M, K * w0._rows, dtype=y_dtype, device=dev)
+    B.dp_allgather_linear_mx4(x, M, D, _row_stride(x), _code(x), x_scale, arr, K, w0._rows,
+                              FORMATS[w0._format], y, _DT[y_dtype], ws, ws.numel())
+    return y
