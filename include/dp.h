@@ -616,7 +616,7 @@ DP_API dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes);
  * written may overlap another buffer of the list.
  *
  * dp_adamw_step: step t >= 1, for every element, in fp32 with one rounding
- * per operation:
+ * per operation (the root and the quotient to 2^-22):
  *   g = grad * *grad_scale          (grad_scale NULL: 1)
  *   m = m * beta1 + g * (1 - beta1)
  *   v = v * beta2 + (g * g) * (1 - beta2)
@@ -633,7 +633,7 @@ DP_API dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes);
  * schedule: NULL, or 3 device floats (lr, 1 - beta1^t, 1 - beta2^t) that are
  * read when the kernel runs in place of the call's values: a captured step
  * is replayed with new ones.
- * Requires 0 <= beta < 1, eps > 0, finite lr.  Steps of one object are
+ * Requires 0 <= beta < 1, eps >= 2^-126, finite lr.  Steps of one object are
  * serialised on the host; the caller orders them on the GPU.
  * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
  */

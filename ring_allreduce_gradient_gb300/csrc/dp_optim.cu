@@ -7,8 +7,9 @@
 //   m' = b1 m + (1 - b1) g'
 //   v' = b2 v + (1 - b2) g'^2
 //   p' = p (1 - lr wd) - lr / (1 - b1^t) * m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
-// in fp32, one rounding per operation (no contraction), with the factors that
-// depend on t alone formed in double on the host.
+// in fp32, one rounding per operation (no contraction), the root and the
+// quotient to 2^-22; the factors that depend on t alone formed in double on the
+// host.
 //
 // 8-bit states: m and r = sqrt(v) are e4m3 codes with one fp32 scale for each
 // 256 consecutive elements, the block's largest magnitude at e4m3's largest
@@ -29,6 +30,7 @@
 #include "dp_launch.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -39,8 +41,10 @@ namespace {
 
 using namespace dpk;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;      // AdamW
 constexpr int kWarps = kThreads / 32;
+constexpr int kNormThreads = 256;
+constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kUnit = 256;         // elements a warp takes at once = an 8-bit block
 constexpr int kNormUnit = 1024;    // the norm's: four loads in flight per lane
 constexpr int kNormSlots = 608;    // partial sums of one norm launch: four CTAs on each of 152 SMs
@@ -104,19 +108,24 @@ __device__ __forceinline__ void put(uint16_t* p, float v) { *p = bf16_rn(v); }
 
 // ---- AdamW -------------------------------------------------------------------
 
+// One tensor of a list; what a warp needs of it lies together.
+struct alignas(16) AdamwTensor {
+  void* param;
+  const void* grad;
+  uint16_t* copy;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  unsigned long long numel;
+  double decay;
+  int vec_ok;
+};
+
 template <int CAP>
 struct AdamwParams {
-  void* param[CAP];
-  const void* grad[CAP];
-  uint16_t* copy[CAP];
-  void* m[CAP];
-  void* v[CAP];
-  float* m_scale[CAP];
-  float* v_scale[CAP];
-  unsigned long long numel[CAP];
+  AdamwTensor tensor[CAP];
   unsigned ustart[CAP + 1];  // prefix sums of units (kUnit elements) per tensor
-  double decay[CAP];
-  uint8_t vec_ok[CAP];
   int n;
   double lr;
   float beta1, omb1, beta2, omb2, eps, step_size, inv_root;
@@ -128,15 +137,33 @@ struct Hyper {
   float coef, beta1, omb1, beta2, omb2, eps, step_size, inv_root;
 };
 
+// Root and quotient to 2^-22 of the step, which is itself far below the
+// parameter: the correctly rounded forms take about 20 instructions each and
+// a call for every zero (parameters that have had no gradient yet), which
+// bound the kernel: eight 8 Mi shards with 8-bit states took 204 us with them,
+// and 293 us where the gradients are zero.  A v below the normal range counts
+// as 0 in the root (1e-19, against eps); the divisor is at least eps, which is
+// in it.
+__device__ __forceinline__ float root_of(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float quotient(float a, float b) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
+  return __fmul_rn(a, r);
+}
+
 // One element: the new m, v and root of v, and the parameter's step.
 __device__ __forceinline__ float adamw_one(float p, float g, float& m, float& v, float& root,
                                            float keep, const Hyper& h) {
   g = __fmul_rn(g, h.coef);
   m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.omb1));
   v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, g), h.omb2));
-  root = __fsqrt_rn(v);
+  root = root_of(v);
   const float denom = __fadd_rn(__fmul_rn(root, h.inv_root), h.eps);
-  return __fsub_rn(__fmul_rn(p, keep), __fmul_rn(h.step_size, __fdiv_rn(m, denom)));
+  return __fsub_rn(__fmul_rn(p, keep), __fmul_rn(h.step_size, quotient(m, denom)));
 }
 
 // A block's largest magnitude over the warp.  Magnitudes order as their bit
@@ -152,13 +179,18 @@ __device__ __forceinline__ float code_factor(float top) {
   return top > kTiny ? __fmul_rn(__frcp_rn(top), kE4m3Max) : (top <= kTiny ? 0.0f : top);
 }
 
+// CTAs on an SM: eight of four warps for fp32 parameters (64 registers, which
+// spills nothing on the aligned path; eight 8 Mi shards with 8-bit states 173
+// us, against 179 us at the 80 registers it would take), six for bf16 ones,
+// whose lane-by-lane path would spill at 64 (ragged bf16 list 109 us, against
+// 118 us).
+template <typename PT>
+constexpr int kAdamwCtas = sizeof(PT) == 4 ? 8 : 6;
+
 template <typename PT, typename GT, bool S8, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
+__global__ void __launch_bounds__(kThreads, kAdamwCtas<PT>) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
   const int lane = threadIdx.x & 31;
   const unsigned units = a.ustart[a.n];
-  const unsigned stride = gridDim.x * kWarps;
-  unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= units) return;
   Hyper h{1.0f, a.beta1, a.omb1, a.beta2, a.omb2, a.eps, a.step_size, a.inv_root};
   double lr = a.lr;
   if (a.grad_scale) h.coef = __ldg(a.grad_scale);
@@ -167,30 +199,30 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     h.step_size = (float)(lr / (double)__ldg(a.schedule + 1));
     h.inv_root = (float)(1.0 / sqrt((double)__ldg(a.schedule + 2)));
   }
-  // the tensor of the first unit: the last t with ustart[t] <= u
-  int t = 0;
-  for (int hi = a.n - 1; t < hi;) {
-    const int mid = (t + hi + 1) >> 1;
-    if (a.ustart[mid] <= u) t = mid;
-    else hi = mid - 1;
-  }
-  for (; u < units; u += stride) {
-    while (a.ustart[t + 1] <= u) ++t;
+  for (unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
+    // the unit's tensor: the last t with ustart[t] <= u
+    int t = 0;
+    for (int hi = a.n - 1; t < hi;) {
+      const int mid = (t + hi + 1) >> 1;
+      if (a.ustart[mid] <= u) t = mid;
+      else hi = mid - 1;
+    }
+    const AdamwTensor& x = a.tensor[t];
     const unsigned b = u - a.ustart[t];  // block of this tensor
     const unsigned long long e0 = (unsigned long long)b * kUnit;
-    const unsigned long long left = a.numel[t] - e0;
-    PT* pp = static_cast<PT*>(a.param[t]) + e0;
-    const GT* gp = static_cast<const GT*>(a.grad[t]) + e0;
-    uint16_t* cp = a.copy[t] ? a.copy[t] + e0 : nullptr;
-    const bool vec = a.vec_ok[t] && left >= kUnit;
+    const unsigned long long left = x.numel - e0;
+    PT* pp = static_cast<PT*>(x.param) + e0;
+    const GT* gp = static_cast<const GT*>(x.grad) + e0;
+    uint16_t* cp = x.copy ? x.copy + e0 : nullptr;
+    const bool vec = x.vec_ok && left >= kUnit;
     const int len = left < kUnit ? (int)left : kUnit;
     float p[8], g[8], m[8], v[8], root[8];
     uint32_t mc[2], rc[2];
     float ms = 0.0f, rs = 0.0f;
-    float* mp = static_cast<float*>(a.m[t]) + (S8 ? 0 : e0);
-    float* vp = static_cast<float*>(a.v[t]) + (S8 ? 0 : e0);
-    uint8_t* m8 = static_cast<uint8_t*>(a.m[t]) + e0;
-    uint8_t* r8 = static_cast<uint8_t*>(a.v[t]) + e0;
+    float* mp = static_cast<float*>(x.m) + (S8 ? 0 : e0);
+    float* vp = static_cast<float*>(x.v) + (S8 ? 0 : e0);
+    uint8_t* m8 = static_cast<uint8_t*>(x.m) + e0;
+    uint8_t* r8 = static_cast<uint8_t*>(x.v) + e0;
     if (vec) {
       const int o = lane * 8;
       ld8(pp + o, p);
@@ -198,8 +230,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       if constexpr (S8) {
         ld8_codes(m8 + o, mc);
         ld8_codes(r8 + o, rc);
-        ms = a.m_scale[t][b];
-        rs = a.v_scale[t][b];
+        ms = x.m_scale[b];
+        rs = x.v_scale[b];
         widen_codes(mc, m);
         widen_codes(rc, v);
       } else {
@@ -223,12 +255,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         }
       }
       if constexpr (S8) {
-        ms = a.m_scale[t][b];
-        rs = a.v_scale[t][b];
+        ms = x.m_scale[b];
+        rs = x.v_scale[b];
       }
     }
     if (h.coef != h.coef) return;  // the norm was not finite: nothing is changed
-    const float keep = (float)(1.0 - lr * a.decay[t]);
+    const float keep = (float)(1.0 - lr * x.decay);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (S8) {
@@ -253,8 +285,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         if (v[i] > 0.0f && root[i] < kE4m3Min) root[i] = kE4m3Min;
       }
       if (lane == 0) {
-        a.m_scale[t][b] = __fmul_rn(mt, 1.0f / kE4m3Max);
-        a.v_scale[t][b] = __fmul_rn(rt, 1.0f / kE4m3Max);
+        x.m_scale[b] = __fmul_rn(mt, 1.0f / kE4m3Max);
+        x.v_scale[b] = __fmul_rn(rt, 1.0f / kE4m3Max);
       }
     }
     if (vec) {
@@ -291,16 +323,21 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 
 template <typename KernelT>
 int resident_blocks(KernelT kernel, const dph::DeviceInfo& dev) {
-  const int b = dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kThreads, 0, dev.device);
+  const int b = dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kNormThreads, 0, dev.device);
   long long r = (long long)dev.sm_count * (b < 1 ? 1 : b);
   const int limit = dph::stream_cta_limit();
   if (limit > 0 && r > limit) r = limit;
   return (int)r;
 }
 
-int blocks_for(unsigned units, int resident) {
-  const long long want = ((long long)units + kWarps - 1) / kWarps;
-  return (int)std::max(1LL, std::min<long long>(want, resident));
+// A warp for each unit: the hardware hands out CTAs as SMs become free, which
+// the two dies do at different rates (GPT-2-small-shaped step, fp32 states: 524
+// us, against 590 with a resident grid over the units).  Under a CTA limit the
+// CTAs go over the units.
+unsigned blocks_for(unsigned units) {
+  const unsigned want = (units - 1) / kWarps + 1;
+  const int limit = dph::stream_cta_limit();
+  return limit > 0 ? std::min(want, (unsigned)limit) : want;
 }
 
 // ---- the global norm -----------------------------------------------------------
@@ -353,13 +390,13 @@ __device__ __forceinline__ double warp_joined(double v) {
 // partial sums in order: the result depends neither on the grid nor on the
 // order in which CTAs finish.
 template <typename GT, int OP, int CAP>
-__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ NormParams<CAP> a) {
-  __shared__ double sums[kWarps];
+__global__ void __launch_bounds__(kNormThreads, 4) norm_kernel(const __grid_constant__ NormParams<CAP> a) {
+  __shared__ double sums[kNormWarps];
   __shared__ bool is_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned units = a.ustart[a.n];
   for (int s = blockIdx.x; s < a.slots; s += gridDim.x) {
-    unsigned u = (unsigned)s * kWarps + warp;
+    unsigned u = (unsigned)s * kNormWarps + warp;
     double sum = 0.0;
     int t = 0;
     for (int hi = a.n - 1; t < hi;) {
@@ -367,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
       if (a.ustart[mid] <= u) t = mid;
       else hi = mid - 1;
     }
-    for (; u < units; u += (unsigned)a.slots * kWarps) {
+    for (; u < units; u += (unsigned)a.slots * kNormWarps) {
       while (a.ustart[t + 1] <= u) ++t;
       const unsigned long long e0 = (unsigned long long)(u - a.ustart[t]) * kNormUnit;
       const unsigned long long left = a.numel[t] - e0;
@@ -403,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
     __syncthreads();
     if (threadIdx.x == 0) {
       double all = 0.0;
-      for (int w = 0; w < kWarps; ++w) all = joined<OP>(all, sums[w]);
+      for (int w = 0; w < kNormWarps; ++w) all = joined<OP>(all, sums[w]);
       a.part[a.slots_before + s] = all;
     }
     __syncthreads();
@@ -418,13 +455,13 @@ __global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant
   __threadfence();
   const int total = a.slots_before + a.slots;
   double sum = 0.0;
-  for (int i = threadIdx.x; i < total; i += kThreads) sum = joined<OP>(sum, __ldcg(a.part + i));
+  for (int i = threadIdx.x; i < total; i += kNormThreads) sum = joined<OP>(sum, __ldcg(a.part + i));
   sum = warp_joined<OP>(sum);
   if (lane == 0) sums[warp] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     double all = 0.0;
-    for (int w = 0; w < kWarps; ++w) all = joined<OP>(all, sums[w]);
+    for (int w = 0; w < kNormWarps; ++w) all = joined<OP>(all, sums[w]);
     if constexpr (OP == kMaxAbs) {
       *a.norm = __fmul_rn(__uint_as_float((uint32_t)all), kTopFp4);
       return;
@@ -479,7 +516,7 @@ cudaError_t norm_launch(const void* const* grads, const size_t* numels, const st
   }
   p.n = (int)count;
   p.ustart[count] = units;
-  *slots = (int)std::min<unsigned>(kNormSlots, std::max(1u, (units + kWarps - 1) / kWarps));
+  *slots = (int)std::min<unsigned>(kNormSlots, std::max(1u, (units + kNormWarps - 1) / kNormWarps));
   p.slots = *slots;
   p.slots_before = slots_before;
   p.last = last;
@@ -489,7 +526,7 @@ cudaError_t norm_launch(const void* const* grads, const size_t* numels, const st
   p.norm = norm;
   p.coef = coef;
   const int grid = std::min(*slots, resident_blocks(norm_kernel<GT, OP, CAP>, dev));
-  norm_kernel<GT, OP, CAP><<<grid, kThreads, 0, s>>>(p);
+  norm_kernel<GT, OP, CAP><<<grid, kNormThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -500,7 +537,7 @@ constexpr size_t kNormHead = 256;  // the ticket, ahead of the partial sums
 // ---- the AdamW object ----------------------------------------------------------
 
 struct dp_adamw {
-  static constexpr int kCap = 384;      // tensors per launch (30 KB of kernel parameters)
+  static constexpr int kCap = 384;      // tensors per launch (32 KB of kernel parameters)
   static constexpr int kCapSmall = 32;  // short lists: less to pass with each launch
   dp_dtype_t param_dtype, grad_dtype;
   dp_state_t state;
@@ -511,27 +548,16 @@ struct dp_adamw {
 namespace {
 
 template <typename PT, typename GT, bool S8>
-cudaError_t adamw_launch(const AdamwParams<dp_adamw::kCap>& table, const dph::DeviceInfo& dev,
-                         cudaStream_t s) {
+cudaError_t adamw_launch(const AdamwParams<dp_adamw::kCap>& table, cudaStream_t s) {
   const unsigned units = table.ustart[table.n];
   if (table.n > dp_adamw::kCapSmall) {
-    auto k = adamw_kernel<PT, GT, S8, dp_adamw::kCap>;
-    k<<<blocks_for(units, resident_blocks(k, dev)), kThreads, 0, s>>>(table);
+    adamw_kernel<PT, GT, S8, dp_adamw::kCap><<<blocks_for(units), kThreads, 0, s>>>(table);
     return cudaGetLastError();
   }
   AdamwParams<dp_adamw::kCapSmall> p;
   const size_t n = (size_t)table.n;
-  memcpy(p.param, table.param, n * 8);
-  memcpy(p.grad, table.grad, n * 8);
-  memcpy(p.copy, table.copy, n * 8);
-  memcpy(p.m, table.m, n * 8);
-  memcpy(p.v, table.v, n * 8);
-  memcpy(p.m_scale, table.m_scale, n * 8);
-  memcpy(p.v_scale, table.v_scale, n * 8);
-  memcpy(p.numel, table.numel, n * 8);
-  memcpy(p.ustart, table.ustart, (n + 1) * 4);
-  memcpy(p.decay, table.decay, n * 8);
-  memcpy(p.vec_ok, table.vec_ok, n);
+  memcpy(p.tensor, table.tensor, n * sizeof(AdamwTensor));
+  memcpy(p.ustart, table.ustart, (n + 1) * sizeof(unsigned));
   p.n = table.n;
   p.lr = table.lr;
   p.beta1 = table.beta1;
@@ -543,25 +569,24 @@ cudaError_t adamw_launch(const AdamwParams<dp_adamw::kCap>& table, const dph::De
   p.inv_root = table.inv_root;
   p.grad_scale = table.grad_scale;
   p.schedule = table.schedule;
-  auto k = adamw_kernel<PT, GT, S8, dp_adamw::kCapSmall>;
-  k<<<blocks_for(units, resident_blocks(k, dev)), kThreads, 0, s>>>(p);
+  adamw_kernel<PT, GT, S8, dp_adamw::kCapSmall><<<blocks_for(units), kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename PT, typename GT>
 cudaError_t adamw_launch_s(const dp_adamw& o, const AdamwParams<dp_adamw::kCap>& table,
-                           const dph::DeviceInfo& dev, cudaStream_t s) {
-  return o.state == DP_STATE_8BIT ? adamw_launch<PT, GT, true>(table, dev, s)
-                                  : adamw_launch<PT, GT, false>(table, dev, s);
+                           cudaStream_t s) {
+  return o.state == DP_STATE_8BIT ? adamw_launch<PT, GT, true>(table, s)
+                                  : adamw_launch<PT, GT, false>(table, s);
 }
 
 cudaError_t adamw_dispatch(const dp_adamw& o, const AdamwParams<dp_adamw::kCap>& table,
-                           const dph::DeviceInfo& dev, cudaStream_t s) {
+                           cudaStream_t s) {
   if (o.param_dtype == DP_FP32)
-    return o.grad_dtype == DP_FP32 ? adamw_launch_s<float, float>(o, table, dev, s)
-                                   : adamw_launch_s<float, uint16_t>(o, table, dev, s);
-  return o.grad_dtype == DP_FP32 ? adamw_launch_s<uint16_t, float>(o, table, dev, s)
-                                 : adamw_launch_s<uint16_t, uint16_t>(o, table, dev, s);
+    return o.grad_dtype == DP_FP32 ? adamw_launch_s<float, float>(o, table, s)
+                                   : adamw_launch_s<float, uint16_t>(o, table, s);
+  return o.grad_dtype == DP_FP32 ? adamw_launch_s<uint16_t, float>(o, table, s)
+                                 : adamw_launch_s<uint16_t, uint16_t>(o, table, s);
 }
 
 // One pass over a list: the checks, and as many launches as the list needs.
@@ -717,18 +742,19 @@ dp_status_t dp_adamw_create(const dp_adamw_tensor_t* tensors, int n, dp_dtype_t 
       }
       auto& p = o->tables.back();
       const int i = p.n++;
-      p.param[i] = x.param;
-      p.grad[i] = x.grad;
-      p.copy[i] = static_cast<uint16_t*>(x.copy);
-      p.m[i] = x.exp_avg;
-      p.v[i] = x.exp_avg_sq;
-      p.m_scale[i] = s8 ? x.exp_avg_scale : nullptr;
-      p.v_scale[i] = s8 ? x.exp_avg_sq_scale : nullptr;
-      p.numel[i] = x.numel;
-      p.decay[i] = x.weight_decay;
+      AdamwTensor& y = p.tensor[i];
+      y.param = x.param;
+      y.grad = x.grad;
+      y.copy = static_cast<uint16_t*>(x.copy);
+      y.m = x.exp_avg;
+      y.v = x.exp_avg_sq;
+      y.m_scale = s8 ? x.exp_avg_scale : nullptr;
+      y.v_scale = s8 ? x.exp_avg_sq_scale : nullptr;
+      y.numel = x.numel;
+      y.decay = x.weight_decay;
       // eight elements of every array from an address that one load or store takes
-      p.vec_ok[i] = aligned(x.param, ps * 8) && aligned(x.grad, gs * 8) && aligned(x.copy, 16) &&
-                    aligned(x.exp_avg, ss * 8) && aligned(x.exp_avg_sq, ss * 8);
+      y.vec_ok = aligned(x.param, ps * 8) && aligned(x.grad, gs * 8) && aligned(x.copy, 16) &&
+                 aligned(x.exp_avg, ss * 8) && aligned(x.exp_avg_sq, ss * 8);
       units += u;
       p.ustart[i + 1] = (unsigned)units;
     }
@@ -753,7 +779,7 @@ dp_status_t dp_adamw_step(dp_adamw_t* o, double lr, double beta1, double beta2, 
   dph::NvtxRange nvtx_range("dp_adamw_step");
   if (!o || step < 1 || !std::isfinite(lr)) return DP_ERR_INVALID_ARG;
   if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return DP_ERR_INVALID_ARG;
-  if (!((float)eps > 0.0f) || std::isinf((float)eps)) return DP_ERR_INVALID_ARG;
+  if (!((float)eps >= FLT_MIN) || std::isinf((float)eps)) return DP_ERR_INVALID_ARG;
   if (!aligned(grad_scale, 4) || !aligned(schedule, 4)) return DP_ERR_UNSUPPORTED;
   if (o->tables.empty()) return DP_OK;
   dph::DeviceInfo dev;
@@ -772,7 +798,7 @@ dp_status_t dp_adamw_step(dp_adamw_t* o, double lr, double beta1, double beta2, 
     table.inv_root = (float)(1.0 / std::sqrt(fix2));
     table.grad_scale = grad_scale;
     table.schedule = schedule;
-    if (adamw_dispatch(*o, table, dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (adamw_dispatch(*o, table, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
       return DP_ERR_CUDA;
   }
   return DP_OK;
