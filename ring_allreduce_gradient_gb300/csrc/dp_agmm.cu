@@ -232,16 +232,6 @@ __device__ __forceinline__ void tma_store_2d_hint(const CUtensorMap* map, const 
       : "memory");
 }
 
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_read0() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
 // Barrier 1 among the 128 epilogue threads; the reduction form makes every
 // one of them take the same branch.
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -851,6 +841,22 @@ bool encode_kmajor_bytes(CUtensorMap* map, const void* base, int rows, int row_b
                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+  });
+}
+
+bool encode_output_shards(CUtensorMap* map, void* base, int M, int K, int F_shard, int box_rows) {
+  if (!get_encoder()) return false;
+  // the shards' number has its place in the key beside the box's height
+  const MapKey key{reinterpret_cast<uintptr_t>(base), M, F_shard, box_rows * 64 + K, 6};
+  return cached_map(map, key, [&](CUtensorMap* m) {
+    cuuint64_t dims[3] = {(cuuint64_t)F_shard, (cuuint64_t)K, (cuuint64_t)M};
+    cuuint64_t strides[2] = {(cuuint64_t)F_shard * 2, (cuuint64_t)K * (cuuint64_t)F_shard * 2};
+    cuuint32_t box[3] = {128, 1, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
   });
 }

@@ -60,9 +60,13 @@ constexpr uint32_t kStageW = BM * BK / 2;
 constexpr uint32_t kStageX = kMaxBN * BK / 2;
 constexpr uint32_t kStageSW = 4 * kScaleTile;      // 128 rows x 16 blocks (nvfp4)
 constexpr uint32_t kStageSX = 2 * 4 * kScaleTile;  // 256 rows
+constexpr int kOutTokens = 16;   // tokens of one staged store of an epilogue half
+constexpr uint32_t kStageY = kOutTokens * BM * 2;  // per half
 constexpr size_t kBarBytes = 256;
-constexpr size_t kSmemBytes =
-    1024 + (size_t)kStages * (kStageW + kStageX + kStageSW + kStageSX) + kBarBytes;
+constexpr size_t kSmemBytes = 1024 +
+                              (size_t)kStages * (kStageW + kStageX + kStageSW + kStageSX) +
+                              2 * kStageY + kBarBytes;
+static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 constexpr int kTmemCols = 512;
 constexpr int kScaleCol0 = kMaxBN;   // first scale column
 constexpr int kScaleCols = 48;       // per stage: 16 for W, 32 for X
@@ -72,7 +76,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kMaxSplit = 8;
 
 struct Mx4mmParams {
-  CUtensorMap tmX;
+  CUtensorMap tmX, tmY;
   CUtensorMap tmW[kMaxK];
   const uint8_t* sx;
   const uint8_t* sw[kMaxK];
@@ -80,7 +84,7 @@ struct Mx4mmParams {
   const float* tw[kMaxK];
   void* y;
   unsigned* err;
-  int M, D, F, F_shard;
+  int M, D, K, F, F_shard;
   int BN;
   int tiles_m, tiles_f;   // tiles_f: of one shard
   int tile0, tiles;       // this launch's tiles
@@ -88,8 +92,25 @@ struct Mx4mmParams {
   int col_tiles;          // scale tiles along d
   int x_row_tiles;
   int split;              // CTAs of a cluster that share a tile
+  int pair;               // CTAs of a cluster that share X: 2, or 1
   int y_f32;
 };
+
+// Tile i of this launch, or of a pair's two the one of CTA `sub`: the last
+// pair of an odd number of weight row tiles has the last one twice, stored by
+// the first CTA alone.
+struct Tile {
+  int shard, f0, m0;
+  bool own;
+};
+__device__ __forceinline__ Tile tile_at(const Mx4mmParams& p, int i, int sub) {
+  const int tile = p.tile0 + i;
+  const int fp = tile / p.tiles_m, mt = tile - fp * p.tiles_m;
+  const int ft = fp * p.pair + sub, last = p.K * p.tiles_f - 1;
+  const int fe = ft < last ? ft : last;
+  const int shard = fe / p.tiles_f;
+  return Tile{shard, (fe - shard * p.tiles_f) * BM, mt * p.BN, ft <= last};
+}
 
 // ---- PTX wrappers ------------------------------------------------------------
 
@@ -99,6 +120,40 @@ __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* 
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
           "r"(smem_u32(dst)),
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The same tensor load into this offset of both CTAs of a pair, each barrier
+// at this offset counting its own bytes.
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint64_t* bar, void* dst,
+                                                 int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// An arrival at this offset of both CTAs of a pair once the MMAs have finished.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
       : "memory");
 }
 
@@ -155,6 +210,25 @@ __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
   return v;
 }
 
+// Barrier among the 128 threads of an epilogue half.
+__device__ __forceinline__ void half_barrier(int half) {
+  asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
+}
+
+// ... that tells all of them whether one of them has `v`.
+__device__ __forceinline__ bool half_any(int half, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\t"
+      "setp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, %2, 128, pi;\n\t"
+      "selp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(half + 1)
+      : "memory");
+  return r != 0;
+}
+
 template <bool MX>
 __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_constant__ Mx4mmParams p) {
   constexpr int BLOCK = MX ? kMxBlock : kNvBlock;
@@ -167,29 +241,30 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   uint8_t* sX = sW + kStages * kStageW;
   uint8_t* sSW = sX + kStages * kStageX;
   uint8_t* sSX = sSW + kStages * kStageSW;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSX + kStages * kStageSX);
+  uint8_t* sY = sSX + kStages * kStageSX;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sY + 2 * kStageY);
   uint64_t* empty = full + kStages;
   uint64_t* sfull = empty + kStages;    // a stage's scales are in shared memory
-  uint64_t* sready = sfull + kStages;   // ... and in TMEM
-  uint64_t* tmem_full = sready + kStages;
+  uint64_t* tmem_full = sfull + kStages;
   uint64_t* tmem_empty = tmem_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_empty + 1);
   volatile int* aborted = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
-  const int first = p.split > 1 ? (int)blockIdx.x / p.split : (int)blockIdx.x;
-  const int stride = p.split > 1 ? p.tiles : (int)gridDim.x;  // a cluster runs one tile
-  const int kb_lo = (int)rank * p.num_kb / p.split;
-  const int kb_hi = ((int)rank + 1) * p.num_kb / p.split;
+  const uint32_t rank = p.split > 1 || p.pair > 1 ? cluster_rank() : 0;
+  const int ctas = p.split * p.pair;  // of a cluster
+  const int first = (int)blockIdx.x / ctas;
+  const int stride = p.split > 1 ? p.tiles : (int)gridDim.x / ctas;  // a split cluster runs one tile
+  const int kb_lo = p.split > 1 ? (int)rank * p.num_kb / p.split : 0;
+  const int kb_hi = p.split > 1 ? ((int)rank + 1) * p.num_kb / p.split : p.num_kb;
+  const int sub = p.pair > 1 ? (int)rank : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 2);  // W and X
-      mbar_init(&empty[s], 1);
+      mbar_init(&full[s], 6);  // W, X, and the four scale warps
+      mbar_init(&empty[s], (uint32_t)p.pair);  // a pair's stage is free when both have read it
       mbar_init(&sfull[s], 1);
-      mbar_init(&sready[s], 4);  // one arrival per scale warp
     }
     mbar_init(tmem_full, 1);
     mbar_init(tmem_empty, kEpiWarps);
@@ -206,6 +281,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
+  if (p.pair > 1) cluster_barrier();  // the other's barriers are set up
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -218,10 +294,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       bool armed[kStages];
       for (int s = 0; s < kStages; ++s) armed[s] = false;
       for (int i = first; i < p.tiles && !*aborted; i += stride) {
-        const int tile = p.tile0 + i;
-        const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
-        const int shard = ft / p.tiles_f, f0 = (ft - shard * p.tiles_f) * BM;
-        const int m0 = mt * p.BN;
+        const Tile t = tile_at(p, i, sub);
         for (int kb = kb_lo; kb < kb_hi; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs)) {
             *aborted = 1;
@@ -232,16 +305,23 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
               (uint32_t)min(kTilesKb, p.col_tiles - t0) * kScaleTile;  // the last stage may end early
           if (warp == 0) {
             mbar_arrive_expect_tx(&full[stage], kStageW);
-            tma_load_2d(&p.tmW[shard], &full[stage], sW + stage * kStageW, kb * (BK / 2), f0);
+            tma_load_2d(&p.tmW[t.shard], &full[stage], sW + stage * kStageW, kb * (BK / 2), t.f0);
           } else if (warp == 2) {
             mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * (BK / 2));
-            tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), m0);
+            if (p.pair > 1) {  // half of the rows, for both CTAs
+              const int rows = p.BN / 2;
+              tma_load_2d_pair(&p.tmX, &full[stage],
+                               sX + stage * kStageX + (uint32_t)(sub * rows) * (BK / 2),
+                               kb * (BK / 2), t.m0 + sub * rows);
+            } else {
+              tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), t.m0);
+            }
           } else {
-            const int r0 = m0 / kScaleRows;
+            const int r0 = t.m0 / kScaleRows;
             const int rows = min((p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
             mbar_arrive_expect_tx(&sfull[stage], sbytes * (uint32_t)(rows + 1));
             bulk_load(&sfull[stage], sSW + stage * kStageSW,
-                      p.sw[shard] + ((size_t)(f0 / kScaleRows) * p.col_tiles + t0) * kScaleTile,
+                      p.sw[t.shard] + ((size_t)(t.f0 / kScaleRows) * p.col_tiles + t0) * kScaleTile,
                       sbytes);
             for (int r = 0; r < rows; ++r)
               bulk_load(&sfull[stage], sSX + stage * kStageSX + r * kScaleKb,
@@ -265,10 +345,12 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     // ------------------------------ MMA issuer --------------------------------
     if (lane == 0) {
       const uint32_t idesc = idesc_fp4(MX, p.BN);
+      const uint64_t a0 = sw128_kmajor_desc(smem_u32(sW)), b0 = sw128_kmajor_desc(smem_u32(sX));
       int stage = 0, w = 0;
       uint32_t phase = 0;
       bool issued = false;
       for (int i = first; i < p.tiles && !*aborted; i += stride, ++w) {
+        bool ready = false;
         if (!mbar_wait_bounded(tmem_empty, ((uint32_t)w & 1u) ^ 1u, p.err, kTimeoutNs)) {
           *aborted = 1;
           break;
@@ -276,35 +358,48 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         tc_fence_after();
         bool ok = true;
         for (int kb = kb_lo; kb < kb_hi; ++kb) {
-          if (!mbar_wait_bounded(&full[stage], phase, p.err, kTimeoutNs) ||
-              !mbar_wait_bounded(&sready[stage], phase, p.err, kTimeoutNs)) {
+          if (!ready && !mbar_wait_bounded(&full[stage], phase, p.err, kTimeoutNs)) {
             *aborted = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const int steps = min(BK / kStep, (p.D - kb * BK + kStep - 1) / kStep);
+          const uint64_t a = a0 + (uint32_t)stage * (kStageW >> 4);
+          const uint64_t b = b0 + (uint32_t)stage * (kStageX >> 4);
           const uint32_t tw = tmem_base + (uint32_t)(kScaleCol0 + stage * kScaleCols);
           const uint32_t tx = tw + 16u;
-          const uint32_t a0 = smem_u32(sW + stage * kStageW), b0 = smem_u32(sX + stage * kStageX);
-#pragma unroll
-          for (int k = 0; k < BK / kStep; ++k) {
-            if (k < steps) {
-              // nvfp4: a step's four scales are a tile's; mxfp4: its two are
-              // half of a tile's, chosen by the scale ids of the descriptor
-              const int t = MX ? k / 2 : k;
-              const uint32_t id = MX ? (uint32_t)(k & 1) * 2u : 0u;
-              mma_fp4<MX>(tmem_base, sw128_kmajor_desc(a0 + 32u * k), sw128_kmajor_desc(b0 + 32u * k),
-                          idesc | (id << 4) | (id << 29), tw + 4u * t, tx + 8u * t,
-                          (kb > kb_lo || k > 0) ? 1u : 0u);
-            }
+          const int steps = (p.D - kb * BK + kStep - 1) / kStep;  // the last stage may end early
+          // step k: 32 bytes further along the rows.  nvfp4: its four scales
+          // are a tile's; mxfp4: its two are half of a tile's, chosen by the
+          // scale ids of the descriptor
+#define DP_STEP(k)                                                                          \
+  mma_fp4<MX>(tmem_base, a + 2u * (k), b + 2u * (k),                                        \
+              MX ? idesc | ((uint32_t)((k) & 1) << 5) | ((uint32_t)((k) & 1) << 30) : idesc, \
+              tw + 4u * (MX ? (k) / 2 : (k)), tx + 8u * (MX ? (k) / 2 : (k)),               \
+              (k) > 0 || kb > kb_lo ? 1u : 0u)
+          if (steps >= 4) {
+            DP_STEP(0);
+            DP_STEP(1);
+            DP_STEP(2);
+            DP_STEP(3);
+          } else {
+            DP_STEP(0);
+            if (steps > 1) DP_STEP(1);
+            if (steps > 2) DP_STEP(2);
           }
-          mma_commit(&empty[stage]);
+#undef DP_STEP
+          if (p.pair > 1)
+            mma_commit_pair(&empty[stage]);
+          else
+            mma_commit(&empty[stage]);
           issued = true;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
+          // the MMAs are issued at about the rate at which they run, so what
+          // comes between two stages' must be short: one look at the next one
+          ready = mbar_test_wait(&full[stage], phase);
         }
         if (!ok) break;
         mma_commit(tmem_full);
@@ -359,7 +454,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sready[stage]);
+        if (lane == 0) mbar_arrive(&full[stage]);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
@@ -376,31 +471,28 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     const int fl = quarter * 32 + lane;
     int w = 0;
     for (int i = first; i < p.tiles; i += stride, ++w) {
-      const int tile = p.tile0 + i;
-      const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
-      const int shard = ft / p.tiles_f, f0 = (ft - shard * p.tiles_f) * BM;
-      const int m0 = mt * p.BN + c0 * 16;
+      const Tile t = tile_at(p, i, sub);
+      const int shard = t.shard, m0 = t.m0 + c0 * 16;
       float alpha = 1.0f;
       if constexpr (!MX) {
         if (p.tx) alpha = __ldg(p.tx);
         if (p.tw[shard]) alpha = __fmul_rn(alpha, __ldg(p.tw[shard]));
       }
       const bool ok = mbar_wait_bounded(tmem_full, (uint32_t)w & 1u, p.err, kTimeoutNs);
-      if (!__all_sync(0xffffffffu, ok)) {  // the warp's lanes leave together
+      if (half_any(half, !ok || *aborted)) {  // the half's threads leave together
         *aborted = 1;
         break;
       }
       tc_fence_after();
       const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c0 * 16);
-      const int f = f0 + fl;                       // inside the shard
-      const size_t yf = (size_t)shard * p.F_shard + f;
-      const bool f_in = f < p.F_shard;
+      const int f = t.f0 + fl;                     // inside the shard
+      const bool f_in = f < p.F_shard && t.own;
       if (p.split > 1 || p.y_f32) {
         // 32-bit values leave chunk by chunk: the partial sums of a split tile
         // as [token][128 f] to where the operands were (every MMA of this tile,
         // the CTA's only one, has completed), or y
         float* red = reinterpret_cast<float*>(smem) + c0 * 16 * BM + fl;
-        float* y = static_cast<float*>(p.y) + yf;
+        float* y = static_cast<float*>(p.y) + (size_t)shard * p.F_shard + f;
         for (int c = 0; c < cn; ++c) {
           uint32_t r[16];
           DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16), r);
@@ -422,50 +514,59 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       // bf16: pairs of tokens are packed into a register as they are read, so
       // the accumulator is free again before the first store
       uint32_t h[8][8];
-#pragma unroll
-      for (int c = 0; c < 8; c += 2) {
-        uint32_t r[2][16];
-        if (c < cn) DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16), r[0]);
-        if (c + 1 < cn) DP_TMEM_LD_X16(tbase + (uint32_t)(c * 16 + 16), r[1]);
-        tmem_ld_wait();
+      const auto pack32 = [&](const uint32_t(&r)[32], int c) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (c + e < cn)
-              h[c + e][q] = pack_bf16x2_rn(__fmul_rn(__uint_as_float(r[e][2 * q]), alpha),
-                                           __fmul_rn(__uint_as_float(r[e][2 * q + 1]), alpha));
+          for (int q = 0; q < 8; ++q) {
+            const float lo = __uint_as_float(r[e * 16 + 2 * q]);
+            const float hi = __uint_as_float(r[e * 16 + 2 * q + 1]);
+            h[c + e][q] = MX ? pack_bf16x2_rn(lo, hi)
+                             : pack_bf16x2_rn(__fmul_rn(lo, alpha), __fmul_rn(hi, alpha));
+          }
+      };
+#pragma unroll
+      for (int c = 0; c < 8; c += 2) {
+        uint32_t r[32];
+        if (c < cn) DP_TMEM_LD_X32(tbase + (uint32_t)(c * 16), r);
+        tmem_ld_wait();
+        pack32(r, c);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tmem_empty);
-      // neighbouring lanes trade halves, so that each stores two f of one
-      // token (F_shard is even)
-      const bool odd = lane & 1;
-      uint16_t* y = static_cast<uint16_t*>(p.y) + (yf & ~(size_t)1);
+      // 16 tokens at a time through the half's 4 KiB of shared memory, which
+      // one thread stores as a box that ends where the shard and y do
+      uint8_t* buf = sY + (uint32_t)half * kStageY;
+      const bool leader = quarter == 0 && lane == 0;
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         if (c < cn) {
+          if (leader) bulk_wait_read0();  // the previous box has been read
+          half_barrier(half);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, h[c][q], 1);
-            const int m = m0 + c * 16 + 2 * q + (odd ? 1 : 0);
-            if (f_in && m < p.M)
-              *reinterpret_cast<uint32_t*>(y + (size_t)m * p.F) =
-                  odd ? __byte_perm(got, h[c][q], 0x7632) : __byte_perm(h[c][q], got, 0x5410);
+            uint16_t* o = reinterpret_cast<uint16_t*>(buf) + (2 * q) * BM + fl;
+            o[0] = (uint16_t)h[c][q];
+            o[BM] = (uint16_t)(h[c][q] >> 16);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          half_barrier(half);
+          if (leader && t.own && m0 + c * 16 < p.M) {
+            tma_store_3d(&p.tmY, buf, t.f0, shard, m0 + c * 16);
+            bulk_commit();
           }
         }
     }
+    if (quarter == 0 && lane == 0) bulk_wait_all();  // written before the CTA leaves
   }
 
   __syncwarp();
   if (p.split > 1) {
     __syncthreads();
     cluster_barrier();  // every CTA's partial sums are in its shared memory
-    const int tile = p.tile0 + first;
-    const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
-    const int shard = ft / p.tiles_f, f0 = (ft - shard * p.tiles_f) * BM;
-    const int m0 = mt * p.BN;
+    const Tile t = tile_at(p, first, 0);
+    const int shard = t.shard, f0 = t.f0, m0 = t.m0;
     float alpha = 1.0f;
     if constexpr (!MX) {
       if (p.tx) alpha = __ldg(p.tx);
@@ -500,6 +601,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
 
   tc_fence_before();
   __syncthreads();
+  if (p.pair > 1) cluster_barrier();  // the other sends nothing more here
   if (warp == 2) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
@@ -519,20 +621,20 @@ cudaError_t launch_mx4mm(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, c
   cfg.blockDim = dim3(kThreadsM);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)(p.split * p.pair);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.split * p.pair > 1 ? 1 : 0;
   if (p.split == 1) {
-    int grid = std::min(tiles, dev.sm_count);
-    if (limit > 0) grid = std::min(grid, limit);
+    int grid = std::min(tiles, dev.sm_count / p.pair) * p.pair;
+    if (limit > 0) grid = std::max(p.pair, std::min(grid, limit / p.pair * p.pair));
     p.tile0 = 0;
     p.tiles = tiles;
     cfg.gridDim = dim3((unsigned)grid);
     return cudaLaunchKernelEx(&cfg, kernel, p);
   }
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)p.split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   // under a CTA limit the clusters go in several launches (one cluster each at least)
   const int per = limit > 0 ? std::max(1, std::min(tiles, limit / p.split)) : tiles;
   for (int t = 0; t < tiles; t += per) {
@@ -612,6 +714,7 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   memset(&p, 0, sizeof p);
   p.M = M;
   p.D = D;
+  p.K = K;
   p.F = F;
   p.F_shard = F_shard;
   p.tiles_f = (F_shard + BM - 1) / BM;
@@ -632,19 +735,25 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   p.split = 1;
   while (p.split < kMaxSplit && tiles * p.split * 2 <= dev.sm_count && p.num_kb >= p.split * 2)
     p.split *= 2;
+  // Two CTAs that share their tokens load half of X each, for both: operand
+  // intake, 54 KiB a stage, is what bounds a launch that fills the GPU.
+  const int limit = dph::gemm_cta_limit();
+  p.pair = p.split == 1 && all_f > 1 && tiles >= dev.sm_count && limit != 1 ? 2 : 1;
   p.sx = static_cast<const uint8_t*>(x->scales);
   p.tx = x->tensor_scale;
   p.y = y;
   p.y_f32 = y_dtype == DP_FP32;
   p.err = dev.err_word;
-  if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, D / 2, p.BN)) return DP_ERR_UNSUPPORTED;
+  if (!p.y_f32 && !dpl::encode_output_shards(&p.tmY, y, M, K, F_shard, kOutTokens))
+    return DP_ERR_UNSUPPORTED;
+  if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, D / 2, p.BN / p.pair)) return DP_ERR_UNSUPPORTED;
   for (int k = 0; k < K; ++k) {
     if (!dpl::encode_kmajor_bytes(&p.tmW[k], w_shards[k].codes, F_shard, D / 2, BM))
       return DP_ERR_UNSUPPORTED;
     p.sw[k] = static_cast<const uint8_t*>(w_shards[k].scales);
     p.tw[k] = w_shards[k].tensor_scale;
   }
-  *tilesp = tiles;
+  *tilesp = p.pair > 1 ? (all_f + 1) / 2 * p.tiles_m : tiles;
   return DP_OK;
 }
 
