@@ -16,7 +16,9 @@
 // One CTA (512 threads) per SM, persistent over tiles of 128 f x BN tokens:
 //   warp 0      W producer: 128 rows x 256 values (128 bytes) by TMA
 //   warp 2      X producer: BN rows x 256 values; also allocates TMEM
-//   warp 3      scales' producer: the rows' 512-byte scale tiles, contiguous copies
+//   warp 3      scales' producer: the rows' 512-byte scale tiles, 16 bytes a lane
+//               by cp.async (as three bulk copies a stage they cost more than
+//               W and X together: 193 us without them, 225 with)
 //   warps 12-15 scales into TMEM: lane l of each 32-lane quarter takes row l of a
 //               scale tile (16 bytes: four columns), tcgen05.st
 //   warp 1      MMA issuer: four MMAs of 64 values a stage
@@ -114,13 +116,18 @@ __device__ __forceinline__ Tile tile_at(const Mx4mmParams& p, int i, int sub) {
 
 // ---- PTX wrappers ------------------------------------------------------------
 
-__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src,
-                                          uint32_t bytes) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+// 16 bytes from global to shared memory by a thread, past L1; the arrival comes
+// when all of the thread's copies so far have landed.
+__device__ __forceinline__ void async_copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void async_copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void async_copy_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // The same tensor load into this offset of both CTAs of a pair, each barrier
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 6);  // W, X, and the four scale warps
       mbar_init(&empty[s], (uint32_t)p.pair);  // a pair's stage is free when both have read it
-      mbar_init(&sfull[s], 1);
+      mbar_init(&sfull[s], 32);  // each lane of warp 3, when its copies have landed
     }
     mbar_init(tmem_full, 1);
     mbar_init(tmem_empty, kEpiWarps);
@@ -285,7 +292,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0 || warp == 2 || warp == 3) {
+  if (warp == 0 || warp == 2) {
     // ------------------------------ producers ---------------------------------
     if (lane == 0) {
       int stage = 0;
@@ -300,13 +307,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
             *aborted = 1;
             break;
           }
-          const int t0 = kb * kTilesKb;
-          const uint32_t sbytes =
-              (uint32_t)min(kTilesKb, p.col_tiles - t0) * kScaleTile;  // the last stage may end early
           if (warp == 0) {
             mbar_arrive_expect_tx(&full[stage], kStageW);
             tma_load_2d(&p.tmW[t.shard], &full[stage], sW + stage * kStageW, kb * (BK / 2), t.f0);
-          } else if (warp == 2) {
+          } else {
             mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * (BK / 2));
             if (p.pair > 1) {  // half of the rows, for both CTAs
               const int rows = p.BN / 2;
@@ -316,16 +320,6 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
             } else {
               tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), t.m0);
             }
-          } else {
-            const int r0 = t.m0 / kScaleRows;
-            const int rows = min((p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
-            mbar_arrive_expect_tx(&sfull[stage], sbytes * (uint32_t)(rows + 1));
-            bulk_load(&sfull[stage], sSW + stage * kStageSW,
-                      p.sw[t.shard] + ((size_t)(t.f0 / kScaleRows) * p.col_tiles + t0) * kScaleTile,
-                      sbytes);
-            for (int r = 0; r < rows; ++r)
-              bulk_load(&sfull[stage], sSX + stage * kStageSX + r * kScaleKb,
-                        p.sx + ((size_t)(r0 + r) * p.col_tiles + t0) * kScaleTile, sbytes);
           }
           armed[stage] = true;
           armed_phase[stage] = phase;
@@ -337,10 +331,46 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       }
       // Drain: every load this thread issued has landed before the CTA exits.
       for (int s = 0; s < kStages; ++s)
-        if (armed[s])
-          (void)mbar_wait_bounded(warp == 3 ? &sfull[s] : &full[s], armed_phase[s], p.err,
-                                  kTimeoutNs);
+        if (armed[s]) (void)mbar_wait_bounded(&full[s], armed_phase[s], p.err, kTimeoutNs);
     }
+  } else if (warp == 3) {
+    // ------------------------------ scales into shared memory -----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = first; i < p.tiles && !*aborted; i += stride) {
+      const Tile t = tile_at(p, i, sub);
+      const uint8_t* gw =
+          p.sw[t.shard] + (size_t)(t.f0 / kScaleRows) * p.col_tiles * kScaleTile + lane * 16;
+      const int r0 = t.m0 / kScaleRows;
+      const uint8_t* gx = p.sx + (size_t)r0 * p.col_tiles * kScaleTile + lane * 16;
+      const int rows = min((p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        const bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          *aborted = 1;
+          break;
+        }
+        uint8_t* dw = sSW + stage * kStageSW + lane * 16;
+        uint8_t* dx = sSX + stage * kStageSX + lane * 16;
+#pragma unroll
+        for (int j = 0; j < kTilesKb; ++j) {
+          const int c = kb * kTilesKb + j;
+          if (c < p.col_tiles) {  // the last stage may end early
+            async_copy16(dw + j * kScaleTile, gw + (size_t)c * kScaleTile);
+            async_copy16(dx + j * kScaleTile, gx + (size_t)c * kScaleTile);
+            if (rows > 1)
+              async_copy16(dx + kScaleKb + j * kScaleTile,
+                           gx + ((size_t)p.col_tiles + c) * kScaleTile);
+          }
+        }
+        async_copy_arrive(&sfull[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    async_copy_wait_all();  // no copy outlives the CTA
   } else if (warp == 1) {
     // ------------------------------ MMA issuer --------------------------------
     if (lane == 0) {
