@@ -155,15 +155,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// An arrival at this offset of both CTAs of a pair once the MMAs have finished.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
 // Instruction descriptor of the block-scaled kinds: A and B e2m1, both
 // K-major; scales ue8m0 (mxfp4) or e4m3.
 __device__ __forceinline__ uint32_t idesc_fp4(bool mx, int n) {
@@ -174,26 +165,51 @@ __device__ __forceinline__ uint32_t idesc_fp4(bool mx, int n) {
          | ((uint32_t)(BM >> 7) << 27); // M >> 7
 }
 
+// The MMA and its commits are run by a whole warp and issued by one elected
+// lane: with every operand the same in all lanes the compiler keeps them in
+// uniform registers.  Inside an if (lane == 0) each MMA took 73 clocks to
+// issue, and a stage 788 clocks for 548 of MMAs.
 template <bool MX>
 __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                         uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
                                         uint32_t accumulate) {
   if constexpr (MX)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
         "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
+}
+
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+// An arrival at this offset of both CTAs of a pair once the MMAs have finished.
+__device__ __forceinline__ void commit_elected_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     // ------------------------------ scales into shared memory -----------------
     int stage = 0;
     uint32_t phase = 0;
-    for (int i = first; i < p.tiles && !*aborted; i += stride) {
+    for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride) {
       const Tile t = tile_at(p, i, sub);
       const uint8_t* gw =
           p.sw[t.shard] + (size_t)(t.f0 / kScaleRows) * p.col_tiles * kScaleTile + lane * 16;
@@ -373,80 +389,80 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     async_copy_wait_all();  // no copy outlives the CTA
   } else if (warp == 1) {
     // ------------------------------ MMA issuer --------------------------------
-    if (lane == 0) {
-      const uint32_t idesc = idesc_fp4(MX, p.BN);
-      const uint64_t a0 = sw128_kmajor_desc(smem_u32(sW)), b0 = sw128_kmajor_desc(smem_u32(sX));
-      int stage = 0, w = 0;
-      uint32_t phase = 0;
-      bool issued = false;
-      for (int i = first; i < p.tiles && !*aborted; i += stride, ++w) {
-        bool ready = false;
-        if (!mbar_wait_bounded(tmem_empty, ((uint32_t)w & 1u) ^ 1u, p.err, kTimeoutNs)) {
+    const uint32_t idesc = idesc_fp4(MX, p.BN);
+    const uint64_t a0 = sw128_kmajor_desc(smem_u32(sW)), b0 = sw128_kmajor_desc(smem_u32(sX));
+    int stage = 0, w = 0;
+    uint32_t phase = 0;
+    bool issued = false;
+    for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride, ++w) {
+      bool ready = false;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tmem_empty, ((uint32_t)w & 1u) ^ 1u, p.err,
+                                                     kTimeoutNs))) {
+        *aborted = 1;
+        break;
+      }
+      tc_fence_after();
+      bool ok = true;
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        if (!ready && !__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, p.err,
+                                                                 kTimeoutNs))) {
           *aborted = 1;
+          ok = false;
           break;
         }
         tc_fence_after();
-        bool ok = true;
-        for (int kb = kb_lo; kb < kb_hi; ++kb) {
-          if (!ready && !mbar_wait_bounded(&full[stage], phase, p.err, kTimeoutNs)) {
-            *aborted = 1;
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t a = a0 + (uint32_t)stage * (kStageW >> 4);
-          const uint64_t b = b0 + (uint32_t)stage * (kStageX >> 4);
-          const uint32_t tw = tmem_base + (uint32_t)(kScaleCol0 + stage * kScaleCols);
-          const uint32_t tx = tw + 16u;
-          const int steps = (p.D - kb * BK + kStep - 1) / kStep;  // the last stage may end early
-          // step k: 32 bytes further along the rows.  nvfp4: its four scales
-          // are a tile's; mxfp4: its two are half of a tile's, chosen by the
-          // scale ids of the descriptor
+        const uint64_t a = a0 + (uint32_t)stage * (kStageW >> 4);
+        const uint64_t b = b0 + (uint32_t)stage * (kStageX >> 4);
+        const uint32_t tw = tmem_base + (uint32_t)(kScaleCol0 + stage * kScaleCols);
+        const uint32_t tx = tw + 16u;
+        const int steps = (p.D - kb * BK + kStep - 1) / kStep;  // the last stage may end early
+        // step k: 32 bytes further along the rows.  nvfp4: its four scales
+        // are a tile's; mxfp4: its two are half of a tile's, chosen by the
+        // scale ids of the descriptor
 #define DP_STEP(k)                                                                          \
   mma_fp4<MX>(tmem_base, a + 2u * (k), b + 2u * (k),                                        \
-              MX ? idesc | ((uint32_t)((k) & 1) << 5) | ((uint32_t)((k) & 1) << 30) : idesc, \
-              tw + 4u * (MX ? (k) / 2 : (k)), tx + 8u * (MX ? (k) / 2 : (k)),               \
-              (k) > 0 || kb > kb_lo ? 1u : 0u)
-          if (steps >= 4) {
-            DP_STEP(0);
-            DP_STEP(1);
-            DP_STEP(2);
-            DP_STEP(3);
-          } else {
-            DP_STEP(0);
-            if (steps > 1) DP_STEP(1);
-            if (steps > 2) DP_STEP(2);
-          }
-#undef DP_STEP
-          if (p.pair > 1)
-            mma_commit_pair(&empty[stage]);
-          else
-            mma_commit(&empty[stage]);
-          issued = true;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          // the MMAs are issued at about the rate at which they run, so what
-          // comes between two stages' must be short: one look at the next one
-          ready = mbar_test_wait(&full[stage], phase);
+            MX ? idesc | ((uint32_t)((k) & 1) << 5) | ((uint32_t)((k) & 1) << 30) : idesc, \
+            tw + 4u * (MX ? (k) / 2 : (k)), tx + 8u * (MX ? (k) / 2 : (k)),               \
+            (k) > 0 || kb > kb_lo ? 1u : 0u)
+        if (steps >= 4) {
+          DP_STEP(0);
+          DP_STEP(1);
+          DP_STEP(2);
+          DP_STEP(3);
+        } else {
+          DP_STEP(0);
+          if (steps > 1) DP_STEP(1);
+          if (steps > 2) DP_STEP(2);
         }
-        if (!ok) break;
-        mma_commit(tmem_full);
+#undef DP_STEP
+        if (p.pair > 1)
+          commit_elected_pair(&empty[stage]);
+        else
+          commit_elected(&empty[stage]);
+        issued = true;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        // the MMAs are issued at about the rate at which they run, so what
+        // comes between two stages' must be short: one look at the next one
+        ready = __all_sync(0xffffffffu, mbar_test_wait(&full[stage], phase));
       }
-      // Drain: every MMA issued has completed before TMEM is freed.
-      if (issued) {
-        const int last = stage == 0 ? kStages - 1 : stage - 1;
-        const uint32_t last_phase = stage == 0 ? phase ^ 1u : phase;
-        (void)mbar_wait_bounded(&empty[last], last_phase, p.err, kTimeoutNs);
-      }
+      if (!ok) break;
+      commit_elected(tmem_full);
+    }
+    // Drain: every MMA issued has completed before TMEM is freed.
+    if (issued) {
+      const int last = stage == 0 ? kStages - 1 : stage - 1;
+      const uint32_t last_phase = stage == 0 ? phase ^ 1u : phase;
+      (void)mbar_wait_bounded(&empty[last], last_phase, p.err, kTimeoutNs);
     }
   } else if (warp >= 12) {
     // ------------------------------ scales into TMEM --------------------------
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int stage = 0;
     uint32_t phase = 0;
-    for (int i = first; i < p.tiles && !*aborted; i += stride) {
+    for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride) {
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         const bool ok = mbar_wait_bounded(&sfull[stage], phase, p.err, kTimeoutNs);
         if (!__all_sync(0xffffffffu, ok)) {
