@@ -86,7 +86,7 @@ struct Mx4mmParams {
   const float* tw[kMaxK];
   void* y;
   unsigned* err;
-  int M, D, K, F, F_shard;
+  int M, D, F, F_shard;
   int BN;
   int tiles_m, tiles_f;   // tiles_f: of one shard
   int tile0, tiles;       // this launch's tiles
@@ -94,24 +94,18 @@ struct Mx4mmParams {
   int col_tiles;          // scale tiles along d
   int x_row_tiles;
   int split;              // CTAs of a cluster that share a tile
-  int pair;               // CTAs of a cluster that share X: 2, or 1
   int y_f32;
 };
 
-// Tile i of this launch, or of a pair's two the one of CTA `sub`: the last
-// pair of an odd number of weight row tiles has the last one twice, stored by
-// the first CTA alone.
+// Tile i of this launch.
 struct Tile {
   int shard, f0, m0;
-  bool own;
 };
-__device__ __forceinline__ Tile tile_at(const Mx4mmParams& p, int i, int sub) {
+__device__ __forceinline__ Tile tile_at(const Mx4mmParams& p, int i) {
   const int tile = p.tile0 + i;
-  const int fp = tile / p.tiles_m, mt = tile - fp * p.tiles_m;
-  const int ft = fp * p.pair + sub, last = p.K * p.tiles_f - 1;
-  const int fe = ft < last ? ft : last;
-  const int shard = fe / p.tiles_f;
-  return Tile{shard, (fe - shard * p.tiles_f) * BM, mt * p.BN, ft <= last};
+  const int ft = tile / p.tiles_m, mt = tile - ft * p.tiles_m;
+  const int shard = ft / p.tiles_f;
+  return Tile{shard, (ft - shard * p.tiles_f) * BM, mt * p.BN};
 }
 
 // ---- PTX wrappers ------------------------------------------------------------
@@ -128,18 +122,6 @@ __device__ __forceinline__ void async_copy_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void async_copy_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// The same tensor load into this offset of both CTAs of a pair, each barrier
-// at this offset counting its own bytes.
-__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint64_t* bar, void* dst,
-                                                 int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
 }
 
 // Whether the phase has completed, without waiting.
@@ -201,17 +183,6 @@ __device__ __forceinline__ void commit_elected(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
-// An arrival at this offset of both CTAs of a pair once the MMAs have finished.
-__device__ __forceinline__ void commit_elected_pair(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -268,25 +239,25 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   uint64_t* full = reinterpret_cast<uint64_t*>(sY + 2 * kStageY);
   uint64_t* empty = full + kStages;
   uint64_t* sfull = empty + kStages;    // a stage's scales are in shared memory
-  uint64_t* tmem_full = sfull + kStages;
+  uint64_t* sempty = sfull + kStages;   // ... and have been read from it
+  uint64_t* tmem_full = sempty + kStages;
   uint64_t* tmem_empty = tmem_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_empty + 1);
   volatile int* aborted = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = p.split > 1 || p.pair > 1 ? cluster_rank() : 0;
-  const int ctas = p.split * p.pair;  // of a cluster
-  const int first = (int)blockIdx.x / ctas;
-  const int stride = p.split > 1 ? p.tiles : (int)gridDim.x / ctas;  // a split cluster runs one tile
-  const int kb_lo = p.split > 1 ? (int)rank * p.num_kb / p.split : 0;
-  const int kb_hi = p.split > 1 ? ((int)rank + 1) * p.num_kb / p.split : p.num_kb;
-  const int sub = p.pair > 1 ? (int)rank : 0;
+  const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
+  const int first = (int)blockIdx.x / p.split;
+  const int stride = p.split > 1 ? p.tiles : (int)gridDim.x;  // a cluster runs one tile
+  const int kb_lo = (int)rank * p.num_kb / p.split;
+  const int kb_hi = ((int)rank + 1) * p.num_kb / p.split;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 6);  // W, X, and the four scale warps
-      mbar_init(&empty[s], (uint32_t)p.pair);  // a pair's stage is free when both have read it
+      mbar_init(&empty[s], 1);
+      mbar_init(&sempty[s], 4);  // one arrival per scale warp
       mbar_init(&sfull[s], 32);  // each lane of warp 3, when its copies have landed
     }
     mbar_init(tmem_full, 1);
@@ -304,7 +275,6 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
-  if (p.pair > 1) cluster_barrier();  // the other's barriers are set up
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -317,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       bool armed[kStages];
       for (int s = 0; s < kStages; ++s) armed[s] = false;
       for (int i = first; i < p.tiles && !*aborted; i += stride) {
-        const Tile t = tile_at(p, i, sub);
+        const Tile t = tile_at(p, i);
         for (int kb = kb_lo; kb < kb_hi; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs)) {
             *aborted = 1;
@@ -328,14 +298,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
             tma_load_2d(&p.tmW[t.shard], &full[stage], sW + stage * kStageW, kb * (BK / 2), t.f0);
           } else {
             mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * (BK / 2));
-            if (p.pair > 1) {  // half of the rows, for both CTAs
-              const int rows = p.BN / 2;
-              tma_load_2d_pair(&p.tmX, &full[stage],
-                               sX + stage * kStageX + (uint32_t)(sub * rows) * (BK / 2),
-                               kb * (BK / 2), t.m0 + sub * rows);
-            } else {
-              tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), t.m0);
-            }
+            tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), t.m0);
           }
           armed[stage] = true;
           armed_phase[stage] = phase;
@@ -354,14 +317,14 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     int stage = 0;
     uint32_t phase = 0;
     for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride) {
-      const Tile t = tile_at(p, i, sub);
+      const Tile t = tile_at(p, i);
       const uint8_t* gw =
           p.sw[t.shard] + (size_t)(t.f0 / kScaleRows) * p.col_tiles * kScaleTile + lane * 16;
       const int r0 = t.m0 / kScaleRows;
       const uint8_t* gx = p.sx + (size_t)r0 * p.col_tiles * kScaleTile + lane * 16;
       const int rows = min((p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
-        const bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs);
+        const bool ok = mbar_wait_bounded(&sempty[stage], phase ^ 1u, p.err, kTimeoutNs);
         if (!__all_sync(0xffffffffu, ok)) {
           *aborted = 1;
           break;
@@ -435,10 +398,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           if (steps > 2) DP_STEP(2);
         }
 #undef DP_STEP
-        if (p.pair > 1)
-          commit_elected_pair(&empty[stage]);
-        else
-          commit_elected(&empty[stage]);
+        commit_elected(&empty[stage]);
         issued = true;
         if (++stage == kStages) {
           stage = 0;
@@ -469,7 +429,6 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           *aborted = 1;
           break;
         }
-        tc_fence_after();
         // this quarter's copy of each tile; a tile that the last stage lacks,
         // or a second row tile that X lacks, is stale and belongs to no step or
         // to no token
@@ -488,6 +447,14 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
             x[o] = b.x, x[o + 1] = b.y, x[o + 2] = b.z, x[o + 3] = b.w;
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[stage]);  // the next ones can come while these wait
+        const bool free = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs);
+        if (!__all_sync(0xffffffffu, free)) {
+          *aborted = 1;
+          break;
+        }
+        tc_fence_after();
         if constexpr (MX) {
           DP_TMEM_ST_X8(tw, w);
           DP_TMEM_ST_X16(tw + 16u, x);
@@ -517,7 +484,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     const int fl = quarter * 32 + lane;
     int w = 0;
     for (int i = first; i < p.tiles; i += stride, ++w) {
-      const Tile t = tile_at(p, i, sub);
+      const Tile t = tile_at(p, i);
       const int shard = t.shard, m0 = t.m0 + c0 * 16;
       float alpha = 1.0f;
       if constexpr (!MX) {
@@ -532,7 +499,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       tc_fence_after();
       const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c0 * 16);
       const int f = t.f0 + fl;                     // inside the shard
-      const bool f_in = f < p.F_shard && t.own;
+      const bool f_in = f < p.F_shard;
       if (p.split > 1 || p.y_f32) {
         // 32-bit values leave chunk by chunk: the partial sums of a split tile
         // as [token][128 f] to where the operands were (every MMA of this tile,
@@ -598,7 +565,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           half_barrier(half);
-          if (leader && t.own && m0 + c * 16 < p.M) {
+          if (leader && m0 + c * 16 < p.M) {
             tma_store_3d(&p.tmY, buf, t.f0, shard, m0 + c * 16);
             bulk_commit();
           }
@@ -611,7 +578,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   if (p.split > 1) {
     __syncthreads();
     cluster_barrier();  // every CTA's partial sums are in its shared memory
-    const Tile t = tile_at(p, first, 0);
+    const Tile t = tile_at(p, first);
     const int shard = t.shard, f0 = t.f0, m0 = t.m0;
     float alpha = 1.0f;
     if constexpr (!MX) {
@@ -647,7 +614,6 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
 
   tc_fence_before();
   __syncthreads();
-  if (p.pair > 1) cluster_barrier();  // the other sends nothing more here
   if (warp == 2) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
@@ -669,13 +635,13 @@ cudaError_t launch_mx4mm(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, c
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)(p.split * p.pair);
+  attr.val.clusterDim.x = (unsigned)p.split;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = p.split * p.pair > 1 ? 1 : 0;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
   if (p.split == 1) {
-    int grid = std::min(tiles, dev.sm_count / p.pair) * p.pair;
-    if (limit > 0) grid = std::max(p.pair, std::min(grid, limit / p.pair * p.pair));
+    int grid = std::min(tiles, dev.sm_count);
+    if (limit > 0) grid = std::min(grid, limit);
     p.tile0 = 0;
     p.tiles = tiles;
     cfg.gridDim = dim3((unsigned)grid);
@@ -760,7 +726,6 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   memset(&p, 0, sizeof p);
   p.M = M;
   p.D = D;
-  p.K = K;
   p.F = F;
   p.F_shard = F_shard;
   p.tiles_f = (F_shard + BM - 1) / BM;
@@ -781,10 +746,6 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   p.split = 1;
   while (p.split < kMaxSplit && tiles * p.split * 2 <= dev.sm_count && p.num_kb >= p.split * 2)
     p.split *= 2;
-  // Two CTAs that share their tokens load half of X each, for both: operand
-  // intake, 54 KiB a stage, is what bounds a launch that fills the GPU.
-  const int limit = dph::gemm_cta_limit();
-  p.pair = p.split == 1 && all_f > 1 && tiles >= dev.sm_count && limit != 1 ? 2 : 1;
   p.sx = static_cast<const uint8_t*>(x->scales);
   p.tx = x->tensor_scale;
   p.y = y;
@@ -792,14 +753,14 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   p.err = dev.err_word;
   if (!p.y_f32 && !dpl::encode_output_shards(&p.tmY, y, M, K, F_shard, kOutTokens))
     return DP_ERR_UNSUPPORTED;
-  if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, D / 2, p.BN / p.pair)) return DP_ERR_UNSUPPORTED;
+  if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, D / 2, p.BN)) return DP_ERR_UNSUPPORTED;
   for (int k = 0; k < K; ++k) {
     if (!dpl::encode_kmajor_bytes(&p.tmW[k], w_shards[k].codes, F_shard, D / 2, BM))
       return DP_ERR_UNSUPPORTED;
     p.sw[k] = static_cast<const uint8_t*>(w_shards[k].scales);
     p.tw[k] = w_shards[k].tensor_scale;
   }
-  *tilesp = p.pair > 1 ? (all_f + 1) / 2 * p.tiles_m : tiles;
+  *tilesp = tiles;
   return DP_OK;
 }
 
