@@ -358,9 +358,11 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     uint32_t phase = 0;
     bool issued = false;
     for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride, ++w) {
-      bool ready = false;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tmem_empty, ((uint32_t)w & 1u) ^ 1u, p.err,
-                                                     kTimeoutNs))) {
+      // the first stage first: it is there long before the accumulator is free
+      bool ready = true;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, p.err, kTimeoutNs) &&
+                                       mbar_wait_bounded(tmem_empty, ((uint32_t)w & 1u) ^ 1u,
+                                                         p.err, kTimeoutNs))) {
         *aborted = 1;
         break;
       }
@@ -491,11 +493,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         if (p.tx) alpha = __ldg(p.tx);
         if (p.tw[shard]) alpha = __fmul_rn(alpha, __ldg(p.tw[shard]));
       }
+      // A wait that ran out is acted on where the half's threads next meet, so
+      // that they leave together; until then nothing depends on what was read.
       const bool ok = mbar_wait_bounded(tmem_full, (uint32_t)w & 1u, p.err, kTimeoutNs);
-      if (half_any(half, !ok || *aborted)) {  // the half's threads leave together
-        *aborted = 1;
-        break;
-      }
+      __syncwarp();
       tc_fence_after();
       const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(c0 * 16);
       const int f = t.f0 + fl;                     // inside the shard
@@ -522,6 +523,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(tmem_empty);
+        if (half_any(half, !ok || *aborted)) {
+          *aborted = 1;
+          break;
+        }
         continue;
       }
       // bf16: pairs of tokens are packed into a register as they are read, so
@@ -552,6 +557,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       // one thread stores as a box that ends where the shard and y do
       uint8_t* buf = sY + (uint32_t)half * kStageY;
       const bool leader = quarter == 0 && lane == 0;
+      if (half_any(half, !ok || *aborted)) {
+        *aborted = 1;
+        break;
+      }
 #pragma unroll
       for (int c = 0; c < 8; ++c)
         if (c < cn) {
