@@ -15,8 +15,8 @@
 //
 // Bound by memory: 2 bytes read and 0.53 / 0.56 written for each bf16 value.
 // Rows form: a warp takes up to 1024 columns of a row with all its loads
-// issued first, a lane eight columns of each 256, so a block is 2 or 4
-// neighbouring lanes.  Transposed form: blocks run down the columns, so a lane
+// issued first, a lane sixteen columns of each 512, so a block is one lane
+// (nvfp4) or two.  Transposed form: blocks run down the columns, so a lane
 // takes two neighbouring columns and reads 64 rows of them (a warp reads 128
 // contiguous bytes of each bf16 row): a block's largest value needs no
 // exchange, a lane ends with 32 contiguous bytes of each of its two output
@@ -109,7 +109,8 @@ struct Divisor {
   bool near;
   __device__ __forceinline__ explicit Divisor(float v) : d(v) {
     near = v > 1e-30f && v < 1e30f;
-    hi = __frcp_rn(v);
+    // any value within 2^-22 of the reciprocal: lo takes up what it misses
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(v));
     lo = __fmul_rn(__fmaf_rn(-hi, v, 1.0f), hi);
   }
   __device__ __forceinline__ float of(float x) const {
@@ -145,15 +146,16 @@ template <>
 struct Scale<kNvBlock> {
   uint32_t byte;
   float step;
-  __device__ __forceinline__ Scale(float amax, float t, const Divisor& by_t) {
+  Divisor by;
+  __device__ __forceinline__ Scale(float amax, float t, const Divisor& by_t) : by(1.0f) {
     uint16_t c;
     const float s = amax > 0.0f ? by_t.of(__fmul_rn(amax, 1.0f / 6.0f)) : 0.0f;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(s));
     byte = __float_as_uint(amax) < 0x7f800000u ? (uint32_t)c & 0xffu : 0x7fu;
     step = __fmul_rn(e4m3_value(byte), t);
+    by = Divisor(step);
   }
   __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
-    const Divisor by(step);
     float w[8];
     if (by.near) {
 #pragma unroll
@@ -166,16 +168,26 @@ struct Scale<kNvBlock> {
   }
 };
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
-                 "=f"(v[6]), "=f"(v[7])
-               : "l"(p));
+// Sixteen consecutive elements, widened: from a 32-byte boundary.
+__device__ __forceinline__ void load16(const float* p, float (&v)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[h][0]), "=f"(v[h][1]), "=f"(v[h][2]), "=f"(v[h][3]), "=f"(v[h][4]),
+                   "=f"(v[h][5]), "=f"(v[h][6]), "=f"(v[h][7])
+                 : "l"(p + 8 * h));
 }
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  uint4 raw[1];
-  Vec8<uint16_t>::load(p, raw);
-  Vec8<uint16_t>::widen(raw, v);
+__device__ __forceinline__ void load16(const uint16_t* p, float (&v)[2][8]) {
+  uint32_t r[8];
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i / 4][2 * (i % 4)] = bf16lo(r[i]);
+    v[i / 4][2 * (i % 4) + 1] = bf16hi(r[i]);
+  }
 }
 
 // Where the four scales of (row, column tile) lie.
@@ -186,57 +198,52 @@ __device__ __forceinline__ size_t scale_at(int row, int tile, int col_tiles) {
 
 // ---- rows form ---------------------------------------------------------------
 
-// One row's G x 256 columns from e0 on, by a warp.
+// One row's G x 512 columns from e0 on, by a warp.
 template <typename T, int BLOCK, int G>
 __device__ __forceinline__ void quant_row(const QuantParams& p, int r, int e0, bool vec, float t,
                                           const Divisor& by_t) {
-  constexpr int kLanes = BLOCK / 8;  // lanes of a block
   const int lane = threadIdx.x & 31;
-  float v[G][8];
+  float v[G][2][8];
   const T* x = r < p.R ? row_at<T>(p, r) : nullptr;
-  if (x && vec && e0 + G * 256 <= p.L) {
+  if (x && vec && e0 + G * 512 <= p.L) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) load8(x + e0 + g * 256 + lane * 8, v[g]);
+    for (int g = 0; g < G; ++g) load16(x + e0 + g * 512 + lane * 16, v[g]);
   } else {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int e = e0 + g * 256 + lane * 8;
-      const bool in = x && e < p.L;  // L is a multiple of 32: all eight are inside or none
+      const int e = e0 + g * 512 + lane * 16;
+      const bool in = x && e < p.L;  // L is a multiple of 32: all sixteen are inside or none
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[g][i] = in ? widen_scalar(x, e + i) : 0.0f;
+      for (int i = 0; i < 16; ++i) v[g][i / 8][i % 8] = in ? widen_scalar(x, e + i) : 0.0f;
     }
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int e = e0 + g * 256 + lane * 8;
+    const int e = e0 + g * 512 + lane * 16;
+    const bool in = x && e < p.L;
     uint32_t top = 0;  // magnitudes order as their bits, NaN above all
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[g][i]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 1; o < kLanes; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[g][i / 8][i % 8]) & 0x7fffffffu);
+    if (BLOCK == kMxBlock) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     const Scale<BLOCK> s(__uint_as_float(top), t, by_t);
-    if (x && e < p.L)
-      *reinterpret_cast<uint32_t*>(p.codes + (size_t)r * (p.L / 2) + e / 2) = s.codes(v[g]);
-    const uint32_t byte = x && e < p.L ? s.byte : 0u;
-    uint32_t four = byte;
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-      four |= __shfl_down_sync(0xffffffffu, byte, i * kLanes) << (8 * i);
-    const int tile = e / (4 * BLOCK);
-    if (lane % (4 * kLanes) == 0 && tile < p.col_tiles)
-      *reinterpret_cast<uint32_t*>(p.scales + scale_at(r, tile, p.col_tiles)) = four;
+    if (in)
+      *reinterpret_cast<uint2*>(p.codes + (size_t)r * (p.L / 2) + e / 2) =
+          make_uint2(s.codes(v[g][0]), s.codes(v[g][1]));
+    const int b = e / BLOCK;
+    if (b / 4 < p.col_tiles && (BLOCK == kNvBlock || lane % 2 == 0))
+      p.scales[scale_at(r, b / 4, p.col_tiles) + b % 4] = in ? (uint8_t)s.byte : (uint8_t)0;
   }
 }
 
 template <typename T, int BLOCK, int G>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_constant__ QuantParams p) {
-  const unsigned groups = ((unsigned)p.col_tiles * 4 * BLOCK + G * 256 - 1) / (G * 256);
+  const unsigned groups = ((unsigned)p.col_tiles * 4 * BLOCK + G * 512 - 1) / (G * 512);
   const unsigned blocks = ((unsigned)p.R + kScaleRows - 1) / kScaleRows * (kScaleRows / kWarps) * groups;
   const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
   const Divisor by_t(t);
   for (unsigned b = blockIdx.x; b < blocks; b += gridDim.x) {
     const unsigned q = b / groups;
-    quant_row<T, BLOCK, G>(p, (int)(q * kWarps + (threadIdx.x >> 5)), (int)((b - q * groups) * G * 256),
+    quant_row<T, BLOCK, G>(p, (int)(q * kWarps + (threadIdx.x >> 5)), (int)((b - q * groups) * G * 512),
                            p.vec_ok, t, by_t);
   }
 }
@@ -406,9 +413,9 @@ cudaError_t launch(KernelT kernel, const P& p, long long blocks, cudaStream_t s)
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// Columns a warp takes at once in the rows form and in decoding: all its loads
-// are in flight together, so 1024 where rows are that long and enough of them
-// to fill the GPU; short calls spread wider with 256.
+// Whether a warp takes 1024 columns at once in the rows form and in decoding:
+// all its loads are in flight together, where rows are that long and enough of
+// them to fill the GPU; short calls spread wider, with 512 and 256.
 bool wide(long long rows, long long cols) { return cols >= 1024 && rows * cols >= (1ll << 21); }
 
 template <typename T, int BLOCK>
@@ -422,8 +429,8 @@ cudaError_t quantize(const QuantParams& p, bool transpose, cudaStream_t s) {
     return launch(quant_cols_kernel<T, BLOCK, false>, p, blocks, s);
   }
   if (wide(p.R, p.L))
-    return launch(quant_rows_kernel<T, BLOCK, 4>, p, rows / kWarps * ceil_div(cols, 1024), s);
-  return launch(quant_rows_kernel<T, BLOCK, 1>, p, rows / kWarps * ceil_div(cols, 256), s);
+    return launch(quant_rows_kernel<T, BLOCK, 2>, p, rows / kWarps * ceil_div(cols, 1024), s);
+  return launch(quant_rows_kernel<T, BLOCK, 1>, p, rows / kWarps * ceil_div(cols, 512), s);
 }
 
 template <typename T, int BLOCK>
@@ -490,7 +497,7 @@ dp_status_t dp_mx4_quantize(const void* const* x, int K, int rows, int cols, lon
     if (!aligned(x[k], esz)) return DP_ERR_UNSUPPORTED;
     const Span in = span_of(x[k], ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * esz);
     if (clash(in, out[0]) || clash(in, out[1])) return DP_ERR_ALIAS;
-    vec = vec && aligned(x[k], transpose ? 2 * esz : 8 * esz);
+    vec = vec && aligned(x[k], transpose ? 2 * esz : 32);
     p.x[k] = x[k];
   }
   if (tensor_scale) {
@@ -500,7 +507,7 @@ dp_status_t dp_mx4_quantize(const void* const* x, int K, int rows, int cols, lon
   p.rows = rows;
   p.whole = K == 1 || rows % 32 == 0;
   p.ld = ld;
-  p.vec_ok = vec && ld % (transpose ? 2 : 8) == 0;
+  p.vec_ok = vec && ld % (transpose ? 2 : 16) == 0;
   p.R = R;
   p.L = L;
   p.col_tiles = mx4_col_tiles(L, mx4_block(format));

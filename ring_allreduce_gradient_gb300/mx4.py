@@ -116,22 +116,29 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
         with _on(stream, xs[0].device):
             return quantize(xs, format, tensor_scale, transpose)
     x0 = xs[0]
-    for t in xs:
-        if t.dim() != 2 or t.shape != x0.shape or t.dtype != x0.dtype or t.device != x0.device \
-                or t.stride() != x0.stride() or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError("need matrices of one shape, dtype, device and row stride, with unit "
-                             "stride along the rows")
-    rows, cols = x0.shape
-    _check_scale(tensor_scale, x0.device)
+    rows, cols = _matrix(x0)
+    for t in xs[1:]:
+        if t.shape != x0.shape or t.dtype != x0.dtype or t.device != x0.device or \
+                t.stride() != x0.stride():
+            raise ValueError("need shards of one shape, dtype, device and row stride")
+    dev = x0.device
+    _check_scale(tensor_scale, dev)
     K = len(xs)
     R, L = (cols, K * rows) if transpose else (K * rows, cols)
-    codes = torch.empty(R, L // 2, dtype=torch.uint8, device=x0.device)
-    scales = torch.empty(_scale_bytes(R, L, format), dtype=torch.uint8, device=x0.device)
+    codes = torch.empty((R, L // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty(_scale_bytes(R, L, format), dtype=torch.uint8, device=dev)
     B.dp_mx4_quantize(xs, K, rows, cols, _row_stride(x0), _code(x0), fmt, transpose, tensor_scale,
                       codes, scales)
     q = Mx4Tensor.__new__(Mx4Tensor)
     q._set(codes, scales, R, L, format, tensor_scale)
     return q
+
+
+def _matrix(x):
+    """The shape of a matrix with unit stride along its rows."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("need a matrix with unit stride along its rows")
+    return x.shape
 
 
 def _row_stride(x) -> int:
@@ -185,11 +192,9 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
     if stream is not None:
         with _on(stream, x.device):
             return linear(x, w_shards, x_scale, y_dtype)
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("x: a matrix with unit stride along its rows")
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
-    M, D = x.shape
+    M, D = _matrix(x)
     dev, K, w0 = x.device, len(w_shards), w_shards[0]
     arr = _shards(w_shards, D, w0._format, dev)
     _check_scale(x_scale, dev)
