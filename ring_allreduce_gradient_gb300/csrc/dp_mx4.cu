@@ -237,6 +237,8 @@ __device__ __forceinline__ void quant_row(const QuantParams& p, int r, int e0, b
 
 template <typename T, int BLOCK, int G>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_constant__ QuantParams p) {
+  // a product that follows may set itself up meanwhile (it waits for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const unsigned groups = ((unsigned)p.col_tiles * 4 * BLOCK + G * 512 - 1) / (G * 512);
   const unsigned blocks = ((unsigned)p.R + kScaleRows - 1) / kScaleRows * (kScaleRows / kWarps) * groups;
   const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;

@@ -86,7 +86,7 @@ struct Mx4mmParams {
   const float* tw[kMaxK];
   void* y;
   unsigned* err;
-  int M, D, F, F_shard;
+  int M, D, K, F, F_shard;
   int BN;
   int tiles_m, tiles_f;   // tiles_f: of one shard
   int tile0, tiles;       // this launch's tiles
@@ -122,6 +122,10 @@ __device__ __forceinline__ void async_copy_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void async_copy_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // Whether the phase has completed, without waiting.
@@ -273,10 +277,19 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (threadIdx.x == 0) {
+    prefetch_map(&p.tmX);
+    if (!p.y_f32) prefetch_map(&p.tmY);
+  }
+  if (warp == 0 && lane < p.K) prefetch_map(&p.tmW[lane]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // the launch may begin while the kernel before it in the stream (the
+  // quantisation of x) still runs: nothing of global memory is touched before
+  // that one has ended
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0 || warp == 2) {
     // ------------------------------ producers ---------------------------------
@@ -322,7 +335,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           p.sw[t.shard] + (size_t)(t.f0 / kScaleRows) * p.col_tiles * kScaleTile + lane * 16;
       const int r0 = t.m0 / kScaleRows;
       const uint8_t* gx = p.sx + (size_t)r0 * p.col_tiles * kScaleTile + lane * 16;
-      const int rows = min((p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
+      const int rows =
+          min((t.m0 % kScaleRows + p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - r0);
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         const bool ok = mbar_wait_bounded(&sempty[stage], phase ^ 1u, p.err, kTimeoutNs);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -425,6 +439,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     int stage = 0;
     uint32_t phase = 0;
     for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride) {
+      const int turn = tile_at(p, i).m0 % kScaleRows / 32;  // 0 unless tiles are 32 or 64 tokens
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         const bool ok = mbar_wait_bounded(&sfull[stage], phase, p.err, kTimeoutNs);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -447,6 +462,15 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
             const uint4 b = *reinterpret_cast<const uint4*>(gx + r * kScaleKb + t * kScaleTile);
             const int o = 8 * t + 4 * r;
             x[o] = b.x, x[o + 1] = b.y, x[o + 2] = b.z, x[o + 3] = b.w;
+          }
+        }
+        if (turn) {  // a word is a group of 32 tokens: the tile's first one goes first
+#pragma unroll
+          for (int t = 0; t < kTilesKb; ++t) {
+            uint4 b = make_uint4(x[8 * t], x[8 * t + 1], x[8 * t + 2], x[8 * t + 3]);
+            if (turn & 1) b = make_uint4(b.y, b.z, b.w, b.x);
+            if (turn & 2) b = make_uint4(b.z, b.w, b.x, b.y);
+            x[8 * t] = b.x, x[8 * t + 1] = b.y, x[8 * t + 2] = b.z, x[8 * t + 3] = b.w;
           }
         }
         __syncwarp();
@@ -642,12 +666,14 @@ cudaError_t launch_mx4mm(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, c
   cfg.blockDim = dim3(kThreadsM);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)p.split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
   if (p.split == 1) {
     int grid = std::min(tiles, dev.sm_count);
     if (limit > 0) grid = std::min(grid, limit);
@@ -735,15 +761,19 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   memset(&p, 0, sizeof p);
   p.M = M;
   p.D = D;
+  p.K = K;
   p.F = F;
   p.F_shard = F_shard;
   p.tiles_f = (F_shard + BM - 1) / BM;
   const int all_f = K * p.tiles_f;
-  // Tokens of a tile: up to 128 the call's own, rounded up to the
-  // instruction's 16; beyond, 256 where that still gives every SM a tile, else
-  // 128 (a tile starts on a 128-row scale tile).
-  p.BN = M <= 128 ? (M + 15) / 16 * 16
-                  : ((long long)all_f * ((M + 255) / 256) >= dev.sm_count ? 256 : 128);
+  // Tokens of a tile: the call's own up to 128, rounded up to the
+  // instruction's 16, and beyond that 256; fewer, down to 32, while the tiles
+  // would fill at most half of the SMs (a tile starts on one of the 32-row
+  // groups of a scale tile).
+  p.BN = M <= 128 ? (M + 15) / 16 * 16 : 256;
+  const auto tiles_of = [&](int bn) { return (long long)all_f * ((M + bn - 1) / bn); };
+  if (M > 128 && tiles_of(256) < dev.sm_count) p.BN = 128;
+  while (p.BN > 32 && tiles_of(p.BN) * 2 <= dev.sm_count) p.BN = p.BN > 64 ? 64 : 32;
   p.tiles_m = (M + p.BN - 1) / p.BN;
   p.num_kb = (D + BK - 1) / BK;
   p.col_tiles = mx4_col_tiles(D, block);

@@ -40,7 +40,7 @@ class Mx4Tensor:
     ``tensor_scale``: one fp32 device value or None (nvfp4 only).
     """
 
-    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_format", "_tensor_scale", "_c")
+    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_format", "_tensor_scale", "_kind", "_c")
 
     def __init__(self, codes, scales, rows: int, cols: int, format: str, tensor_scale=None):
         _format(format)
@@ -57,6 +57,7 @@ class Mx4Tensor:
     def _set(self, codes, scales, rows, cols, format, tensor_scale):
         self._codes, self._scales, self._tensor_scale = codes, scales, tensor_scale
         self._rows, self._cols, self._format = rows, cols, format
+        self._kind = (rows, cols, format, codes.device)
         self._c = B.Mx4(codes.data_ptr(), scales.data_ptr(),
                         None if tensor_scale is None else tensor_scale.data_ptr())
 
@@ -159,13 +160,12 @@ def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
 def _shards(w_shards, cols, format, device):
     """The shards' structures, after checking that they make one matrix for this operand."""
     w0 = w_shards[0]
-    rows = w0._rows
-    if w0._cols != cols or w0._format != format:
-        raise ValueError(f"x is {format} with {cols} columns, the shards {w0._format} with "
-                         f"{w0._cols}")
+    kind = (w0._rows, cols, format, device)
+    if w0._kind != kind:
+        raise ValueError(f"x is {format} with {cols} columns on {device}, the shards {w0!r} on "
+                         f"{w0._codes.device}")
     for w in w_shards:
-        if w._rows != rows or w._cols != cols or w._format != format or \
-                w._codes.device != device:
+        if w._kind != kind:
             raise ValueError("need shards of one shape, format and device")
     return (B.Mx4 * len(w_shards))(*[w._c for w in w_shards])
 
@@ -192,16 +192,27 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
     if stream is not None:
         with _on(stream, x.device):
             return linear(x, w_shards, x_scale, y_dtype)
+    # One token's product takes the GPU less time than this function: it makes
+    # the call itself, without the binding's marshalling.
+    M, D = x.shape
+    ld, unit = x.stride()
+    if unit != 1 and D > 1:
+        raise ValueError("x: need a matrix with unit stride along its rows")
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
-    M, D = _matrix(x)
     dev, K, w0 = x.device, len(w_shards), w_shards[0]
-    arr = _shards(w_shards, D, w0._format, dev)
-    _check_scale(x_scale, dev)
+    format, F = w0._format, w0._rows
+    arr = _shards(w_shards, D, format, dev)
+    if x_scale is not None:
+        _check_scale(x_scale, dev)
     # scratch of this call alone: the allocator hands it on in stream order
-    ws = torch.empty(-(-M * (D // 2) // 256) * 256 + _scale_bytes(M, D, w0._format),
-                     dtype=torch.uint8, device=dev)
-    y = torch.empty(M, K * w0._rows, dtype=y_dtype, device=dev)
-    B.dp_allgather_linear_mx4(x, M, D, _row_stride(x), _code(x), x_scale, arr, K, w0._rows,
-                              FORMATS[w0._format], y, _DT[y_dtype], ws, ws.numel())
+    nbytes = -(-M * (D // 2) // 256) * 256 + _scale_bytes(M, D, format)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
+    st = (B._lib or B.load()).dp_allgather_linear_mx4(
+        x.data_ptr(), M, D, ld if M > 1 and ld > D else D, _code(x),
+        None if x_scale is None else x_scale.data_ptr(), arr, K, F, FORMATS[format],
+        y.data_ptr(), _DT[y_dtype], ws.data_ptr(), nbytes, B._stream(None))
+    if st:
+        raise B.DpError(st, "dp_allgather_linear_mx4")
     return y

@@ -203,7 +203,7 @@ PRODUCTS = [  # M, D, K, F_shard
     (1, 32, 1, 16), (1, 256, 1, 128), (5, 96, 2, 48), (16, 512, 8, 64), (17, 1056, 3, 144),
     (128, 512, 8, 64), (129, 320, 2, 256), (255, 2048, 4, 80), (300, 4096, 1, 128),
     (1, 4096, 8, 512), (700, 288, 8, 512), (2100, 512, 4, 400), (5000, 160, 5, 336),
-    (40, 96, 16, 2048),
+    (40, 96, 16, 2048), (100, 704, 2, 272), (200, 2048, 1, 512), (64, 1024, 8, 16),
 ]
 
 
