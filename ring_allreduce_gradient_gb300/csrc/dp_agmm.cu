@@ -831,34 +831,26 @@ namespace dpl {
 bool encode_kmajor_bytes(CUtensorMap* map, const void* base, int rows, int row_bytes,
                          int box_rows) {
   if (!get_encoder()) return false;
-  const MapKey key{reinterpret_cast<uintptr_t>(base), rows, row_bytes, box_rows, 5};
-  return cached_map(map, key, [&](CUtensorMap* m) {
-    cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-    cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-  });
+  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_output_shards(CUtensorMap* map, void* base, int M, int K, int F_shard, int box_rows) {
   if (!get_encoder()) return false;
-  // the shards' number has its place in the key beside the box's height
-  const MapKey key{reinterpret_cast<uintptr_t>(base), M, F_shard, box_rows * 64 + K, 6};
-  return cached_map(map, key, [&](CUtensorMap* m) {
-    cuuint64_t dims[3] = {(cuuint64_t)F_shard, (cuuint64_t)K, (cuuint64_t)M};
-    cuuint64_t strides[2] = {(cuuint64_t)F_shard * 2, (cuuint64_t)K * (cuuint64_t)F_shard * 2};
-    cuuint32_t box[3] = {128, 1, (cuuint32_t)box_rows};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-  });
+  cuuint64_t dims[3] = {(cuuint64_t)F_shard, (cuuint64_t)K, (cuuint64_t)M};
+  cuuint64_t strides[2] = {(cuuint64_t)F_shard * 2, (cuuint64_t)K * (cuuint64_t)F_shard * 2};
+  cuuint32_t box[3] = {128, 1, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace dpl

@@ -110,7 +110,7 @@ __device__ __forceinline__ void tmem_st_wait() {
 }  // namespace dpk
 
 namespace dpl {
-// An operand map for packed 4-bit values (cached; false where it cannot be encoded).
+// An operand map for packed 4-bit values; false where it cannot be encoded.
 bool encode_kmajor_bytes(CUtensorMap* map, const void* base, int rows, int row_bytes,
                          int box_rows);
 // An output map of bf16 y [M, K * F_shard] as (f of a shard, shard, row): boxes

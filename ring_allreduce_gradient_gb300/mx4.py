@@ -123,15 +123,20 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
                 t.stride() != x0.stride():
             raise ValueError("need shards of one shape, dtype, device and row stride")
     dev = x0.device
-    _check_scale(tensor_scale, dev)
+    if tensor_scale is not None:
+        _check_scale(tensor_scale, dev)
     K = len(xs)
     R, L = (cols, K * rows) if transpose else (K * rows, cols)
     codes = torch.empty((R, L // 2), dtype=torch.uint8, device=dev)
     scales = torch.empty(_scale_bytes(R, L, format), dtype=torch.uint8, device=dev)
-    B.dp_mx4_quantize(xs, K, rows, cols, _row_stride(x0), _code(x0), fmt, transpose, tensor_scale,
-                      codes, scales)
     q = Mx4Tensor.__new__(Mx4Tensor)
     q._set(codes, scales, R, L, format, tensor_scale)
+    c = q._c
+    st = (B._lib or B.load()).dp_mx4_quantize(
+        B._parray(xs), K, rows, cols, _row_stride(x0), _code(x0), fmt, 1 if transpose else 0,
+        c.tensor_scale, c.codes, c.scales, B._stream(None))
+    if st:
+        raise B.DpError(st, "dp_mx4_quantize")
     return q
 
 
@@ -151,9 +156,15 @@ def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     if stream is not None:
         with _on(stream, q._codes.device):
             return dequantize(q, dtype)
-    out = torch.empty(q._rows, q._cols, dtype=dtype, device=q._codes.device)
-    B.dp_mx4_dequantize(q._codes, q._scales, q._rows, q._cols, FORMATS[q._format],
-                        q._tensor_scale, out, _code(out))
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    out = torch.empty((q._rows, q._cols), dtype=dtype, device=q._codes.device)
+    c = q._c
+    st = (B._lib or B.load()).dp_mx4_dequantize(c.codes, c.scales, q._rows, q._cols,
+                                                FORMATS[q._format], c.tensor_scale,
+                                                out.data_ptr(), _DT[dtype], B._stream(None))
+    if st:
+        raise B.DpError(st, "dp_mx4_dequantize")
     return out
 
 
