@@ -711,13 +711,9 @@ bool clash(const Span& a, const Span& b) {
 
 namespace {
 
-// The product's checks and launch parameters; nothing is enqueued.  *tiles is
-// 0 where there is nothing to multiply (then *zero_bytes of y are to be zeroed).
-dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, int K, int F_shard,
-                    dp_mx4_format_t format, void* y, dp_dtype_t y_dtype, dph::DeviceInfo* devp,
-                    Mx4mmParams* pp, int* tilesp, size_t* zero_bytes) {
-  *tilesp = 0;
-  *zero_bytes = 0;
+// The product's checks, on the host alone.
+dp_status_t check_args(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, int K,
+                       int F_shard, dp_mx4_format_t format, void* y, dp_dtype_t y_dtype) {
   if (!x || !w_shards || K < 1 || K > DP_MAX_K) return DP_ERR_INVALID_ARG;
   if (M < 0 || D < 0 || F_shard < 0) return DP_ERR_INVALID_ARG;
   if (format != DP_MXFP4 && format != DP_NVFP4) return DP_ERR_UNSUPPORTED;
@@ -727,8 +723,7 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
     return DP_ERR_UNSUPPORTED;
   if (!aligned(y, 16)) return DP_ERR_UNSUPPORTED;
   const bool mx = format == DP_MXFP4;
-  const int F = K * F_shard, block = mx4_block(format);
-  const size_t ysz = (size_t)M * F * (y_dtype == DP_FP32 ? 4 : 2);
+  const size_t ysz = (size_t)M * K * F_shard * (y_dtype == DP_FP32 ? 4 : 2);
   if (!y && ysz) return DP_ERR_INVALID_ARG;
   const Span out = span_of(y, ysz);
   const auto check = [&](const dp_mx4_t& a, int rows) -> dp_status_t {
@@ -746,7 +741,19 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   };
   dp_status_t st = check(*x, M);
   for (int k = 0; k < K && st == DP_OK; ++k) st = check(w_shards[k], F_shard);
-  if (st != DP_OK) return st;
+  return st;
+}
+
+// The launch parameters of a checked product; nothing is enqueued.  *tiles is
+// 0 where there is nothing to multiply (then *zero_bytes of y are to be zeroed).
+dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, int K, int F_shard,
+                    dp_mx4_format_t format, void* y, dp_dtype_t y_dtype, dph::DeviceInfo* devp,
+                    Mx4mmParams* pp, int* tilesp, size_t* zero_bytes) {
+  *tilesp = 0;
+  *zero_bytes = 0;
+  const bool mx = format == DP_MXFP4;
+  const int F = K * F_shard, block = mx4_block(format);
+  const size_t ysz = (size_t)M * F * (y_dtype == DP_FP32 ? 4 : 2);
   if (M == 0 || F == 0) return DP_OK;
   dph::DeviceInfo& dev = *devp;
   if (!dph::current_device(&dev)) return DP_ERR_CUDA;
@@ -829,8 +836,9 @@ dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D, const dp_mx
   Mx4mmParams p;
   int tiles;
   size_t zero;
-  const dp_status_t st =
-      prepare(x, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
+  dp_status_t st = check_args(x, M, D, w_shards, K, F_shard, format, y, y_dtype);
+  if (st == DP_OK)
+    st = prepare(x, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
   if (st != DP_OK) return st;
   p.y = y;
   return enqueue(p, tiles, zero, format, dev, reinterpret_cast<cudaStream_t>(stream));
@@ -859,13 +867,9 @@ dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long long ld, d
   if (st != DP_OK) return st;
   if (workspace_bytes < need || (!workspace && need)) return DP_ERR_INVALID_ARG;
   const dp_mx4_t q{workspace, static_cast<uint8_t*>(workspace) + codes_bytes(M, D), x_scale};
-  dph::DeviceInfo dev;
-  Mx4mmParams p;
-  int tiles;
-  size_t zero;
   // everything is checked before the first launch; the workspace, written by
-  // the quantisation, must leave the weights alone too
-  st = prepare(&q, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
+  // the quantisation, must leave the weights alone too, and y the unquantised x
+  st = check_args(&q, M, D, w_shards, K, F_shard, format, y, y_dtype);
   if (st != DP_OK) return st;
   const Span ws = span_of(workspace, need);
   size_t sbytes = 0;
@@ -875,10 +879,16 @@ dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long long ld, d
         clash(ws, span_of(w_shards[k].scales, sbytes)) ||
         (w_shards[k].tensor_scale && clash(ws, span_of(w_shards[k].tensor_scale, 4))))
       return DP_ERR_ALIAS;
-  if (M > 0 && D > 0 && x &&
-      clash(span_of(x, ((size_t)(M - 1) * (size_t)(ld > 0 ? ld : 0) + D) * (x_dtype == DP_FP32 ? 4 : 2)),
+  if (M > 0 && D > 0 && x && ld >= D &&
+      clash(span_of(x, ((size_t)(M - 1) * (size_t)ld + D) * (x_dtype == DP_FP32 ? 4 : 2)),
             span_of(y, (size_t)M * K * F_shard * (y_dtype == DP_FP32 ? 4 : 2))))
     return DP_ERR_ALIAS;
+  dph::DeviceInfo dev;
+  Mx4mmParams p;
+  int tiles;
+  size_t zero;
+  st = prepare(&q, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
+  if (st != DP_OK) return st;
   st = dp_mx4_quantize(&x, 1, M, D, ld, x_dtype, format, 0, x_scale, workspace,
                        const_cast<void*>(q.scales), stream);
   if (st != DP_OK) return st;

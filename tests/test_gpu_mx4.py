@@ -336,3 +336,27 @@ def test_backward_products_are_the_gradients_of_the_decoded_forward():
         e = np.zeros_like(w)
         e[f, j] = 1
         assert loss(x, w + e) - loss(x, w) == float(dw[f, j])
+
+
+def test_counts_past_32_bits():
+    """More than 2^31 elements of x and of y: the last rows are those of a call on them alone."""
+    rows, cols = (1 << 20) + 128 * 9, 2048
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    tail = dev(np.random.default_rng(1).standard_normal((256, cols)), torch.bfloat16)
+    x[-256:] = tail
+    q, ref = mx4.quantize(x, "nvfp4"), mx4.quantize(tail, "nvfp4")
+    assert x.numel() > 2 ** 31
+    assert torch.equal(q.codes[-256:], ref.codes) and not q.codes[:-256].any()
+    assert torch.equal(q.scales[-ref.scales.numel():], ref.scales)
+    back = mx4.dequantize(q)
+    assert torch.equal(back[-256:], mx4.dequantize(ref))
+    del back, q
+    t = mx4.quantize(x, "mxfp4", transpose=True)
+    ref = mx4.quantize(tail, "mxfp4", transpose=True)
+    assert torch.equal(t.codes[:, -128:], ref.codes)
+    del t
+    w = [mx4.quantize(dev(np.random.default_rng(2).standard_normal((2048, 32))), "mxfp4")]
+    a = x[:, :32]                        # rows 2048 elements apart
+    y = mx4.linear(a, w)
+    assert y.numel() > 2 ** 31
+    assert torch.equal(y[-256:], mx4.linear(tail[:, :32], w)) and not y[:-256].any()
