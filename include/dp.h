@@ -575,9 +575,9 @@ DP_API dp_status_t dp_reducer_wait(dp_reducer_t* r, dp_stream_t stream);
  *   coef = min(1, max_norm / (norm + 1e-6)), or NaN when norm is not finite
  * norm and coef: one device float each; either may be NULL, not both.
  * max_norm > 0 (infinity: coef is 1).  An empty list has norm 0.
- * Squares are summed in fp32 over 32 elements and in double beyond; the
- * order is fixed by the sizes alone, so a list gives the same bits under any
- * CTA limit.  A gradient above 1.8e19 in magnitude overflows its square and
+ * Squares are summed in fp32 over 32 elements, pairs of such sums are added
+ * in fp32, and the rest is in double; the order is fixed by the sizes and
+ * alignments, so a list gives the same bits under any CTA limit.  A gradient above 1.8e19 in magnitude overflows its square and
  * makes the norm infinite.
  *
  * workspace: device memory of at least dp_grad_norm_workspace_size(n) bytes,
