@@ -789,9 +789,11 @@ DP_API int dp_get_collective_variant(void);
  * Process-wide upper bounds on the CTAs one launch may use: gemm_ctas for
  * the tensor-core kernels (dp_allgather_matmul, dp_matmul_*,
  * dp_wgrad_reduce_scatter*; the weight gradient's workspace size follows the
- * limit), stream_ctas
- * for the streaming collectives (reduce-scatter, all-gather, all-reduce,
- * accumulate, bucket and variable-length kernels); 0 means no limit (the
+ * limit; dp_allgather_matmul_mx4 and dp_allgather_linear_mx4, which where they
+ * split a tile over a cluster of 2, 4 or 8 CTAs use one cluster at least),
+ * stream_ctas for the streaming collectives (reduce-scatter, all-gather,
+ * all-reduce, accumulate, bucket and variable-length kernels), the gradient
+ * norm, AdamW and the 4-bit quantisation; 0 means no limit (the
  * default: one resident grid over every SM).  Lets a caller leave SMs free
  * for a kernel on another stream -- the resource-partitioning experiment of
  * "Optimizing ML Concurrent Computation and Communication with GPU DMA

@@ -17,8 +17,7 @@
 //   warp 0      W producer: 128 rows x 256 values (128 bytes) by TMA
 //   warp 2      X producer: BN rows x 256 values; also allocates TMEM
 //   warp 3      scales' producer: the rows' 512-byte scale tiles, 16 bytes a lane
-//               by cp.async (as three bulk copies a stage they cost more than
-//               W and X together: 193 us without them, 225 with)
+//               by cp.async, ahead of the operands
 //   warps 12-15 scales into TMEM: lane l of each 32-lane quarter takes row l of a
 //               scale tile (16 bytes: four columns), tcgen05.st
 //   warp 1      MMA issuer: four MMAs of 64 values a stage
@@ -29,11 +28,21 @@
 // has its own, so they are overwritten only when the stage is.  With the
 // scales two accumulators of 256 columns do not fit.
 //
-// The scales go through registers because tcgen05.cp, which copies a scale
-// tile straight from shared memory, takes its turn with the MMAs: x[8192,8192]
-// . w[8192,8192]^T took 500 us (nvfp4, 12 copies a stage) and 348 us (mxfp4, 6)
-// with it, and 208 / 202 us with the copies of all stages but the first left
-// out, where operand intake (54 KiB a stage) is the limit.
+// Measured (GB300, launches in a CUDA graph): x[8192,4096] . w[4096,4096]^T
+// 49 us in mxfp4 (5.6 PFLOP/s) and 60 us in nvfp4 (4.6); x[8192,8192] .
+// w[8192,8192]^T 162 and 191 us.  What bounds it: the MMAs alone (loads of all
+// stages but the first four left out) take 139 us of the 162; the rest is
+// operand intake, 48 KiB of values a stage, and between tiles the 1300 clocks
+// in which the accumulator is drained.  nvfp4 has twice the scales: reading
+// them four times from shared memory, once for each quarter of TMEM, costs 20
+// us of its 191.  The steps that led here, on that product:
+//   * scales through registers (195 / 167 us, nvfp4 / mxfp4) instead of
+//     tcgen05.cp straight from shared memory (269 / 204 us): the copies take
+//     their turn with the MMAs, about 100 clocks each;
+//   * scales to shared memory by cp.async instead of three bulk copies a stage:
+//     233 -> 216 and 225 -> 195 us;
+//   * output through 4 KiB of shared memory a half and TMA instead of 4-byte
+//     stores, which held the MMA issuer up for half a tile.
 //
 // Few tiles: the blocks of d are split over a cluster of 2, 4 or 8 CTAs,
 // whose fp32 partial sums meet in shared memory: each CTA adds a share of the
@@ -154,7 +163,8 @@ __device__ __forceinline__ uint32_t idesc_fp4(bool mx, int n) {
 // The MMA and its commits are run by a whole warp and issued by one elected
 // lane: with every operand the same in all lanes the compiler keeps them in
 // uniform registers.  Inside an if (lane == 0) each MMA took 73 clocks to
-// issue, and a stage 788 clocks for 548 of MMAs.
+// issue, and a stage 788 clocks for 548 of MMAs (x[8192,8192] .
+// w[8192,8192]^T, mxfp4: 194 us, against 166).
 template <bool MX>
 __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                         uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
@@ -570,9 +580,11 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
 #pragma unroll
       for (int c = 0; c < 8; c += 2) {
         uint32_t r[32];
-        if (c < cn) DP_TMEM_LD_X32(tbase + (uint32_t)(c * 16), r);
-        tmem_ld_wait();
-        pack32(r, c);
+        if (c < cn) {  // an odd last chunk reads 16 columns too many, which stay unused
+          DP_TMEM_LD_X32(tbase + (uint32_t)(c * 16), r);
+          tmem_ld_wait();
+          pack32(r, c);
+        }
       }
       tc_fence_before();
       __syncwarp();
