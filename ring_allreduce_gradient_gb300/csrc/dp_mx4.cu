@@ -14,14 +14,17 @@
 // an infinity has a NaN scale.
 //
 // Bound by memory: 2 bytes read and 0.53 / 0.56 written for each bf16 value.
-// Rows form: a warp takes up to 1024 columns of a row with all its loads
+// Rows form: a warp takes up to 2048 columns of a row with all its loads
 // issued first, a lane sixteen columns of each 512, so a block is one lane
 // (nvfp4) or two.  Transposed form: blocks run down the columns, so a lane
 // takes two neighbouring columns and reads 64 rows of them (a warp reads 128
 // contiguous bytes of each bf16 row): a block's largest value needs no
 // exchange, a lane ends with 32 contiguous bytes of each of its two output
 // rows, and the four warps of a CTA, one below the other, with a 128-byte
-// line.  Neither goes through shared memory.
+// line.  Neither goes through shared memory.  Measured on 8192 x 4096 bf16
+// (GB300, launches in a CUDA graph): rows 14.1 us to nvfp4 and 11.2 to mxfp4
+// (6.1 and 7.7 TB/s, part of it from L2), transposed 17.9 and 12.7, decoding
+// 12.6; the nvfp4 forms are held by their arithmetic, two divisors a block.
 
 #include "dp_launch.h"
 #include "dp_mx4.cuh"
@@ -101,9 +104,9 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 // rounded once, together with x lo, so the result is the rounded quotient
 // unless the quotient lies within 2^-46 of a midpoint between two fp32 values;
 // a quotient that is an fp32 value, a tie between two codes among them, comes
-// out exactly.  Measured against __fdiv_rn for every value: 8192 x 4096 bf16 to
-// nvfp4 43.9 us with it.  Divisors too far from 1 for the two words take the
-// division.
+// out exactly.  (8192 x 4096 bf16 to nvfp4, in the kernel's first form: 43.9 us
+// with __fdiv_rn for every value, 23.5 us with this and the loads issued
+// first.)  Divisors too far from 1 for the two words take the division.
 struct Divisor {
   float d, hi, lo;
   bool near;
@@ -117,6 +120,26 @@ struct Divisor {
     return near ? __fmaf_rn(x, hi, __fmul_rn(x, lo)) : __fdiv_rn(x, d);
   }
 };
+
+// Two fp32 operations in one instruction, each lane of the pair rounded by itself.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 // The tensor's scale, and a block's: its byte from the block's largest
 // magnitude, and eight of its values to codes.
@@ -136,8 +159,9 @@ struct Scale<kMxBlock> {
   }
   __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
     float w[8];
+    const uint64_t ff = pair(f, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __fmul_rn(v[i], f);
+    for (int i = 0; i < 8; i += 2) unpair(mul2(pair(v[i], v[i + 1]), ff), w[i], w[i + 1]);
     return zero ? 0u : pack_e2m1(w);
   }
 };
@@ -158,8 +182,12 @@ struct Scale<kNvBlock> {
   __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
     float w[8];
     if (by.near) {
+      const uint64_t hi = pair(by.hi, by.hi), lo = pair(by.lo, by.lo);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = __fmaf_rn(v[i], by.hi, __fmul_rn(v[i], by.lo));
+      for (int i = 0; i < 8; i += 2) {
+        const uint64_t x = pair(v[i], v[i + 1]);
+        unpair(fma2(x, hi, mul2(x, lo)), w[i], w[i + 1]);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = __fdiv_rn(v[i], step);
@@ -168,27 +196,72 @@ struct Scale<kNvBlock> {
   }
 };
 
-// Sixteen consecutive elements, widened: from a 32-byte boundary.
-__device__ __forceinline__ void load16(const float* p, float (&v)[2][8]) {
+// Sixteen consecutive elements as they were loaded, from a 32-byte boundary:
+// bf16 ones stay in pairs until they are needed, for their registers' sake.
+// Magnitudes order as their bits, NaN above all.
+template <typename T>
+struct Sixteen;
+
+template <>
+struct Sixteen<float> {
+  float v[16];
+  __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(v[h][0]), "=f"(v[h][1]), "=f"(v[h][2]), "=f"(v[h][3]), "=f"(v[h][4]),
-                   "=f"(v[h][5]), "=f"(v[h][6]), "=f"(v[h][7])
-                 : "l"(p + 8 * h));
-}
-__device__ __forceinline__ void load16(const uint16_t* p, float (&v)[2][8]) {
-  uint32_t r[8];
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7])
-               : "l"(p));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i / 4][2 * (i % 4)] = bf16lo(r[i]);
-    v[i / 4][2 * (i % 4) + 1] = bf16hi(r[i]);
+    for (int h = 0; h < 16; h += 8)
+      asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=f"(v[h]), "=f"(v[h + 1]), "=f"(v[h + 2]), "=f"(v[h + 3]), "=f"(v[h + 4]),
+                     "=f"(v[h + 5]), "=f"(v[h + 6]), "=f"(v[h + 7])
+                   : "l"(p + h));
   }
+  __device__ __forceinline__ void each(const float* p, bool in) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = in ? __ldg(p + i) : 0.0f;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t = max(t, __float_as_uint(v[i]) & 0x7fffffffu);
+    return t;
+  }
+  __device__ __forceinline__ void widen(int half, float (&w)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = v[8 * half + i];
+  }
+};
+
+// The larger magnitude of each half of two pairs of bf16.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t t, uint32_t v) {
+  return __vmaxu2(t, v & 0x7fff7fffu);
 }
+
+template <>
+struct Sixteen<uint16_t> {
+  uint32_t r[8];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+  }
+  __device__ __forceinline__ void each(const uint16_t* p, bool in) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r[i] = in ? (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16 : 0u;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max_abs2(t, r[i]);
+    return max(t & 0xffff0000u, t << 16);
+  }
+  __device__ __forceinline__ void widen(int half, float (&w)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[2 * i] = bf16lo(r[4 * half + i]);
+      w[2 * i + 1] = bf16hi(r[4 * half + i]);
+    }
+  }
+};
 
 // Where the four scales of (row, column tile) lie.
 __device__ __forceinline__ size_t scale_at(int row, int tile, int col_tiles) {
@@ -203,32 +276,34 @@ template <typename T, int BLOCK, int G>
 __device__ __forceinline__ void quant_row(const QuantParams& p, int r, int e0, bool vec, float t,
                                           const Divisor& by_t) {
   const int lane = threadIdx.x & 31;
-  float v[G][2][8];
+  Sixteen<T> v[G];
   const T* x = r < p.R ? row_at<T>(p, r) : nullptr;
   if (x && vec && e0 + G * 512 <= p.L) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) load16(x + e0 + g * 512 + lane * 16, v[g]);
+    for (int g = 0; g < G; ++g) v[g].load(x + e0 + g * 512 + lane * 16);
   } else {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int e = e0 + g * 512 + lane * 16;
-      const bool in = x && e < p.L;  // L is a multiple of 32: all sixteen are inside or none
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[g][i / 8][i % 8] = in ? widen_scalar(x, e + i) : 0.0f;
+      v[g].each(x + e, x && e < p.L);  // L is a multiple of 32: all sixteen are inside or none
     }
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int e = e0 + g * 512 + lane * 16;
     const bool in = x && e < p.L;
-    uint32_t top = 0;  // magnitudes order as their bits, NaN above all
-#pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[g][i / 8][i % 8]) & 0x7fffffffu);
+    uint32_t top = v[g].top();
     if (BLOCK == kMxBlock) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     const Scale<BLOCK> s(__uint_as_float(top), t, by_t);
+    uint32_t c[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float w[8];
+      v[g].widen(h, w);
+      c[h] = s.codes(w);
+    }
     if (in)
-      *reinterpret_cast<uint2*>(p.codes + (size_t)r * (p.L / 2) + e / 2) =
-          make_uint2(s.codes(v[g][0]), s.codes(v[g][1]));
+      *reinterpret_cast<uint2*>(p.codes + (size_t)r * (p.L / 2) + e / 2) = make_uint2(c[0], c[1]);
     const int b = e / BLOCK;
     if (b / 4 < p.col_tiles && (BLOCK == kNvBlock || lane % 2 == 0))
       p.scales[scale_at(r, b / 4, p.col_tiles) + b % 4] = in ? (uint8_t)s.byte : (uint8_t)0;
@@ -265,6 +340,25 @@ __device__ __forceinline__ uint32_t load2(const uint16_t* x, int c, int last) {
 }
 __device__ __forceinline__ float part(float2 v, int j) { return j ? v.y : v.x; }
 __device__ __forceinline__ float part(uint32_t v, int j) { return j ? bf16hi(v) : bf16lo(v); }
+
+// The two columns' largest magnitudes over N rows.
+template <int N>
+__device__ __forceinline__ void tops(const float2* v, uint32_t (&t)[2]) {
+  t[0] = t[1] = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    t[0] = max(t[0], __float_as_uint(v[i].x) & 0x7fffffffu);
+    t[1] = max(t[1], __float_as_uint(v[i].y) & 0x7fffffffu);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tops(const uint32_t* v, uint32_t (&t)[2]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max_abs2(m, v[i]);
+  t[0] = m << 16;
+  t[1] = m & 0xffff0000u;
+}
 
 template <typename T>
 struct Pair;
@@ -311,14 +405,12 @@ __global__ void __launch_bounds__(kThreads) quant_cols_kernel(const __grid_const
         if (FAST || p.whole) x += p.ld;
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int b = 0; b < 32 / BLOCK; ++b) {
+        uint32_t top[2];
+        tops<BLOCK>(v + b * BLOCK, top);
 #pragma unroll
-        for (int b = 0; b < 32 / BLOCK; ++b) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < BLOCK; ++i)
-            top = max(top, __float_as_uint(part(v[b * BLOCK + i], j)) & 0x7fffffffu);
-          const Scale<BLOCK> s(__uint_as_float(top), t, by_t);
+        for (int j = 0; j < 2; ++j) {
+          const Scale<BLOCK> s(__uint_as_float(top[j]), t, by_t);
           if (c + j < p.R) sc[j] |= s.byte << (8 * (h * (32 / BLOCK) + b));
 #pragma unroll
           for (int i = 0; i < BLOCK / 8; ++i) {
@@ -328,6 +420,7 @@ __global__ void __launch_bounds__(kThreads) quant_cols_kernel(const __grid_const
             code[j][4 * h + b * (BLOCK / 8) + i] = s.codes(w);
           }
         }
+      }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -415,10 +508,13 @@ cudaError_t launch(KernelT kernel, const P& p, long long blocks, cudaStream_t s)
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// Whether a warp takes 1024 columns at once in the rows form and in decoding:
-// all its loads are in flight together, where rows are that long and enough of
-// them to fill the GPU; short calls spread wider, with 512 and 256.
-bool wide(long long rows, long long cols) { return cols >= 1024 && rows * cols >= (1ll << 21); }
+// Whether there is work enough to fill the GPU with warps that take `span`
+// columns of a row at once.  All loads of a warp are in flight together: 8192 x
+// 4096 bf16 to nvfp4 18.8 us with 512 columns, 15.7 with 1024, 14.1 with 2048;
+// short calls spread wider instead.
+bool wide(long long rows, long long cols, int span) {
+  return cols >= span && rows * cols >= (1ll << 11) * span;
+}
 
 template <typename T, int BLOCK>
 cudaError_t quantize(const QuantParams& p, bool transpose, cudaStream_t s) {
@@ -430,14 +526,16 @@ cudaError_t quantize(const QuantParams& p, bool transpose, cudaStream_t s) {
       return launch(quant_cols_kernel<T, BLOCK, true>, p, blocks, s);
     return launch(quant_cols_kernel<T, BLOCK, false>, p, blocks, s);
   }
-  if (wide(p.R, p.L))
+  if (wide(p.R, p.L, 2048))
+    return launch(quant_rows_kernel<T, BLOCK, 4>, p, rows / kWarps * ceil_div(cols, 2048), s);
+  if (wide(p.R, p.L, 1024))
     return launch(quant_rows_kernel<T, BLOCK, 2>, p, rows / kWarps * ceil_div(cols, 1024), s);
   return launch(quant_rows_kernel<T, BLOCK, 1>, p, rows / kWarps * ceil_div(cols, 512), s);
 }
 
 template <typename T, int BLOCK>
 cudaError_t decode(const DecodeParams& p, cudaStream_t s) {
-  if (wide(p.R, p.L))
+  if (wide(p.R, p.L, 1024))
     return launch(decode_kernel<T, BLOCK, 4>, p, ceil_div(p.R, kWarps) * ceil_div(p.L, 1024), s);
   return launch(decode_kernel<T, BLOCK, 1>, p, ceil_div(p.R, kWarps) * ceil_div(p.L, 256), s);
 }

@@ -96,7 +96,8 @@ def check(q, x64, fmt, t=1.0):
     assert np.all(np.abs(mine - got) <= 2 * U * np.abs(mine))
 
 
-SHAPES = [(1, 32), (3, 64), (127, 96), (128, 256), (130, 512 + 32), (257, 1056)]
+SHAPES = [(1, 32), (3, 64), (127, 96), (128, 256), (130, 512 + 32), (257, 1056), (2050, 1120),
+          (2049, 2080)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
