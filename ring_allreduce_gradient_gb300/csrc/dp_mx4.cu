@@ -180,6 +180,7 @@ struct Scale<kNvBlock> {
     by = Divisor(step);
   }
   __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
+    if (!(step > 0.0f)) return 0u;  // a block of zeros, or a NaN step
     float w[8];
     if (by.near) {
       const uint64_t hi = pair(by.hi, by.hi), lo = pair(by.lo, by.lo);
@@ -192,7 +193,7 @@ struct Scale<kNvBlock> {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = __fdiv_rn(v[i], step);
     }
-    return step > 0.0f ? pack_e2m1(w) : 0u;  // also where the step is NaN
+    return pack_e2m1(w);
   }
 };
 
@@ -295,15 +296,16 @@ __device__ __forceinline__ void quant_row(const QuantParams& p, int r, int e0, b
     uint32_t top = v[g].top();
     if (BLOCK == kMxBlock) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     const Scale<BLOCK> s(__uint_as_float(top), t, by_t);
-    uint32_t c[2];
+    if (in) {
+      uint32_t c[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float w[8];
-      v[g].widen(h, w);
-      c[h] = s.codes(w);
-    }
-    if (in)
+      for (int h = 0; h < 2; ++h) {
+        float w[8];
+        v[g].widen(h, w);
+        c[h] = s.codes(w);
+      }
       *reinterpret_cast<uint2*>(p.codes + (size_t)r * (p.L / 2) + e / 2) = make_uint2(c[0], c[1]);
+    }
     const int b = e / BLOCK;
     if (b / 4 < p.col_tiles && (BLOCK == kNvBlock || lane % 2 == 0))
       p.scales[scale_at(r, b / 4, p.col_tiles) + b % 4] = in ? (uint8_t)s.byte : (uint8_t)0;

@@ -40,7 +40,7 @@ class Mx4Tensor:
     ``tensor_scale``: one fp32 device value or None (nvfp4 only).
     """
 
-    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_format", "_tensor_scale", "_kind", "_c")
+    __slots__ = ("_codes", "_scales", "_store", "_tensor_scale", "_kind", "_c")
 
     def __init__(self, codes, scales, rows: int, cols: int, format: str, tensor_scale=None):
         _format(format)
@@ -52,24 +52,48 @@ class Mx4Tensor:
         if scales.device != codes.device:
             raise ValueError("codes and scales on one device")
         _check_scale(tensor_scale, codes.device)
-        self._set(codes, scales, rows, cols, format, tensor_scale)
-
-    def _set(self, codes, scales, rows, cols, format, tensor_scale):
-        self._codes, self._scales, self._tensor_scale = codes, scales, tensor_scale
-        self._rows, self._cols, self._format = rows, cols, format
+        self._codes, self._scales, self._store = codes, scales, None
+        self._tensor_scale = tensor_scale
         self._kind = (rows, cols, format, codes.device)
         self._c = B.Mx4(codes.data_ptr(), scales.data_ptr(),
                         None if tensor_scale is None else tensor_scale.data_ptr())
 
-    codes = property(lambda self: self._codes)
-    scales = property(lambda self: self._scales)
-    rows = property(lambda self: self._rows)
-    cols = property(lambda self: self._cols)
-    format = property(lambda self: self._format)
+    @classmethod
+    def _empty(cls, rows, cols, format, tensor_scale, device):
+        """A matrix to be written, codes and scales in one allocation."""
+        q = cls.__new__(cls)
+        n = -(-rows * (cols // 2) // 256) * 256
+        q._store = torch.empty(n + _scale_bytes(rows, cols, format), dtype=torch.uint8,
+                               device=device)
+        q._codes = q._scales = None      # views, made when they are asked for
+        q._tensor_scale = tensor_scale
+        q._kind = (rows, cols, format, device)
+        at = q._store.data_ptr()
+        q._c = B.Mx4(at, at + n, None if tensor_scale is None else tensor_scale.data_ptr())
+        return q
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            rows, cols = self.rows, self.cols
+            self._codes = self._store[:rows * (cols // 2)].view(rows, cols // 2)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            n = _scale_bytes(self.rows, self.cols, self.format)
+            self._scales = self._store[self._store.numel() - n:]
+        return self._scales
+
+    rows = property(lambda self: self._kind[0])
+    cols = property(lambda self: self._kind[1])
+    format = property(lambda self: self._kind[2])
+    device = property(lambda self: self._kind[3])
     tensor_scale = property(lambda self: self._tensor_scale)
 
     def __repr__(self):
-        return f"Mx4Tensor({self._rows} x {self._cols}, {self._format})"
+        return f"Mx4Tensor({self.rows} x {self.cols}, {self.format}, {self.device})"
 
 
 def _check_scale(scale, device):
@@ -127,10 +151,7 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
         _check_scale(tensor_scale, dev)
     K = len(xs)
     R, L = (cols, K * rows) if transpose else (K * rows, cols)
-    codes = torch.empty((R, L // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(_scale_bytes(R, L, format), dtype=torch.uint8, device=dev)
-    q = Mx4Tensor.__new__(Mx4Tensor)
-    q._set(codes, scales, R, L, format, tensor_scale)
+    q = Mx4Tensor._empty(R, L, format, tensor_scale, dev)
     c = q._c
     st = (B._lib or B.load()).dp_mx4_quantize(
         B._parray(xs), K, rows, cols, _row_stride(x0), _code(x0), fmt, 1 if transpose else 0,
@@ -153,16 +174,17 @@ def _row_stride(x) -> int:
 
 def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values a 4-bit matrix stands for."""
+    rows, cols, format, dev = q._kind
     if stream is not None:
-        with _on(stream, q._codes.device):
+        with _on(stream, dev):
             return dequantize(q, dtype)
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}")
-    out = torch.empty((q._rows, q._cols), dtype=dtype, device=q._codes.device)
+    out = torch.empty((rows, cols), dtype=dtype, device=dev)
     c = q._c
-    st = (B._lib or B.load()).dp_mx4_dequantize(c.codes, c.scales, q._rows, q._cols,
-                                                FORMATS[q._format], c.tensor_scale,
-                                                out.data_ptr(), _DT[dtype], B._stream(None))
+    st = (B._lib or B.load()).dp_mx4_dequantize(c.codes, c.scales, rows, cols, FORMATS[format],
+                                                c.tensor_scale, out.data_ptr(), _DT[dtype],
+                                                B._stream(None))
     if st:
         raise B.DpError(st, "dp_mx4_dequantize")
     return out
@@ -171,10 +193,9 @@ def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
 def _shards(w_shards, cols, format, device):
     """The shards' structures, after checking that they make one matrix for this operand."""
     w0 = w_shards[0]
-    kind = (w0._rows, cols, format, device)
+    kind = (w0._kind[0], cols, format, device)
     if w0._kind != kind:
-        raise ValueError(f"x is {format} with {cols} columns on {device}, the shards {w0!r} on "
-                         f"{w0._codes.device}")
+        raise ValueError(f"x is {format} with {cols} columns on {device}, the shards {w0!r}")
     for w in w_shards:
         if w._kind != kind:
             raise ValueError("need shards of one shape, format and device")
@@ -183,16 +204,17 @@ def _shards(w_shards, cols, format, device):
 
 def matmul(x: Mx4Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = x . w^T with w the row concatenation of the 4-bit shards."""
+    M, D, format, dev = x._kind
     if stream is not None:
-        with _on(stream, x._codes.device):
+        with _on(stream, dev):
             return matmul(x, w_shards, y_dtype)
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
-    dev, K = x._codes.device, len(w_shards)
-    arr = _shards(w_shards, x._cols, x._format, dev)
-    y = torch.empty(x._rows, K * w_shards[0]._rows, dtype=y_dtype, device=dev)
-    B.dp_allgather_matmul_mx4(x._c, x._rows, x._cols, arr, K, w_shards[0]._rows,
-                              FORMATS[x._format], y, _DT[y_dtype])
+    K = len(w_shards)
+    arr = _shards(w_shards, D, format, dev)
+    y = torch.empty((M, K * w_shards[0].rows), dtype=y_dtype, device=dev)
+    B.dp_allgather_matmul_mx4(x._c, M, D, arr, K, w_shards[0].rows, FORMATS[format], y,
+                              _DT[y_dtype])
     return y
 
 
@@ -211,8 +233,8 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
         raise ValueError("x: need a matrix with unit stride along its rows")
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
-    dev, K, w0 = x.device, len(w_shards), w_shards[0]
-    format, F = w0._format, w0._rows
+    dev, K = x.device, len(w_shards)
+    F, _, format, _ = w_shards[0]._kind
     arr = _shards(w_shards, D, format, dev)
     if x_scale is not None:
         _check_scale(x_scale, dev)
