@@ -361,3 +361,25 @@ def test_counts_past_32_bits():
     y = mx4.linear(a, w)
     assert y.numel() > 2 ** 31
     assert torch.equal(y[-256:], mx4.linear(tail[:, :32], w)) and not y[:-256].any()
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_a_stream_given_by_hand(as_handle):
+    """Every call on the stream it is given, its results allocated there."""
+    side = torch.cuda.Stream()
+    st = side.cuda_stream if as_handle else side
+    rng = np.random.default_rng(6)
+    x = dev(rng.standard_normal((48, 256)), torch.bfloat16)
+    w = dev(rng.standard_normal((64, 256)))
+    s = mx4.tensor_scale(x)
+    want = mx4.linear(x, [mx4.quantize(w, "nvfp4", s)], s)
+    side.wait_stream(torch.cuda.current_stream())
+    s2 = mx4.tensor_scale(x, stream=st)
+    wq = mx4.quantize(w, "nvfp4", s2, stream=st)
+    y = mx4.linear(x, [wq], s2, stream=st)
+    xq = mx4.quantize(x, "nvfp4", s2, stream=st)
+    y2 = mx4.matmul(xq, [wq], stream=st)
+    d = mx4.dequantize(xq, stream=st)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(s, s2) and torch.equal(y, want) and torch.equal(y2, want)
+    assert torch.equal(d, mx4.dequantize(mx4.quantize(x, "nvfp4", s)))

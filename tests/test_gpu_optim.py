@@ -328,3 +328,19 @@ def test_clipped_steps_follow_the_formula_over_a_run():
             travel[i] += 3 * U * np.abs(p) + 200 * U * (step + terms * 3e-3)
     for i in range(len(sizes)):
         assert np.all(np.abs(host(opt.params[i]) - ref[i][0]) <= travel[i])
+
+
+def test_a_stream_given_by_hand():
+    opt, _ = make([1000, 33], torch.float32, torch.float32, 0, step=0)
+    ref, _ = make([1000, 33], torch.float32, torch.float32, 0, step=0)
+    clip = optim.GradNorm(opt.grads, max_norm=0.01)
+    ref.step(grad_scale=optim.GradNorm(ref.grads, max_norm=0.01)()[1])
+    side = torch.cuda.Stream()
+    for st in (side, side.cuda_stream):
+        side.wait_stream(torch.cuda.current_stream())
+        coef = clip(stream=st)[1]
+        if st is side:
+            opt.step(grad_scale=coef, stream=st)
+        torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(opt.params + opt.exp_avg, ref.params + ref.exp_avg):
+        assert torch.equal(a, b)
