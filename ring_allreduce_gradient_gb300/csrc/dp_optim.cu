@@ -35,6 +35,7 @@
 #include <cstring>
 #include <mutex>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 namespace {
@@ -183,16 +184,13 @@ __device__ __forceinline__ float code_factor(float top) {
   return top > kTiny ? __fmul_rn(__frcp_rn(top), kE4m3Max) : (top <= kTiny ? 0.0f : top);
 }
 
-// CTAs on an SM: eight of four warps for fp32 parameters (64 registers, which
-// spills nothing on the aligned path; eight 8 Mi shards with 8-bit states 173
-// us, against 179 us at the 80 registers it would take), six for bf16 ones,
-// whose lane-by-lane path would spill at 64 (ragged bf16 list 109 us, against
-// 118 us).
-template <typename PT>
-constexpr int kAdamwCtas = sizeof(PT) == 4 ? 8 : 6;
+// Eight CTAs of four warps on an SM, which is 64 registers: eight 8 Mi shards
+// with 8-bit states 173 us, against 179 us at the 80 registers the kernel would
+// take; ragged bf16 parameters with 8-bit states 95 us, against 107 us.
+constexpr int kAdamwCtas = 8;
 
 template <typename PT, typename GT, bool S8, int CAP>
-__global__ void __launch_bounds__(kThreads, kAdamwCtas<PT>) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
+__global__ void __launch_bounds__(kThreads, kAdamwCtas) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
   const int lane = threadIdx.x & 31;
   const unsigned units = a.ustart[a.n];
   Hyper h{1.0f, a.beta1, a.omb1, a.beta2, a.omb2, a.eps, a.step_size, a.inv_root};
@@ -243,21 +241,27 @@ __global__ void __launch_bounds__(kThreads, kAdamwCtas<PT>) adamw_kernel(const _
         ld8(vp + o, v);
       }
     } else {
+      const auto load = [&](auto whole) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int o = i * 32 + lane;
-        const bool in = o < len;
-        p[i] = in ? widen_scalar(pp, o) : 0.0f;
-        g[i] = in ? widen_scalar(gp, o) : 0.0f;
-        if constexpr (S8) {
-          float none;
-          widen_e4m3x2(in ? (uint16_t)m8[o] : (uint16_t)0, m[i], none);
-          widen_e4m3x2(in ? (uint16_t)r8[o] : (uint16_t)0, v[i], none);
-        } else {
-          m[i] = in ? mp[o] : 0.0f;
-          v[i] = in ? vp[o] : 0.0f;
+        for (int i = 0; i < 8; ++i) {
+          const int o = i * 32 + lane;
+          const bool in = whole.value || o < len;
+          p[i] = in ? widen_scalar(pp, o) : 0.0f;
+          g[i] = in ? widen_scalar(gp, o) : 0.0f;
+          if constexpr (S8) {
+            float none;
+            widen_e4m3x2(in ? (uint16_t)m8[o] : (uint16_t)0, m[i], none);
+            widen_e4m3x2(in ? (uint16_t)r8[o] : (uint16_t)0, v[i], none);
+          } else {
+            m[i] = in ? mp[o] : 0.0f;
+            v[i] = in ? vp[o] : 0.0f;
+          }
         }
-      }
+      };
+      // without bounds where there are none to keep: 61 ragged bf16 tensors 109
+      // us, against 119 us
+      if (len == kUnit) load(std::true_type{});
+      else load(std::false_type{});
       if constexpr (S8) {
         ms = x.m_scale[b];
         rs = x.v_scale[b];
