@@ -24,9 +24,9 @@
 //   warps 4-11  epilogue: a warp takes 32 f and half of the tokens, packs its
 //               accumulator columns into registers, releases TMEM and stores
 //               while the next tile runs
-// TMEM: 256 accumulator columns (one tile) and 4 x 48 scale columns: a stage
-// has its own, so they are overwritten only when the stage is.  With the
-// scales two accumulators of 256 columns do not fit.
+// TMEM: 256 accumulator columns (one tile) and 4 x 48 scale columns (narrow
+// tiles: see Geo): a stage has its own, so they are overwritten only when the
+// stage is.  With the scales two accumulators of 256 columns do not fit.
 //
 // Measured (GB300, launches in a CUDA graph): x[8192,4096] . w[4096,4096]^T
 // 49 us in mxfp4 (5.6 PFLOP/s) and 60 us in nvfp4 (4.6); x[8192,8192] .
@@ -65,22 +65,36 @@ using namespace dpk;
 constexpr int BM = 128;          // weight rows of a tile
 constexpr int BK = 256;          // values of d per stage: one 128-byte swizzle row
 constexpr int kStep = 64;        // values of d per MMA
-constexpr int kMaxBN = 256;      // tokens of a tile
-constexpr int kStages = 4;
 constexpr uint32_t kStageW = BM * BK / 2;
-constexpr uint32_t kStageX = kMaxBN * BK / 2;
-constexpr uint32_t kStageSW = 4 * kScaleTile;      // 128 rows x 16 blocks (nvfp4)
-constexpr uint32_t kStageSX = 2 * 4 * kScaleTile;  // 256 rows
+constexpr uint32_t kStageSW = 4 * kScaleTile;  // 128 rows x 16 blocks (nvfp4)
 constexpr int kOutTokens = 16;   // tokens of one staged store of an epilogue half
 constexpr uint32_t kStageY = kOutTokens * BM * 2;  // per half
-constexpr size_t kBarBytes = 256;
-constexpr size_t kSmemBytes = 1024 +
-                              (size_t)kStages * (kStageW + kStageX + kStageSW + kStageSX) +
-                              2 * kStageY + kBarBytes;
-static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
+constexpr size_t kBarBytes = 512;
+
+// What follows from the widest tile (in tokens) of a kernel: a narrow tile's
+// stages are small, and what bounds it is how many weight bytes are on their
+// way.  Measured with 8 and 6 stages against 4 of the widest tile's: one token
+// times w[65536,8192] in nvfp4 52.2 us (5.8 TB/s), against 55.7 us; 128 tokens
+// times w[4096,4096] 8.9 us, against 9.7 us.
+template <int BNMAX>
+struct Geo {
+  static constexpr int kStages = BNMAX == 256 ? 4 : BNMAX == 128 ? 6 : 8;
+  static constexpr uint32_t kStageX = BNMAX * BK / 2;
+  static constexpr int kXTiles = BNMAX > 128 ? 2 : 1;  // 128-row scale tiles of X
+  static constexpr uint32_t kStageSX = kXTiles * 4 * kScaleTile;
+  static constexpr int kXCols = 4 * kXTiles;           // TMEM columns of a step's X scales
+  static constexpr int kScaleCol0 = BNMAX;             // first scale column
+  static constexpr int kScaleCols = 16 + 4 * kXCols;   // per stage: W's, then X's
+  static constexpr size_t kSmem = 1024 +
+                                  (size_t)kStages * (kStageW + kStageX + kStageSW + kStageSX) +
+                                  2 * kStageY + kBarBytes;
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+  static_assert(kScaleCol0 + kStages * kScaleCols <= 512, "TMEM columns");
+  static_assert((uint32_t)BNMAX * BM * 4 <= kStages * (kStageW + kStageX), "partial sums");
+  static_assert((4 * kStages + 2) * 8 + 8 <= kBarBytes, "barriers");
+};
+
 constexpr int kTmemCols = 512;
-constexpr int kScaleCol0 = kMaxBN;   // first scale column
-constexpr int kScaleCols = 48;       // per stage: 16 for W, 32 for X
 constexpr int kThreadsM = 512;
 constexpr int kEpiWarps = 8;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
@@ -237,8 +251,13 @@ __device__ __forceinline__ bool half_any(int half, bool v) {
   return r != 0;
 }
 
-template <bool MX>
+template <bool MX, int BNMAX>
 __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_constant__ Mx4mmParams p) {
+  using G = Geo<BNMAX>;
+  constexpr int kStages = G::kStages, kXCols = G::kXCols;
+  constexpr uint32_t kStageX = G::kStageX, kStageSX = G::kStageSX;
+  constexpr int kScaleCol0 = G::kScaleCol0, kScaleCols = G::kScaleCols;
+  constexpr int kHalfChunks = BNMAX / 32;  // chunks of 16 tokens of an epilogue half, at most
   constexpr int BLOCK = MX ? kMxBlock : kNvBlock;
   constexpr int kTilesKb = BK / (4 * BLOCK);          // scale tiles of a stage along d
   constexpr uint32_t kScaleKb = kTilesKb * kScaleTile;  // bytes, of 128 rows
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           if (c < p.col_tiles) {  // the last stage may end early
             async_copy16(dw + j * kScaleTile, gw + (size_t)c * kScaleTile);
             async_copy16(dx + j * kScaleTile, gx + (size_t)c * kScaleTile);
-            if (rows > 1)
+            if (G::kXTiles > 1 && rows > 1)
               async_copy16(dx + kScaleKb + j * kScaleTile,
                            gx + ((size_t)p.col_tiles + c) * kScaleTile);
           }
@@ -411,7 +430,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
 #define DP_STEP(k)                                                                          \
   mma_fp4<MX>(tmem_base, a + 2u * (k), b + 2u * (k),                                        \
             MX ? idesc | ((uint32_t)((k) & 1) << 5) | ((uint32_t)((k) & 1) << 30) : idesc, \
-            tw + 4u * (MX ? (k) / 2 : (k)), tx + 8u * (MX ? (k) / 2 : (k)),               \
+            tw + 4u * (MX ? (k) / 2 : (k)), tx + (uint32_t)kXCols * (MX ? (k) / 2 : (k)),               \
             (k) > 0 || kb > kb_lo ? 1u : 0u)
         if (steps >= 4) {
           DP_STEP(0);
@@ -462,25 +481,26 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         const uint8_t* gw = sSW + stage * kStageSW + lane * 16;
         const uint8_t* gx = sSX + stage * kStageSX + lane * 16;
         const uint32_t tw = tmem_base + lanes + (uint32_t)(kScaleCol0 + stage * kScaleCols);
-        uint32_t w[4 * kTilesKb], x[8 * kTilesKb];
+        uint32_t w[4 * kTilesKb], x[kXCols * kTilesKb];
 #pragma unroll
         for (int t = 0; t < kTilesKb; ++t) {
           const uint4 a = *reinterpret_cast<const uint4*>(gw + t * kScaleTile);
           w[4 * t] = a.x, w[4 * t + 1] = a.y, w[4 * t + 2] = a.z, w[4 * t + 3] = a.w;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+          for (int r = 0; r < G::kXTiles; ++r) {
             const uint4 b = *reinterpret_cast<const uint4*>(gx + r * kScaleKb + t * kScaleTile);
-            const int o = 8 * t + 4 * r;
+            const int o = kXCols * t + 4 * r;
             x[o] = b.x, x[o + 1] = b.y, x[o + 2] = b.z, x[o + 3] = b.w;
           }
         }
-        if (turn) {  // a word is a group of 32 tokens: the tile's first one goes first
+        if (G::kXTiles == 1 && turn) {  // a word is a group of 32 tokens: the tile's first one goes first
 #pragma unroll
           for (int t = 0; t < kTilesKb; ++t) {
-            uint4 b = make_uint4(x[8 * t], x[8 * t + 1], x[8 * t + 2], x[8 * t + 3]);
+            const int o = kXCols * t;
+            uint4 b = make_uint4(x[o], x[o + 1], x[o + 2], x[o + 3]);
             if (turn & 1) b = make_uint4(b.y, b.z, b.w, b.x);
             if (turn & 2) b = make_uint4(b.z, b.w, b.x, b.y);
-            x[8 * t] = b.x, x[8 * t + 1] = b.y, x[8 * t + 2] = b.z, x[8 * t + 3] = b.w;
+            x[o] = b.x, x[o + 1] = b.y, x[o + 2] = b.z, x[o + 3] = b.w;
           }
         }
         __syncwarp();
@@ -491,14 +511,18 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           break;
         }
         tc_fence_after();
-        if constexpr (MX) {
+        if constexpr (MX)
           DP_TMEM_ST_X8(tw, w);
-          DP_TMEM_ST_X16(tw + 16u, x);
-        } else {
+        else
           DP_TMEM_ST_X16(tw, w);
+        if constexpr (kXCols * kTilesKb == 8) {
+          DP_TMEM_ST_X8(tw + 16u, x);
+        } else {
           DP_TMEM_ST_X16(tw + 16u, x);
-          const uint32_t* hi = x + 16;
-          DP_TMEM_ST_X16(tw + 32u, hi);
+          if constexpr (kXCols * kTilesKb == 32) {
+            const uint32_t* hi = x + 16;
+            DP_TMEM_ST_X16(tw + 32u, hi);
+          }
         }
         tmem_st_wait();
         tc_fence_before();
@@ -565,7 +589,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       }
       // bf16: pairs of tokens are packed into a register as they are read, so
       // the accumulator is free again before the first store
-      uint32_t h[8][8];
+      constexpr int kH = kHalfChunks > 1 ? kHalfChunks : 2;  // read two at a time
+      uint32_t h[kH][8];
       const auto pack32 = [&](const uint32_t(&r)[32], int c) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
@@ -578,7 +603,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           }
       };
 #pragma unroll
-      for (int c = 0; c < 8; c += 2) {
+      for (int c = 0; c < kH; c += 2) {
         uint32_t r[32];
         if (c < cn) {  // an odd last chunk reads 16 columns too many, which stay unused
           DP_TMEM_LD_X32(tbase + (uint32_t)(c * 16), r);
@@ -598,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         break;
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+      for (int c = 0; c < kHalfChunks; ++c)
         if (c < cn) {
           if (leader) bulk_wait_read0();  // the previous box has been read
           half_barrier(half);
@@ -667,9 +692,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   }
 }
 
-template <bool MX>
-cudaError_t launch_mx4mm(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, cudaStream_t s) {
-  auto kernel = mx4mm_kernel<MX>;
+template <bool MX, int BNMAX>
+cudaError_t launch_for(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, cudaStream_t s) {
+  constexpr size_t kSmemBytes = Geo<BNMAX>::kSmem;
+  auto kernel = mx4mm_kernel<MX, BNMAX>;
   if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kThreadsM, kSmemBytes,
                           dev.device) < 1)
     return cudaErrorInvalidConfiguration;
@@ -704,6 +730,14 @@ cudaError_t launch_mx4mm(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, c
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+template <bool MX>
+cudaError_t launch_mx4mm(const Mx4mmParams& p, int tiles, const dph::DeviceInfo& dev,
+                         cudaStream_t s) {
+  if (p.BN <= 32) return launch_for<MX, 32>(p, tiles, dev, s);
+  if (p.BN <= 128) return launch_for<MX, 128>(p, tiles, dev, s);
+  return launch_for<MX, 256>(p, tiles, dev, s);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -763,7 +797,6 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
                     Mx4mmParams* pp, int* tilesp, size_t* zero_bytes) {
   *tilesp = 0;
   *zero_bytes = 0;
-  const bool mx = format == DP_MXFP4;
   const int F = K * F_shard, block = mx4_block(format);
   const size_t ysz = (size_t)M * F * (y_dtype == DP_FP32 ? 4 : 2);
   if (M == 0 || F == 0) return DP_OK;
@@ -773,7 +806,7 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
     *zero_bytes = ysz;
     return DP_OK;
   }
-  if (dev.cc_major != 10 || dev.cc_minor != 3 || dev.smem_optin < kSmemBytes)
+  if (dev.cc_major != 10 || dev.cc_minor != 3 || dev.smem_optin < Geo<256>::kSmem)
     return DP_ERR_UNSUPPORTED;
 
   Mx4mmParams& p = *pp;
