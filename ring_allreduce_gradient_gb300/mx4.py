@@ -192,6 +192,8 @@ def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
 
 def _shards(w_shards, cols, format, device):
     """The shards' structures, after checking that they make one matrix for this operand."""
+    if not w_shards:
+        raise ValueError("need at least one shard")
     w0 = w_shards[0]
     kind = (w0._kind[0], cols, format, device)
     if w0._kind != kind:
@@ -233,6 +235,8 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
         raise ValueError("x: need a matrix with unit stride along its rows")
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
+    if not w_shards:
+        raise ValueError("need at least one shard")
     dev, K = x.device, len(w_shards)
     F, _, format, _ = w_shards[0]._kind
     arr = _shards(w_shards, D, format, dev)

@@ -186,3 +186,8 @@ def test_the_tensor_helpers_check():
         mx4.linear(x, [q])
     with pytest.raises(ValueError, match="contiguous tensors"):
         mx4.tensor_scale([])
+
+
+def test_a_product_needs_a_shard():
+    with pytest.raises(ValueError, match="at least one shard"):
+        mx4.linear(torch.zeros(4, 64), [])
