@@ -22,7 +22,7 @@ SOURCES = ["dp_api.cu", "dp_stream.cu", "dp_odc.cu", "dp_agmm.cu", "dp_bucket.cu
            "dp_mx4.cu", "dp_mx4mm.cu"]
 HEADERS = [os.path.join(CSRC, "dp_common.cuh"), os.path.join(CSRC, "dp_launch.h"),
            os.path.join(CSRC, "dp_stream_common.cuh"), os.path.join(CSRC, "dp_tc.cuh"),
-           os.path.join(CSRC, "dp_mx4.cuh"),
+           os.path.join(CSRC, "dp_early.cuh"), os.path.join(CSRC, "dp_mx4.cuh"),
            os.path.join(ROOT, "include", "dp.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -5,6 +5,40 @@
 
 #include "dp_common.cuh"
 
+#include <algorithm>
+#include <vector>
+
+namespace dph {
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// A range of addresses, and whether the call writes there.
+struct Span {
+  uintptr_t lo, hi;
+  bool written;
+};
+inline Span span_of(const void* p, size_t n, bool written = false) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Span{a, a + n, written};
+}
+inline bool clash(const Span& a, const Span& b) {
+  return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
+}
+// True if a written range overlaps any other range of the list.
+inline bool spans_clash(std::vector<Span>& s) {
+  std::sort(s.begin(), s.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t end_any = 0, end_written = 0;
+  for (const Span& x : s) {
+    if (x.lo >= x.hi) continue;
+    if (x.lo < end_written || (x.written && x.lo < end_any)) return true;
+    end_any = std::max(end_any, x.hi);
+    if (x.written) end_written = std::max(end_written, x.hi);
+  }
+  return false;
+}
+
+}  // namespace dph
+
 // Launchers (host functions defined in the kernel translation units).  They
 // assume validated arguments and return the launch status.
 namespace dpl {

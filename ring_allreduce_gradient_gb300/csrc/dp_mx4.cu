@@ -23,9 +23,10 @@
 // rows, and the four warps of a CTA, one below the other, with a 128-byte
 // line.  Neither goes through shared memory.  Measured on 8192 x 4096 bf16
 // (GB300, launches in a CUDA graph): rows 14.1 us to nvfp4 and 11.2 to mxfp4
-// (6.1 and 7.7 TB/s, part of it from L2), transposed 17.9 and 12.7, decoding
-// 12.6; the nvfp4 forms are held by their arithmetic, two divisors a block.
+// (6.1 and 7.7 TB/s, part of it from L2), transposed 16.5 and 12.4, decoding
+// 12.0; the nvfp4 forms are held by their arithmetic, two divisors a block.
 
+#include "dp_early.cuh"
 #include "dp_launch.h"
 #include "dp_mx4.cuh"
 
@@ -209,14 +210,14 @@ struct Sixteen<float> {
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
     for (int h = 0; h < 16; h += 8)
-      asm volatile("ld.global.nc.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                    : "=f"(v[h]), "=f"(v[h + 1]), "=f"(v[h + 2]), "=f"(v[h + 3]), "=f"(v[h + 4]),
                      "=f"(v[h + 5]), "=f"(v[h + 6]), "=f"(v[h + 7])
                    : "l"(p + h));
   }
   __device__ __forceinline__ void each(const float* p, bool in) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = in ? __ldg(p + i) : 0.0f;
+    for (int i = 0; i < 16; ++i) v[i] = in ? p[i] : 0.0f;
   }
   __device__ __forceinline__ uint32_t top() const {
     uint32_t t = 0;
@@ -239,7 +240,7 @@ template <>
 struct Sixteen<uint16_t> {
   uint32_t r[8];
   __device__ __forceinline__ void load(const uint16_t* p) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                    "=r"(r[6]), "=r"(r[7])
                  : "l"(p));
@@ -247,7 +248,7 @@ struct Sixteen<uint16_t> {
   __device__ __forceinline__ void each(const uint16_t* p, bool in) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      r[i] = in ? (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16 : 0u;
+      r[i] = in ? (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16 : 0u;
   }
   __device__ __forceinline__ uint32_t top() const {
     uint32_t t = 0;
@@ -314,11 +315,10 @@ __device__ __forceinline__ void quant_row(const QuantParams& p, int r, int e0, b
 
 template <typename T, int BLOCK, int G>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_constant__ QuantParams p) {
-  // a product that follows may set itself up meanwhile (it waits for this grid's end)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  stream_order();
   const unsigned groups = ((unsigned)p.col_tiles * 4 * BLOCK + G * 512 - 1) / (G * 512);
   const unsigned blocks = ((unsigned)p.R + kScaleRows - 1) / kScaleRows * (kScaleRows / kWarps) * groups;
-  const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
+  const float t = BLOCK == kNvBlock && p.tscale ? *p.tscale : 1.0f;
   const Divisor by_t(t);
   for (unsigned b = blockIdx.x; b < blocks; b += gridDim.x) {
     const unsigned q = b / groups;
@@ -332,13 +332,13 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const __grid_const
 // Two neighbouring columns of a row.
 template <bool FAST>
 __device__ __forceinline__ float2 load2(const float* x, int c, int last) {
-  if constexpr (FAST) return __ldg(reinterpret_cast<const float2*>(x + c));
-  return make_float2(__ldg(x + c), __ldg(x + min(c + 1, last)));
+  if constexpr (FAST) return *reinterpret_cast<const float2*>(x + c);
+  return make_float2(x[c], x[min(c + 1, last)]);
 }
 template <bool FAST>
 __device__ __forceinline__ uint32_t load2(const uint16_t* x, int c, int last) {
-  if constexpr (FAST) return __ldg(reinterpret_cast<const uint32_t*>(x + c));
-  return (uint32_t)__ldg(x + c) | (uint32_t)__ldg(x + min(c + 1, last)) << 16;
+  if constexpr (FAST) return *reinterpret_cast<const uint32_t*>(x + c);
+  return (uint32_t)x[c] | (uint32_t)x[min(c + 1, last)] << 16;
 }
 __device__ __forceinline__ float part(float2 v, int j) { return j ? v.y : v.x; }
 __device__ __forceinline__ float part(uint32_t v, int j) { return j ? bf16hi(v) : bf16lo(v); }
@@ -381,10 +381,11 @@ constexpr int kTRows = 64;  // input rows a warp takes at once: 32 bytes of each
 template <typename T, int BLOCK, bool FAST>
 __global__ void __launch_bounds__(kThreads) quant_cols_kernel(const __grid_constant__ QuantParams p) {
   constexpr int kBlocks = kTRows / BLOCK;
+  stream_order();
   const int lane = threadIdx.x & 31;
   const unsigned cgroups = ((unsigned)p.R + kScaleRows - 1) / kScaleRows * 2;  // 64 columns each
   const unsigned rgroups = ((unsigned)p.col_tiles * 4 * BLOCK + kTRows * kWarps - 1) / (kTRows * kWarps);
-  const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
+  const float t = BLOCK == kNvBlock && p.tscale ? *p.tscale : 1.0f;
   const Divisor by_t(t);
   for (unsigned u = blockIdx.x; u < cgroups * rgroups; u += gridDim.x) {
     const unsigned q = u / cgroups;
@@ -467,7 +468,8 @@ __device__ __forceinline__ float step_of(uint32_t byte, float t) {
 // A warp takes G x 256 columns of a row, a lane eight of each 256.
 template <typename T, int BLOCK, int G>
 __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant__ DecodeParams p) {
-  const float t = BLOCK == kNvBlock && p.tscale ? __ldg(p.tscale) : 1.0f;
+  stream_order();
+  const float t = BLOCK == kNvBlock && p.tscale ? *p.tscale : 1.0f;
   const int lane = threadIdx.x & 31;
   const unsigned groups = ((unsigned)p.L + G * 256 - 1) / (G * 256);
   const unsigned blocks = ((unsigned)p.R + kWarps - 1) / kWarps * groups;
@@ -482,8 +484,8 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
     for (int g = 0; g < G; ++g) {
       const int e = min(e0 + g * 256, p.L - 8);  // past the end: the last, and dropped
       const int b = e / BLOCK;
-      c[g] = __ldg(reinterpret_cast<const uint32_t*>(codes + e / 2));
-      byte[g] = __ldg(p.scales + scale_at(r, b / 4, p.col_tiles) + b % 4);
+      c[g] = *reinterpret_cast<const uint32_t*>(codes + e / 2);
+      byte[g] = p.scales[scale_at(r, b / 4, p.col_tiles) + b % 4];
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -500,12 +502,12 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(const __grid_constant_
 
 // One CTA for each share of the work, which the hardware hands out as SMs
 // become free; under a CTA limit the CTAs go over the shares.
-template <typename KernelT, typename P>
-cudaError_t launch(KernelT kernel, const P& p, long long blocks, cudaStream_t s) {
+template <typename P>
+cudaError_t launch(void (*kernel)(P), const P& p, long long blocks, cudaStream_t s) {
   const int limit = dph::stream_cta_limit();
   if (limit > 0) blocks = std::min<long long>(blocks, limit);
-  kernel<<<(unsigned)std::min<long long>(blocks, 0x7fffffffll), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return dph::launch_early(kernel, p, (unsigned)std::min<long long>(blocks, 0x7fffffffll), kThreads,
+                           s);
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -542,18 +544,10 @@ cudaError_t decode(const DecodeParams& p, cudaStream_t s) {
   return launch(decode_kernel<T, BLOCK, 1>, p, ceil_div(p.R, kWarps) * ceil_div(p.L, 256), s);
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Span {
-  uintptr_t lo, hi;
-};
-Span span_of(const void* p, size_t n) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{a, a + n};
-}
-bool clash(const Span& a, const Span& b) {
-  return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
-}
+using dph::aligned;
+using dph::clash;
+using dph::Span;
+using dph::span_of;
 
 }  // namespace
 

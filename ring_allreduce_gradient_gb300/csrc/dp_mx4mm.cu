@@ -29,13 +29,13 @@
 // stage is.  With the scales two accumulators of 256 columns do not fit.
 //
 // Measured (GB300, launches in a CUDA graph): x[8192,4096] . w[4096,4096]^T
-// 49 us in mxfp4 (5.6 PFLOP/s) and 60 us in nvfp4 (4.6); x[8192,8192] .
-// w[8192,8192]^T 162 and 191 us.  What bounds it: the MMAs alone (loads of all
-// stages but the first four left out) take 139 us of the 162; the rest is
+// 50 us in mxfp4 (5.5 PFLOP/s) and 58 us in nvfp4 (4.8); x[8192,8192] .
+// w[8192,8192]^T 160 and 187 us.  What bounds it: the MMAs alone (loads of all
+// stages but the first four left out) take 139 us of the 160; the rest is
 // operand intake, 48 KiB of values a stage, and between tiles the 1300 clocks
 // in which the accumulator is drained.  nvfp4 has twice the scales: reading
 // them four times from shared memory, once for each quarter of TMEM, costs 20
-// us of its 191.  The steps that led here, on that product:
+// us of its 187.  The steps that led here, on that product:
 //   * scales through registers (195 / 167 us, nvfp4 / mxfp4) instead of
 //     tcgen05.cp straight from shared memory (269 / 204 us): the copies take
 //     their turn with the MMAs, about 100 clocks each;
@@ -51,6 +51,7 @@
 // Every mbarrier wait is bounded; on expiry a role flags the error word and
 // unwinds, and the cluster's barriers are still reached by every thread.
 
+#include "dp_early.cuh"
 #include "dp_launch.h"
 #include "dp_mx4.cuh"
 #include "dp_tc.cuh"
@@ -118,6 +119,7 @@ struct Mx4mmParams {
   int x_row_tiles;
   int split;              // CTAs of a cluster that share a tile
   int y_f32;
+  int next_early;         // let the next kernel move in before this one's end
 };
 
 // Tile i of this launch.
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   // the launch may begin while the kernel before it in the stream (the
   // quantisation of x) still runs: nothing of global memory is touched before
   // that one has ended
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_stream();
 
   if (warp == 0 || warp == 2) {
     // ------------------------------ producers ---------------------------------
@@ -350,6 +352,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           }
         }
       }
+      // the next kernel's CTAs may move in beside the last tile's end
+      if (warp == 0 && p.next_early) let_next_start();
       // Drain: every load this thread issued has landed before the CTA exits.
       for (int s = 0; s < kStages; ++s)
         if (armed[s]) (void)mbar_wait_bounded(&full[s], armed_phase[s], p.err, kTimeoutNs);
@@ -548,8 +552,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       const int shard = t.shard, m0 = t.m0 + c0 * 16;
       float alpha = 1.0f;
       if constexpr (!MX) {
-        if (p.tx) alpha = __ldg(p.tx);
-        if (p.tw[shard]) alpha = __fmul_rn(alpha, __ldg(p.tw[shard]));
+        if (p.tx) alpha = *p.tx;
+        if (p.tw[shard]) alpha = __fmul_rn(alpha, *p.tw[shard]);
       }
       // A wait that ran out is acted on where the half's threads next meet, so
       // that they leave together; until then nothing depends on what was read.
@@ -652,8 +656,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     const int shard = t.shard, f0 = t.f0, m0 = t.m0;
     float alpha = 1.0f;
     if constexpr (!MX) {
-      if (p.tx) alpha = __ldg(p.tx);
-      if (p.tw[shard]) alpha = __fmul_rn(alpha, __ldg(p.tw[shard]));
+      if (p.tx) alpha = *p.tx;
+      if (p.tw[shard]) alpha = __fmul_rn(alpha, *p.tw[shard]);
     }
     const int tokens = min(p.BN, p.M - m0);
     const int share = (tokens + p.split - 1) / p.split;
@@ -740,18 +744,10 @@ cudaError_t launch_mx4mm(const Mx4mmParams& p, int tiles, const dph::DeviceInfo&
   return launch_for<MX, 256>(p, tiles, dev, s);
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Span {
-  uintptr_t lo, hi;
-};
-Span span_of(const void* p, size_t n) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{a, a + n};
-}
-bool clash(const Span& a, const Span& b) {
-  return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
-}
+using dph::aligned;
+using dph::clash;
+using dph::Span;
+using dph::span_of;
 
 }  // namespace
 
@@ -841,6 +837,12 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   while (p.split < kMaxSplit && p.num_kb >= p.split * 2 &&
          tiles * p.split * 2 <= (p.split == 4 ? dev.sm_count / 2 : dev.sm_count))
     p.split *= 2;
+  // A kernel that moves in beside this one's shared memory keeps the little L1
+  // that is left: the next product starts about 1 us earlier (128x512x512: 6.3
+  // -> 5.0 us each; x[16,4096] 7.3 -> 6.6), but a next quantisation of a large x
+  // runs slower by more (linear of x[512,4096]: 10.9 -> 12.0 us, x[8192,4096]:
+  // 63 -> 70, x[128,4096]: 8.9 -> 9.3; x[128,512] and x[16,4096] gain as well).
+  p.next_early = (size_t)M * (size_t)D <= (128u << 10);
   p.sx = static_cast<const uint8_t*>(x->scales);
   p.tx = x->tensor_scale;
   p.y = y;

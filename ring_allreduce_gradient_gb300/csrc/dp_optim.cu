@@ -27,6 +27,7 @@
 // Tensors whose pointers are not aligned for that, and the last elements of a
 // tensor, go lane by lane over consecutive elements with the same arithmetic.
 
+#include "dp_early.cuh"
 #include "dp_launch.h"
 
 #include <algorithm>
@@ -193,13 +194,14 @@ template <typename PT, typename GT, bool S8, int CAP>
 __global__ void __launch_bounds__(kThreads, kAdamwCtas) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
   const int lane = threadIdx.x & 31;
   const unsigned units = a.ustart[a.n];
+  stream_order();
   Hyper h{1.0f, a.beta1, a.omb1, a.beta2, a.omb2, a.eps, a.step_size, a.inv_root};
   double lr = a.lr;
-  if (a.grad_scale) h.coef = __ldg(a.grad_scale);
+  if (a.grad_scale) h.coef = *a.grad_scale;
   if (a.schedule) {
-    lr = (double)__ldg(a.schedule);
-    h.step_size = (float)(lr / (double)__ldg(a.schedule + 1));
-    h.inv_root = (float)(1.0 / sqrt((double)__ldg(a.schedule + 2)));
+    lr = (double)a.schedule[0];
+    h.step_size = (float)(lr / (double)a.schedule[1]);
+    h.inv_root = (float)(1.0 / sqrt((double)a.schedule[2]));
   }
   for (unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
     // the unit's tensor: the last t with ustart[t] <= u
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_kernel(const __grid_cons
   __shared__ bool is_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned units = a.ustart[a.n];
+  stream_order();
   for (int s = blockIdx.x; s < a.slots; s += gridDim.x) {
     unsigned u = (unsigned)s * kNormWarps + warp;
     double sum = 0.0;
@@ -489,25 +492,10 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_kernel(const __grid_cons
 
 size_t esize(dp_dtype_t t) { return t == DP_FP32 ? 4u : 2u; }
 bool dtype_ok(dp_dtype_t t) { return t == DP_FP32 || t == DP_BF16; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Span {
-  uintptr_t lo, hi;
-  bool written;
-};
-
-// True if a written range overlaps any other range.
-bool spans_clash(std::vector<Span>& s) {
-  std::sort(s.begin(), s.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  uintptr_t end_any = 0, end_written = 0;
-  for (const Span& x : s) {
-    if (x.lo >= x.hi) continue;
-    if (x.lo < end_written || (x.written && x.lo < end_any)) return true;
-    end_any = std::max(end_any, x.hi);
-    if (x.written) end_written = std::max(end_written, x.hi);
-  }
-  return false;
-}
+using dph::aligned;
+using dph::Span;
+using dph::span_of;
+using dph::spans_clash;
 
 constexpr int kNormCap = 768;      // tensors per norm launch: 19 KB of kernel parameters
 constexpr int kNormCapSmall = 32;
@@ -539,8 +527,7 @@ cudaError_t norm_launch(const void* const* grads, const size_t* numels, const st
   p.norm = norm;
   p.coef = coef;
   const int grid = std::min(*slots, resident_blocks(norm_kernel<GT, OP, CAP>, dev));
-  norm_kernel<GT, OP, CAP><<<grid, kNormThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return dph::launch_early(norm_kernel<GT, OP, CAP>, p, (unsigned)grid, kNormThreads, s);
 }
 
 constexpr size_t kNormHead = 256;  // the ticket, ahead of the partial sums
@@ -564,8 +551,8 @@ template <typename PT, typename GT, bool S8>
 cudaError_t adamw_launch(const AdamwParams<dp_adamw::kCap>& table, cudaStream_t s) {
   const unsigned units = table.ustart[table.n];
   if (table.n > dp_adamw::kCapSmall) {
-    adamw_kernel<PT, GT, S8, dp_adamw::kCap><<<blocks_for(units), kThreads, 0, s>>>(table);
-    return cudaGetLastError();
+    return dph::launch_early(adamw_kernel<PT, GT, S8, dp_adamw::kCap>, table, blocks_for(units),
+                             kThreads, s);
   }
   AdamwParams<dp_adamw::kCapSmall> p;
   const size_t n = (size_t)table.n;
@@ -582,8 +569,8 @@ cudaError_t adamw_launch(const AdamwParams<dp_adamw::kCap>& table, cudaStream_t 
   p.inv_root = table.inv_root;
   p.grad_scale = table.grad_scale;
   p.schedule = table.schedule;
-  adamw_kernel<PT, GT, S8, dp_adamw::kCapSmall><<<blocks_for(units), kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return dph::launch_early(adamw_kernel<PT, GT, S8, dp_adamw::kCapSmall>, p, blocks_for(units),
+                           kThreads, s);
 }
 
 template <typename PT, typename GT>
@@ -626,13 +613,11 @@ dp_status_t gather_list(const void* const* grads, const size_t* numels, int n,
       if (!grads[t]) return DP_ERR_INVALID_ARG;
       units += (numels[t] - 1) / kNormUnit + 1;
       if (!aligned(grads[t], es) || units > 0x7fffffffull) return DP_ERR_UNSUPPORTED;
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[t]);
-      spans.push_back({lo, lo + numels[t] * es, false});
+      spans.push_back(span_of(grads[t], numels[t] * es));
       at.push_back(t);
     }
     const auto out = [&](const void* p, size_t b) {
-      const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-      if (p) spans.push_back({lo, lo + b, true});
+      if (p) spans.push_back(span_of(p, b, true));
     };
     out(norm, 4);
     out(coef, 4);
@@ -736,8 +721,7 @@ dp_status_t dp_adamw_create(const dp_adamw_tensor_t* tensors, int n, dp_dtype_t 
         break;
       }
       const auto span = [&](const void* p, size_t bytes, bool written) {
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        if (p) spans.push_back({lo, lo + bytes, written});
+        if (p) spans.push_back(span_of(p, bytes, written));
       };
       span(x.param, x.numel * ps, true);
       span(x.grad, x.numel * gs, false);

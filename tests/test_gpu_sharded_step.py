@@ -51,3 +51,42 @@ def test_gradients_of_the_sharded_layer_match_the_decoded_weights():
     want = sum(dy.double().t() @ x.double() for dy, x in zip(dys, xs)) / K
     size = sum(dy.double().abs().t() @ x.double().abs() for dy, x in zip(dys, xs)) / K
     assert bool(((dw - want).abs() <= (K * T + 8) * 2.0 ** -24 * size).all())
+
+
+@pytest.mark.parametrize("format,T,F,D", [("mxfp4", 16, 256, 128), ("nvfp4", 130, 256, 192),
+                                          ("nvfp4", 1, 1024, 2048)])
+def test_calls_in_a_row_see_each_other(format, T, F, D):
+    """Each call reads what the one before wrote, in place, with and without waits between them."""
+    from ring_allreduce_gradient_gb300 import mx4, optim
+    dev = torch.device("cuda", 0)
+
+    def run(wait):
+        gen = torch.Generator(device=dev).manual_seed(17)
+        w = torch.randn(F, D, device=dev, generator=gen)
+        g = torch.randn(F, D, device=dev, generator=gen)
+        copy = torch.zeros(F, D, device=dev, dtype=torch.bfloat16)
+        x = torch.randn(T, D, device=dev, generator=gen).bfloat16()
+        step = optim.AdamW([w], [g], states="8bit", copies=[copy])
+        norm = optim.GradNorm([g], max_norm=1.0)
+        ys = []
+        for _ in range(25):
+            norm()
+            wait()
+            step.step(lr=1e-2, grad_scale=norm.coef)
+            wait()
+            q = mx4.quantize(copy, format, mx4.tensor_scale(copy) if format == "nvfp4" else None)
+            wait()
+            y = mx4.linear(x, [q], mx4.tensor_scale(x) if format == "nvfp4" else None)
+            wait()
+            ys.append(y)
+            qt = mx4.quantize(copy, "mxfp4", transpose=True)
+            wait()
+            ys.append(mx4.dequantize(qt))
+            wait()
+            x = ys[-1].t()[:T].contiguous()
+        torch.cuda.synchronize()
+        return ys + [w]
+
+    a, b = run(torch.cuda.synchronize), run(lambda: None)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert not torch.equal(a[0], a[2])      # the weights moved
