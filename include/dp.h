@@ -577,8 +577,8 @@ DP_API dp_status_t dp_reducer_wait(dp_reducer_t* r, dp_stream_t stream);
  * max_norm > 0 (infinity: coef is 1).  An empty list has norm 0.
  * Squares are summed in fp32 over 32 elements, pairs of such sums are added
  * in fp32, and the rest is in double; the order is fixed by the sizes and
- * alignments, so a list gives the same bits under any CTA limit.  A gradient above 1.8e19 in magnitude overflows its square and
- * makes the norm infinite.
+ * alignments, so a list gives the same bits under any CTA limit.  A gradient
+ * above 1.8e19 in magnitude overflows its square and makes the norm infinite.
  *
  * workspace: device memory of at least dp_grad_norm_workspace_size(n) bytes,
  * 16-byte aligned, overlapping nothing; its first 4 bytes are zero before
@@ -663,7 +663,7 @@ DP_API void dp_adamw_destroy(dp_adamw_t* o);
  * into the GEMM that uses it ("Sharding and Parallelism", section
  * "Communication predictions": a collective's bytes follow the element type).
  *
- * A matrix [rows, cols], cols a multiple of 32, has
+ * A matrix [rows, cols], cols a multiple of 32, both at most 2^31 - 2^16, has
  *   codes    rows x cols/2 bytes: e2m1 values (0 0.5 1 1.5 2 3 4 6, bit 3 the
  *            sign), two to a byte, the earlier column in the low half
  *   scales   one byte for each block of consecutive columns:

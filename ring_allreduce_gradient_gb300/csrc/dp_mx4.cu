@@ -39,6 +39,9 @@ using namespace dpk;
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+// Rows or columns of a matrix: the end of the widest share (2048 columns) that
+// starts inside one has to be an int.
+constexpr int kMaxSize = 0x7fff0000;
 
 struct QuantParams {
   const void* x[kMaxK];
@@ -575,7 +578,7 @@ dp_status_t dp_mx4_quantize(const void* const* x, int K, int rows, int cols, lon
   if (tensor_scale && format != DP_NVFP4) return DP_ERR_INVALID_ARG;
   const size_t esz = x_dtype == DP_FP32 ? 4 : 2;
   const long long all = (long long)K * rows;
-  if (all > 0x7fffff00ll || cols > 0x7fffff00) return DP_ERR_UNSUPPORTED;
+  if (all > kMaxSize || cols > kMaxSize) return DP_ERR_UNSUPPORTED;
   const int R = transpose ? cols : (int)all, L = transpose ? (int)all : cols;
   if (L % 32) return DP_ERR_UNSUPPORTED;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(tensor_scale, 4))
@@ -631,7 +634,7 @@ dp_status_t dp_mx4_dequantize(const void* codes, const void* scales, int rows, i
   if (out_dtype != DP_FP32 && out_dtype != DP_BF16) return DP_ERR_UNSUPPORTED;
   if (format != DP_MXFP4 && format != DP_NVFP4) return DP_ERR_UNSUPPORTED;
   if (tensor_scale && format != DP_NVFP4) return DP_ERR_INVALID_ARG;
-  if (cols % 32 || cols > 0x7fffff00 || rows > 0x7fffff00) return DP_ERR_UNSUPPORTED;
+  if (cols % 32 || cols > kMaxSize || rows > kMaxSize) return DP_ERR_UNSUPPORTED;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 16) || !aligned(tensor_scale, 4))
     return DP_ERR_UNSUPPORTED;
   if (rows == 0 || cols == 0) return DP_OK;

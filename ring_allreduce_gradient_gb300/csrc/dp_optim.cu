@@ -410,10 +410,10 @@ __device__ __forceinline__ double block_joined(double v, double* sums) {
 }
 
 // Squares are summed in fp32 over 32 elements of a lane, two such sums are
-// added in fp32, and the rest is in double.  Partial sum s covers the units of virtual CTA s (s, s + slots, ...
-// by warps), whatever CTA computes it, and the last CTA to finish adds the
-// partial sums in order: the result depends neither on the grid nor on the
-// order in which CTAs finish.
+// added in fp32, and the rest is in double.  Partial sum s covers the units of
+// virtual CTA s (s, s + slots, ... by warps), whatever CTA computes it, and the
+// last CTA to finish adds the partial sums in order: the result depends neither
+// on the grid nor on the order in which CTAs finish.
 template <typename GT, int OP, int CAP>
 __global__ void __launch_bounds__(kNormThreads, 3) norm_kernel(const __grid_constant__ NormParams<CAP> a) {
   __shared__ double sums[kNormWarps];

@@ -191,3 +191,15 @@ def test_the_tensor_helpers_check():
 def test_a_product_needs_a_shard():
     with pytest.raises(ValueError, match="at least one shard"):
         mx4.linear(torch.zeros(4, 64), [])
+
+
+@pytest.mark.parametrize("cols", [0x7fff0020, 0x7fffff00])
+def test_rows_too_long_to_index(cols):
+    def q(tr, rows, n):
+        return B.dp_mx4_quantize([fake(0)], 1, rows, n, n, B.DP_BF16, MX, tr, None, fake(4),
+                                 fake(5), stream=0, check=False)
+
+    assert q(0, 1, cols) == UNSUPPORTED and q(1, 32, cols) == UNSUPPORTED
+    assert q(0, cols, 32) == UNSUPPORTED
+    assert B.dp_mx4_dequantize(fake(0), fake(1), 1, cols, MX, None, fake(2), B.DP_BF16, stream=0,
+                               check=False) == UNSUPPORTED
