@@ -141,11 +141,14 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
         with _on(stream, xs[0].device):
             return quantize(xs, format, tensor_scale, transpose)
     x0 = xs[0]
-    rows, cols = _matrix(x0)
+    first, ld = _rows(x0)
+    rows, cols = x0.shape
     for t in xs[1:]:
         if t.shape != x0.shape or t.dtype != x0.dtype or t.device != x0.device or \
                 t.stride() != x0.stride():
             raise ValueError("need shards of one shape, dtype, device and row stride")
+    if first is not x0:
+        xs = [first] + [_rows(t)[0] for t in xs[1:]]
     dev = x0.device
     if tensor_scale is not None:
         _check_scale(tensor_scale, dev)
@@ -154,22 +157,26 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
     q = Mx4Tensor._empty(R, L, format, tensor_scale, dev)
     c = q._c
     st = (B._lib or B.load()).dp_mx4_quantize(
-        B._parray(xs), K, rows, cols, _row_stride(x0), _code(x0), fmt, 1 if transpose else 0,
+        B._parray(xs), K, rows, cols, ld, _code(x0), fmt, 1 if transpose else 0,
         c.tensor_scale, c.codes, c.scales, B._stream(None))
     if st:
         raise B.DpError(st, "dp_mx4_quantize")
     return q
 
 
-def _matrix(x):
-    """The shape of a matrix with unit stride along its rows."""
+def _rows(x):
+    """A matrix as the library takes it, and the elements between its rows, which
+    are at least a row's length.  Rows that overlap (one row expanded to many, a
+    window moved over a vector) are copied out."""
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("need a matrix with unit stride along its rows")
-    return x.shape
-
-
-def _row_stride(x) -> int:
-    return max(x.stride(0), x.shape[1]) if x.shape[0] > 1 else x.shape[1]
+    rows, cols = x.shape
+    ld = x.stride(0)
+    if rows <= 1:
+        return x, cols
+    if ld < cols:
+        return x.contiguous(), cols
+    return x, ld
 
 
 def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
@@ -229,10 +236,8 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
             return linear(x, w_shards, x_scale, y_dtype)
     # One token's product takes the GPU less time than this function: it makes
     # the call itself, without the binding's marshalling.
+    x, ld = _rows(x)
     M, D = x.shape
-    ld, unit = x.stride()
-    if unit != 1 and D > 1:
-        raise ValueError("x: need a matrix with unit stride along its rows")
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
     if not w_shards:
@@ -247,7 +252,7 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
     st = (B._lib or B.load()).dp_allgather_linear_mx4(
-        x.data_ptr(), M, D, ld if M > 1 and ld > D else D, _code(x),
+        x.data_ptr(), M, D, ld, _code(x),
         None if x_scale is None else x_scale.data_ptr(), arr, K, F, FORMATS[format],
         y.data_ptr(), _DT[y_dtype], ws.data_ptr(), nbytes, B._stream(None))
     if st:

@@ -383,3 +383,19 @@ def test_a_stream_given_by_hand(as_handle):
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(s, s2) and torch.equal(y, want) and torch.equal(y2, want)
     assert torch.equal(d, mx4.dequantize(mx4.quantize(x, "nvfp4", s)))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_that_overlap(fmt, dtype):
+    """One row expanded to many and a window moved over a vector: the bits of their copies."""
+    rng = np.random.default_rng(12)
+    row, line = dev(rng.standard_normal((1, 256)), dtype), dev(rng.standard_normal(4096), dtype)
+    w = [mx4.quantize(dev(rng.standard_normal((64, 256))), fmt) for _ in range(2)]
+    for x in (row.expand(96, 256), line.as_strided((160, 256), (16, 1)), line.unfold(0, 256, 64)[:32]):
+        c = x.contiguous()
+        for tr in (False, True):
+            for a, b in ((x, c), ([x, x], [c, c])):
+                q, ref = mx4.quantize(a, fmt, transpose=tr), mx4.quantize(b, fmt, transpose=tr)
+                assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)
+        assert torch.equal(mx4.linear(x, w), mx4.linear(c, w))

@@ -203,3 +203,25 @@ def test_rows_too_long_to_index(cols):
     assert q(0, cols, 32) == UNSUPPORTED
     assert B.dp_mx4_dequantize(fake(0), fake(1), 1, cols, MX, None, fake(2), B.DP_BF16, stream=0,
                                check=False) == UNSUPPORTED
+
+
+def views():
+    """Matrices whose rows overlap, are expanded from one, or lie apart, and single rows."""
+    base = torch.arange(4096, dtype=torch.float32)
+    return [base[:64].expand(128, 64), base[64:128].view(1, 64).expand(3, 64),
+            base[100:].as_strided((4, 64), (16, 1), 100), base.unfold(0, 96, 32),
+            base[:1].expand(32, 1), base.view(64, 64)[:, :32], base.view(32, 128)[3:9, 5:37],
+            base[:64].view(1, 64), base.view(64, 64)[:1, :32], base.view(128, 32)[:, :1],
+            base.view(64, 64)[:0]]
+
+
+@pytest.mark.parametrize("i", range(len(views())))
+def test_rows_that_the_library_gets_are_the_views(i):
+    """Row r at r * ld of the buffer that is handed on, inside its storage, ld a row or more."""
+    x = views()[i]
+    t, ld = mx4._rows(x)
+    rows, cols = x.shape
+    assert ld >= cols
+    if rows:
+        assert (rows - 1) * ld + cols <= t.untyped_storage().nbytes() // 4 - t.storage_offset()
+        assert torch.equal(t.as_strided((rows, cols), (ld, 1)), x)
