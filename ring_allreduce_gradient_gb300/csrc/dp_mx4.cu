@@ -6,10 +6,10 @@
 // of two is exact, so each value is rounded once.
 // nvfp4: with t the tensor's scale, a block's scale is s = e4m3(amax / 6 / t)
 // and its values are e2m1(x / (s t)): the tensor's scale takes the largest
-// block's s to the top of e4m3, s takes the block's largest value to 6.  The
-// quotient is a true division (rounded once in fp32): bf16 inputs often fall
-// exactly between two values, and a product with a rounded reciprocal would
-// break such ties to either side.
+// block's s to the top of e4m3, s takes the block's largest value to 6; what
+// lies above saturates.  Quotients are rounded once in fp32 (Divisor): bf16
+// inputs often fall exactly between two values, and a product with a rounded
+// reciprocal would break such ties to either side.
 // A block of zeros has scale 0 (mxfp4: 2^-127); a block that holds a NaN or
 // an infinity has a NaN scale.
 //
@@ -104,24 +104,29 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
 }
 
 // Division by a value that many others are divided by, as a product with its
-// reciprocal in two words (hi + lo, relative error below 2^-46): x hi is
-// rounded once, together with x lo, so the result is the rounded quotient
-// unless the quotient lies within 2^-46 of a midpoint between two fp32 values;
-// a quotient that is an fp32 value, a tie between two codes among them, comes
-// out exactly.  (8192 x 4096 bf16 to nvfp4, in the kernel's first form: 43.9 us
-// with __fdiv_rn for every value, 23.5 us with this and the loads issued
-// first.)  Divisors too far from 1 for the two words take the division.
+// reciprocal in two words: hi is within e < 2^-22 of it (relative), lo takes up
+// what hi misses and leaves e^2, so hi + lo is within 2^-44.  x hi is rounded
+// once, together with x lo, so the result is the rounded quotient unless the
+// quotient lies within 2^-44 of a midpoint between two fp32 values; a quotient
+// that is an fp32 value, a tie between two codes among them, comes out exactly.
+// (8192 x 4096 bf16 to nvfp4, in the kernel's first form: 43.9 us with
+// __fdiv_rn for every value, 23.5 us with this and the loads issued first.)
+// Divisors too far from 1 for the two words take the division, and so do values
+// above 1e30 divisors: x lo would overflow by itself and give the quotient the
+// sign of lo.
 struct Divisor {
-  float d, hi, lo;
+  float d, hi, lo, far;
   bool near;
   __device__ __forceinline__ explicit Divisor(float v) : d(v) {
     near = v > 1e-30f && v < 1e30f;
-    // any value within 2^-22 of the reciprocal: lo takes up what it misses
+    far = __fmul_rn(v, 1e30f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(v));
     lo = __fmul_rn(__fmaf_rn(-hi, v, 1.0f), hi);
   }
+  // Whether the two words serve for magnitudes up to x.
+  __device__ __forceinline__ bool fits(float x) const { return near && x <= far; }
   __device__ __forceinline__ float of(float x) const {
-    return near ? __fmaf_rn(x, hi, __fmul_rn(x, lo)) : __fdiv_rn(x, d);
+    return fits(x) ? __fmaf_rn(x, hi, __fmul_rn(x, lo)) : __fdiv_rn(x, d);
   }
 };
 
@@ -175,6 +180,7 @@ struct Scale<kNvBlock> {
   uint32_t byte;
   float step;
   Divisor by;
+  bool fits;
   __device__ __forceinline__ Scale(float amax, float t, const Divisor& by_t) : by(1.0f) {
     uint16_t c;
     const float s = amax > 0.0f ? by_t.of(__fmul_rn(amax, 1.0f / 6.0f)) : 0.0f;
@@ -182,11 +188,12 @@ struct Scale<kNvBlock> {
     byte = __float_as_uint(amax) < 0x7f800000u ? (uint32_t)c & 0xffu : 0x7fu;
     step = __fmul_rn(e4m3_value(byte), t);
     by = Divisor(step);
+    fits = by.fits(amax);
   }
   __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
     if (!(step > 0.0f)) return 0u;  // a block of zeros, or a NaN step
     float w[8];
-    if (by.near) {
+    if (fits) {
       const uint64_t hi = pair(by.hi, by.hi), lo = pair(by.lo, by.lo);
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {

@@ -399,3 +399,24 @@ def test_rows_that_overlap(fmt, dtype):
                 q, ref = mx4.quantize(a, fmt, transpose=tr), mx4.quantize(b, fmt, transpose=tr)
                 assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)
         assert torch.equal(mx4.linear(x, w), mx4.linear(c, w))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_values_far_above_the_tensor_scale_saturate(dtype, transpose):
+    """Spikes up to the type's largest value under a small calibrated scale: the block's scale is
+    e4m3's largest and the spike is 6 of it with its own sign, the values beside it as ever."""
+    rng = np.random.default_rng(14)
+    for t in np.exp(rng.uniform(np.log(1e-32), np.log(1e-6), 40)).astype(np.float32):
+        a = rng.standard_normal((32, 64)) * 900.0 * float(t)
+        spike = np.zeros(a.shape, bool)
+        spike[rng.integers(0, 32, 24), rng.integers(0, 64, 24)] = True
+        a[spike] = rng.uniform(1e36, 3.38e38, spike.sum()) * rng.choice([-1, 1], spike.sum())
+        x = dev(a.T if transpose else a, dtype)
+        q = mx4.quantize(x, "nvfp4", torch.tensor([t], device=DEV), transpose=transpose)
+        x64 = x.double().cpu().numpy()
+        x64 = x64.T if transpose else x64
+        bytes_, _ = linear_scales(q)
+        assert (bytes_[spike.reshape(32, 4, 16).any(2)] == 0x7e).all()
+        assert np.array_equal(unpack(q)[spike], 6 * np.sign(x64[spike]))
+        check(q, x64, "nvfp4", float(t))
