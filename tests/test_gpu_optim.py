@@ -344,3 +344,23 @@ def test_a_stream_given_by_hand():
         torch.cuda.current_stream().wait_stream(side)
     for a, b in zip(opt.params + opt.exp_avg, ref.params + ref.exp_avg):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("states", ["f32", "8bit"])
+def test_second_moments_below_the_normal_range(states):
+    """Squares of gradients from 1e-22 to 1e-18 under an eps far below their root: v is the fp32
+    one, its root is not dropped, and no step is longer than the formula's."""
+    eps = 1e-25
+    mags = np.float32(10.0) ** np.linspace(-21, -18, 7, dtype=np.float32)
+    g = np.repeat(mags, BLOCK).astype(np.float32)
+    params, grads = [torch.zeros(g.size, device=DEV)], [torch.from_numpy(g).to(DEV)]
+    opt = optim.AdamW(params, grads, lr=LR, betas=BETAS, eps=eps, weight_decay=0.0, states=states)
+    opt.step()
+    # fp32 as written in the header: products below 2^-126 are multiples of 2^-149
+    v = (g * g) * np.float32(1 - BETAS[1])
+    assert (v > 0).all() and (v < 2.0 ** -126).any()
+    if states == "f32":
+        assert np.array_equal(host(opt.exp_avg_sq[0]), v.astype(np.float64))
+    m = g.astype(np.float64) * (1 - BETAS[0])
+    step = LR / (1 - BETAS[0]) * m / (np.sqrt(v.astype(np.float64) / (1 - BETAS[1])) + eps)
+    assert np.all(np.abs(host(params[0]) + step) <= 24 * U * step)
