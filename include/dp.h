@@ -616,7 +616,8 @@ DP_API dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes);
  * written may overlap another buffer of the list.
  *
  * dp_adamw_step: step t >= 1, for every element, in fp32 with one rounding
- * per operation (the root, of any v above 0, and the quotient to 2^-22):
+ * per operation (with bf16 parameters or 8-bit states the root, of any v
+ * above 0, and the quotient to 2^-22):
  *   g = grad * *grad_scale          (grad_scale NULL: 1)
  *   m = m * beta1 + g * (1 - beta1)
  *   v = v * beta2 + (g * g) * (1 - beta2)

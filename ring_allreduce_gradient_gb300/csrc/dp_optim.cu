@@ -7,9 +7,9 @@
 //   m' = b1 m + (1 - b1) g'
 //   v' = b2 v + (1 - b2) g'^2
 //   p' = p (1 - lr wd) - lr / (1 - b1^t) * m' / (sqrt(v') / sqrt(1 - b2^t) + eps)
-// in fp32, one rounding per operation (no contraction), the root and the
-// quotient to 2^-22; the factors that depend on t alone formed in double on the
-// host.
+// in fp32, one rounding per operation (no contraction; with bf16 parameters or
+// 8-bit states the root and the quotient to 2^-22); the factors that depend on t
+// alone formed in double on the host.
 //
 // 8-bit states: m and r = sqrt(v) are e4m3 codes with one fp32 scale for each
 // 256 consecutive elements, the block's largest magnitude at e4m3's largest
@@ -143,34 +143,43 @@ struct Hyper {
   float coef, beta1, omb1, beta2, omb2, eps, step_size, inv_root;
 };
 
-// Root and quotient to 2^-22 of the step, which is itself far below the
-// parameter: the correctly rounded forms take about 20 instructions each and
-// a call for every zero (parameters that have had no gradient yet), which
-// bound the kernel: eight 8 Mi shards with 8-bit states take 194 us with them,
-// and 267 us where the gradients are zero, against 172 and 171.  The root is
-// the one that knows v below the normal range (1 us of the 172): a v flushed to
-// 0 would make the step lr m / eps.  The divisor is at least eps, which is in
-// the normal range.
+// Root and quotient.  EXACT, correctly rounded: fp32 parameters with 32-bit
+// states, whose traffic hides them (GPT-2-small-shaped step 524 us with and
+// without, one layer 29.7 and 29.2 us, 98 vectors 2.9 and 2.3 us on the GPU).
+// Otherwise to 2^-22 of the step, which is itself far below a parameter that is
+// rounded to 2^-8 (bf16) or comes from states that are (8-bit ones, 2^-4): the
+// rounded forms take about 20 instructions each and a call for every zero
+// (parameters that have had no gradient yet), which bound those kernels: eight 8
+// Mi shards with 8-bit states take 194 us with them, and 267 us where the
+// gradients are zero, against 172 and 171; a layer's bf16 parameters with 32-bit
+// states 17.9 us, against 14.2.  The root is the one that knows v below the
+// normal range (1 us of the 172): a v flushed to 0 would make the step
+// lr m / eps.  The divisor is at least eps, which is in the normal range.
+template <bool EXACT>
 __device__ __forceinline__ float root_of(float v) {
+  if constexpr (EXACT) return __fsqrt_rn(v);
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+template <bool EXACT>
 __device__ __forceinline__ float quotient(float a, float b) {
+  if constexpr (EXACT) return __fdiv_rn(a, b);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b));
   return __fmul_rn(a, r);
 }
 
 // One element: the new m, v and root of v, and the parameter's step.
+template <bool EXACT>
 __device__ __forceinline__ float adamw_one(float p, float g, float& m, float& v, float& root,
                                            float keep, const Hyper& h) {
   g = __fmul_rn(g, h.coef);
   m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.omb1));
   v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, g), h.omb2));
-  root = root_of(v);
+  root = root_of<EXACT>(v);
   const float denom = __fadd_rn(__fmul_rn(root, h.inv_root), h.eps);
-  return __fsub_rn(__fmul_rn(p, keep), __fmul_rn(h.step_size, quotient(m, denom)));
+  return __fsub_rn(__fmul_rn(p, keep), __fmul_rn(h.step_size, quotient<EXACT>(m, denom)));
 }
 
 // A block's largest magnitude over the warp.  Magnitudes order as their bit
@@ -193,6 +202,7 @@ constexpr int kAdamwCtas = 8;
 
 template <typename PT, typename GT, bool S8, int CAP>
 __global__ void __launch_bounds__(kThreads, kAdamwCtas) adamw_kernel(const __grid_constant__ AdamwParams<CAP> a) {
+  constexpr bool kExact = !S8 && std::is_same<PT, float>::value;
   const int lane = threadIdx.x & 31;
   const unsigned units = a.ustart[a.n];
   stream_order();
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kAdamwCtas) adamw_kernel(const __gri
         v[i] = __fmul_rn(v[i], rs);
         v[i] = __fmul_rn(v[i], v[i]);
       }
-      p[i] = adamw_one(p[i], g[i], m[i], v[i], root[i], keep, h);
+      p[i] = adamw_one<kExact>(p[i], g[i], m[i], v[i], root[i], keep, h);
     }
     if constexpr (S8) {
       if (!vec) {  // lanes past the end take no part in the block's largest value

@@ -364,3 +364,24 @@ def test_second_moments_below_the_normal_range(states):
     m = g.astype(np.float64) * (1 - BETAS[0])
     step = LR / (1 - BETAS[0]) * m / (np.sqrt(v.astype(np.float64) / (1 - BETAS[1])) + eps)
     assert np.all(np.abs(host(params[0]) + step) <= 24 * U * step)
+
+
+@pytest.mark.parametrize("gd", [torch.float32, torch.bfloat16])
+def test_the_step_of_fp32_parameters_and_states_is_the_rounded_operations(gd):
+    """Every operation of the step rounded once to fp32: the bits of the same steps in numpy."""
+    f = np.float32
+    n, t = 5000, 8
+    opt, _ = make([n], torch.float32, gd, 0, step=t - 1, decay=0.1)
+    for x in (opt.grads[0], opt.exp_avg[0], opt.exp_avg_sq[0]):
+        x[:9] = 0
+    p, g, m, v = [host(x).astype(f) for x in (opt.params[0], opt.grads[0], opt.exp_avg[0],
+                                               opt.exp_avg_sq[0])]
+    opt.step(grad_scale=torch.tensor([0.625], device=DEV))
+    g = g * f(0.625)
+    m = m * f(BETAS[0]) + g * f(1 - BETAS[0])
+    v = v * f(BETAS[1]) + (g * g) * f(1 - BETAS[1])
+    denom = np.sqrt(v) * f(1 / np.sqrt(1 - BETAS[1] ** t)) + f(EPS)
+    want = p * f(1 - LR * 0.1) - f(LR / (1 - BETAS[0] ** t)) * (m / denom)
+    assert np.array_equal(host(opt.params[0]), want.astype(np.float64))
+    assert np.array_equal(host(opt.exp_avg[0]), m.astype(np.float64))
+    assert np.array_equal(host(opt.exp_avg_sq[0]), v.astype(np.float64))
