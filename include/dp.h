@@ -630,12 +630,19 @@ DP_API dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes);
  * the smallest code (2^-9).  Of a block whose largest magnitude is below
  * 2^-110 m is dropped.
  * grad_scale: NULL or a device float (dp_grad_norm's coef).  A NaN there
- * leaves every buffer as it is.
+ * leaves every buffer as it is: the step is left out.
  * schedule: NULL, or 3 device floats (lr, 1 - beta1^t, 1 - beta2^t) that are
  * read when the kernel runs in place of the call's values: a captured step
  * is replayed with new ones.
  * Requires 0 <= beta < 1, eps >= 2^-126, finite lr.  Steps of one object are
  * serialised on the host; the caller orders them on the GPU.
+ *
+ * dp_adamw_count_skips: skips is a device word (4-byte aligned, outside the
+ * list's buffers) to which every later step that is left out adds 1 when it
+ * runs, or NULL, as at creation.  A step with a word takes t = step - *skips in
+ * its bias corrections (without schedule), so that steps left out, which the
+ * host does not know of, do not count; where *skips > 0 the corrections are
+ * formed in fp32, within 2^-21.  The caller zeroes it before the first step.
  * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
  */
 #define DP_STATE_BLOCK 256
@@ -657,6 +664,7 @@ DP_API dp_status_t dp_adamw_create(const dp_adamw_tensor_t* tensors, int n,
 DP_API dp_status_t dp_adamw_step(dp_adamw_t* o, double lr, double beta1, double beta2, double eps,
                                  long long step, const float* grad_scale, const float* schedule,
                                  dp_stream_t stream);
+DP_API dp_status_t dp_adamw_count_skips(dp_adamw_t* o, unsigned int* skips);
 DP_API void dp_adamw_destroy(dp_adamw_t* o);
 
 /*

@@ -133,6 +133,7 @@ def load() -> ctypes.CDLL:
                                                        ctypes.POINTER(ctypes.c_size_t)],
             "dp_adamw_create": [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32,
                                 ctypes.POINTER(ctypes.c_void_p)],
+            "dp_adamw_count_skips": [vp, vp],
             "dp_adamw_step": [vp, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                               ctypes.c_double, ctypes.c_longlong, vp, vp, vp],
             "dp_set_cta_limits": [i32, i32],
@@ -542,6 +543,10 @@ def dp_adamw_step(h, lr, beta1, beta2, eps, step, grad_scale=None, schedule=None
     st = load().dp_adamw_step(h, lr, beta1, beta2, eps, step, _ptr(grad_scale), _ptr(schedule),
                               _stream(stream))
     return _ret(st, "dp_adamw_step", check)
+
+
+def dp_adamw_count_skips(h, skips, check=True) -> int:
+    return _ret(load().dp_adamw_count_skips(h, _ptr(skips)), "dp_adamw_count_skips", check)
 
 
 def dp_adamw_destroy(h) -> None:

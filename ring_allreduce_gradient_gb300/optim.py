@@ -83,6 +83,10 @@ class AdamW:
     * ``states="8bit"``: ``exp_avg`` and ``exp_avg_sq`` are float8_e4m3fn codes
       of m and of sqrt(v), with ``exp_avg_scale`` / ``exp_avg_sq_scale``, one
       fp32 scale for each 256 elements of a tensor.
+
+    ``steps`` counts the calls of ``step``; ``skipped``, one int32 on the device,
+    those that a NaN coefficient left out, which the bias corrections do not
+    count.  A run is resumed with ``step = opt.steps - int(opt.skipped)``.
     """
 
     def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -126,6 +130,8 @@ class AdamW:
                         self.exp_avg_sq_scale or none, numels, decay))
         _, self.handle = B.dp_adamw_create(rows, len(rows), _code(self.params[0]),
                                            _code(self.grads[0]), _STATES[states])
+        self.skipped = torch.zeros(1, dtype=torch.int32, device=dev)
+        B.dp_adamw_count_skips(self.handle, self.skipped)
 
     def step(self, lr=None, grad_scale=None, schedule=None, stream=None) -> None:
         """One step.  ``lr`` replaces the constructor's for this step;

@@ -385,3 +385,72 @@ def test_the_step_of_fp32_parameters_and_states_is_the_rounded_operations(gd):
     assert np.array_equal(host(opt.params[0]), want.astype(np.float64))
     assert np.array_equal(host(opt.exp_avg[0]), m.astype(np.float64))
     assert np.array_equal(host(opt.exp_avg_sq[0]), v.astype(np.float64))
+
+
+@pytest.mark.parametrize("states", ["f32", "8bit"])
+@pytest.mark.parametrize("count", [1, 500])
+def test_a_left_out_step_does_not_count(states, count):
+    """Steps with a NaN coefficient before and between others, on one launch and on two: each step
+    that is taken is the formula's for the number of steps taken.  With steps left out the factors
+    of t are formed in fp32: 8u in lr / (1 - beta1^t) and 5u in the root's, so 16u of the step
+    beside the other errors."""
+    sizes = [257 + i % 3 for i in range(count)]
+    opt, decay = make(sizes, torch.float32, torch.float32, 0, states=states, step=0,
+                      decay=[0.0] * count)
+    for x in opt.exp_avg + opt.exp_avg_sq:
+        x.view(torch.uint8).zero_()
+    nan, one = (torch.tensor([c], device=DEV) for c in (float("nan"), 1.0))
+    taken = 0
+    for skip in (True, False, False, True, True, False, False):
+        old = [[host(x[0]), host(x[1])] + ([host(x[2]), host(x[3])] if states == "f32" else
+               [decode(x[2], x[4]), decode(x[3], x[5]) ** 2])
+               for x in zip(opt.params, opt.grads, opt.exp_avg, opt.exp_avg_sq,
+                            *([opt.exp_avg_scale, opt.exp_avg_sq_scale] if states == "8bit" else []))]
+        opt.step(grad_scale=nan if skip else one)
+        taken += not skip
+        for i in {0, count - 1}:
+            if skip:
+                assert np.array_equal(host(opt.params[i]), old[i][0])
+                continue
+            p, g, m, v = old[i]
+            want, _, _, step = formula(p, g, m, v, taken, 0.0)
+            terms = BETAS[0] * np.abs(m) + (1 - BETAS[0]) * np.abs(g)
+            v1 = BETAS[1] * v + (1 - BETAS[1]) * g * g
+            size = LR / (1 - BETAS[0] ** taken) * terms / (np.sqrt(v1 / (1 - BETAS[1] ** taken)) + EPS)
+            assert np.all(np.abs(host(opt.params[i]) - want) <=
+                          3 * U * np.abs(p) + 24 * U * (step + size) + 16 * U * step + 1e-38)
+    assert opt.steps == 7 and int(opt.skipped) == 3
+    # a run resumed with the steps taken goes on as one that has left none out
+    other = optim.AdamW([p.clone() for p in opt.params], opt.grads, lr=LR, betas=BETAS, eps=EPS,
+                        weight_decay=0.0, states=states, step=opt.steps - int(opt.skipped),
+                        **{k: [x.clone() for x in getattr(opt, k)] for k in
+                           (("exp_avg", "exp_avg_sq") if states == "f32" else
+                            ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"))})
+    before = [host(p) for p in opt.params]
+    opt.step(grad_scale=one)
+    other.step(grad_scale=one)
+    for a, b, c in zip(opt.params, other.params, before):
+        moved = np.abs(host(b) - c)
+        assert np.all(np.abs(host(a) - host(b)) <= 16 * U * moved + 3 * U * np.abs(c))
+
+
+def test_left_out_steps_of_a_replayed_graph():
+    """Replays with a NaN coefficient add to the count; the schedule's corrections stay the caller's."""
+    opt, _ = make([300], torch.float32, torch.float32, 0, step=4)
+    ref, _ = make([300], torch.float32, torch.float32, 0, step=4)
+    coef = torch.ones(1, device=DEV)
+    sched = torch.tensor([LR, 1 - BETAS[0] ** 5, 1 - BETAS[1] ** 5], dtype=torch.float64).float().to(DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            opt.step(grad_scale=coef, schedule=sched)
+    for c in (float("nan"), float("nan"), 1.0):
+        coef.fill_(c)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+    ref.step(grad_scale=torch.ones(1, device=DEV), schedule=sched)
+    assert int(opt.skipped) == 2 and int(ref.skipped) == 0
+    assert torch.equal(opt.params[0], ref.params[0])

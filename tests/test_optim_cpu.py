@@ -150,3 +150,17 @@ def test_the_tensor_objects_check_their_lists():
     with pytest.raises(B.DpError):
         opt.step(lr=float("nan"))
     assert opt.steps == 0
+
+
+def test_the_count_of_left_out_steps_checks_its_word():
+    rows = [row(), row(1)]
+    _, h = B.dp_adamw_create(rows, 2, B.DP_FP32, B.DP_FP32, B.DP_STATE_FP32)
+    count = lambda p, h=h: B.dp_adamw_count_skips(h, p, check=False)  # noqa: E731
+    assert count(fake(20)) == B.DP_OK and count(None) == B.DP_OK
+    assert count(fake(20, 2)) == UNSUPPORTED
+    assert count(fake(0, 3996)) == ALIAS and count(fake(0, 4000)) == B.DP_OK
+    assert count(fake(9)) == ALIAS                             # a gradient, which is read
+    assert count(fake(20), h=0) == INVALID
+    B.dp_adamw_destroy(h)
+    opt = optim.AdamW([torch.zeros(4)], [torch.zeros(4)])
+    assert opt.skipped.tolist() == [0]
