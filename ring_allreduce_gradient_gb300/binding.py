@@ -197,6 +197,23 @@ def _stream(stream) -> int | None:
     return int(stream.cuda_stream)
 
 
+def _stream_on(device, where: str) -> int | None:
+    """The handle of PyTorch's current stream, for a call ``where`` on tensors of
+    ``device``: it is launched on the current CUDA device, and their pointers mean
+    nothing there if they lie anywhere else."""
+    if _raw_stream:
+        cur = _current_device()
+        if device.index == cur:
+            return _raw_stream(cur)
+    elif device.type == "cuda":
+        st = _stream(None)
+        import torch
+        if device.index == torch.cuda.current_device():
+            return st
+    raise DpError(DP_ERR_UNSUPPORTED,
+                  f"{where}: tensors on {device}, which is not the current CUDA device")
+
+
 _DTYPE_CODES: dict = {}  # dtype (string or torch dtype) -> code, filled as they are seen
 
 

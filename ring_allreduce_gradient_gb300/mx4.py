@@ -123,7 +123,8 @@ def tensor_scale(x, out=None, stream=None) -> torch.Tensor:
     out = torch.empty(1, dtype=torch.float32, device=dev) if out is None else out
     _check_scale(out, dev)
     ws = torch.zeros(B.dp_grad_norm_workspace_size(len(xs)), dtype=torch.uint8, device=dev)
-    B.dp_mx4_tensor_scale(xs, [t.numel() for t in xs], len(xs), _code(xs[0]), out, ws)
+    B.dp_mx4_tensor_scale(xs, [t.numel() for t in xs], len(xs), _code(xs[0]), out, ws,
+                          stream=B._stream_on(dev, "tensor_scale"))
     return out
 
 
@@ -158,7 +159,7 @@ def quantize(x, format: str = "mxfp4", tensor_scale=None, transpose: bool = Fals
     c = q._c
     st = (B._lib or B.load()).dp_mx4_quantize(
         B._parray(xs), K, rows, cols, ld, _code(x0), fmt, 1 if transpose else 0,
-        c.tensor_scale, c.codes, c.scales, B._stream(None))
+        c.tensor_scale, c.codes, c.scales, B._stream_on(dev, "quantize"))
     if st:
         raise B.DpError(st, "dp_mx4_quantize")
     return q
@@ -191,7 +192,7 @@ def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     c = q._c
     st = (B._lib or B.load()).dp_mx4_dequantize(c.codes, c.scales, rows, cols, FORMATS[format],
                                                 c.tensor_scale, out.data_ptr(), _DT[dtype],
-                                                B._stream(None))
+                                                B._stream_on(dev, "dequantize"))
     if st:
         raise B.DpError(st, "dp_mx4_dequantize")
     return out
@@ -223,7 +224,7 @@ def matmul(x: Mx4Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch
     arr = _shards(w_shards, D, format, dev)
     y = torch.empty((M, K * w_shards[0].rows), dtype=y_dtype, device=dev)
     B.dp_allgather_matmul_mx4(x._c, M, D, arr, K, w_shards[0].rows, FORMATS[format], y,
-                              _DT[y_dtype])
+                              _DT[y_dtype], stream=B._stream_on(dev, "matmul"))
     return y
 
 
@@ -254,7 +255,7 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
     st = (B._lib or B.load()).dp_allgather_linear_mx4(
         x.data_ptr(), M, D, ld, _code(x),
         None if x_scale is None else x_scale.data_ptr(), arr, K, F, FORMATS[format],
-        y.data_ptr(), _DT[y_dtype], ws.data_ptr(), nbytes, B._stream(None))
+        y.data_ptr(), _DT[y_dtype], ws.data_ptr(), nbytes, B._stream_on(dev, "linear"))
     if st:
         raise B.DpError(st, "dp_allgather_linear_mx4")
     return y

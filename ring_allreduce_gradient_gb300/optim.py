@@ -52,7 +52,7 @@ class GradNorm:
     def __init__(self, grads, max_norm: float = float("inf")):
         self.grads = _check_list("grads", grads)
         self.max_norm = float(max_norm)
-        dev = self.grads[0].device
+        dev = self._device = self.grads[0].device
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.coef = torch.ones(1, dtype=torch.float32, device=dev)
         self._n = len(self.grads)
@@ -63,8 +63,9 @@ class GradNorm:
         self._numels = B._sizes(g.numel() for g in self.grads)
 
     def __call__(self, stream=None):
+        here = B._stream_on(self._device, "GradNorm")
         B.dp_grad_norm(self._ptrs, self._numels, self._n, self._dtype, self.max_norm, self.norm,
-                       self.coef, self._ws, stream=stream)
+                       self.coef, self._ws, stream=here if stream is None else stream)
         return self.norm, self.coef
 
 
@@ -97,7 +98,7 @@ class AdamW:
             raise ValueError(f"states: 'f32' or '8bit', not {states!r}")
         self.params = _check_list("params", params)
         numels = [p.numel() for p in self.params]
-        dev = self.params[0].device
+        dev = self._device = self.params[0].device
         self.grads = _check_list("grads", grads, numels, device=dev)
         self.copies = None if copies is None else \
             _check_list("copies", copies, numels, torch.bfloat16, dev)
@@ -141,10 +142,12 @@ class AdamW:
         captured in a graph and replayed."""
         for name, t, n in (("grad_scale", grad_scale, 1), ("schedule", schedule, 3)):
             if t is not None and (t.dtype != torch.float32 or t.numel() != n or
-                                  t.device != self.params[0].device or not t.is_contiguous()):
-                raise ValueError(f"{name}: {n} fp32 value(s) on {self.params[0].device}")
+                                  t.device != self._device or not t.is_contiguous()):
+                raise ValueError(f"{name}: {n} fp32 value(s) on {self._device}")
+        here = B._stream_on(self._device, "AdamW.step")
         B.dp_adamw_step(self.handle, self.lr if lr is None else lr, self.betas[0], self.betas[1],
-                        self.eps, self.steps + 1, grad_scale, schedule, stream)
+                        self.eps, self.steps + 1, grad_scale, schedule,
+                        here if stream is None else stream)
         self.steps += 1
 
     def __del__(self):

@@ -225,3 +225,30 @@ def test_rows_that_the_library_gets_are_the_views(i):
     if rows:
         assert (rows - 1) * ld + cols <= t.untyped_storage().nbytes() // 4 - t.storage_offset()
         assert torch.equal(t.as_strided((rows, cols), (ld, 1)), x)
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    """Host memory, or another GPU's: the library is not called at all."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    q = mx4.Mx4Tensor(torch.zeros(4 * 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8),
+                      4, 64, "mxfp4")
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or (b"" if name.endswith("_string") else 0)
+
+    monkeypatch.setattr(B, "_lib", Library())
+    for with_gpu in (False, True):
+        if with_gpu:      # as on a machine whose current device is cuda:0
+            monkeypatch.setattr(B, "_raw_stream", lambda d: 0)
+            monkeypatch.setattr(B, "_current_device", lambda: 0)
+        for call in (lambda: mx4.quantize(x), lambda: mx4.quantize([x, x]),
+                     lambda: mx4.dequantize(q), lambda: mx4.matmul(q, [q]),
+                     lambda: mx4.linear(x, [q]), lambda: mx4.tensor_scale(x)):
+            with pytest.raises(B.DpError, match="tensors on cpu, which is not the current"):
+                call()
+    assert B._stream_on(torch.device("cuda", 0), "here") == 0
+    with pytest.raises(B.DpError, match="cuda:1"):
+        B._stream_on(torch.device("cuda", 1), "here")
+    assert [c for c in calls if not c.endswith(("_size", "_string"))] == []

@@ -164,3 +164,12 @@ def test_the_count_of_left_out_steps_checks_its_word():
     B.dp_adamw_destroy(h)
     opt = optim.AdamW([torch.zeros(4)], [torch.zeros(4)])
     assert opt.skipped.tolist() == [0]
+
+
+def test_steps_on_host_tensors_are_refused():
+    g = [torch.zeros(10), torch.zeros(4)]
+    opt, norm = optim.AdamW([torch.zeros(10), torch.zeros(4)], g), optim.GradNorm(g)
+    for call in (opt.step, norm, lambda: opt.step(stream=0), lambda: norm(stream=0)):
+        with pytest.raises(B.DpError, match="tensors on cpu, which is not the current"):
+            call()
+    assert opt.steps == 0
