@@ -169,10 +169,12 @@ def _rows(x):
     """A matrix as the library takes it, and the elements between its rows, which
     are at least a row's length.  Rows that overlap (one row expanded to many, a
     window moved over a vector) are copied out."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("need a matrix with unit stride along its rows")
+    if x.dim() != 2:
+        raise ValueError(f"need a matrix, got {tuple(x.shape)}: flatten the other dimensions first")
     rows, cols = x.shape
-    ld = x.stride(0)
+    ld, unit = x.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError("need a matrix with unit stride along its rows")
     if rows <= 1:
         return x, cols
     if ld < cols:
@@ -231,7 +233,9 @@ def matmul(x: Mx4Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch
 def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
            stream=None) -> torch.Tensor:
     """y = x . w^T with x [M, D] quantised to the shards' format on the way
-    (``x_scale``: its nvfp4 tensor scale), in one call."""
+    (``x_scale``: its nvfp4 tensor scale), in one call.  Like every call here it
+    records no gradient: an autograd function calls it in its forward, and its
+    backward products (above) in its backward."""
     if stream is not None:
         with _on(stream, x.device):
             return linear(x, w_shards, x_scale, y_dtype)

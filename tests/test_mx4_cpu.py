@@ -252,3 +252,13 @@ def test_tensors_off_the_current_device_are_refused(monkeypatch):
     with pytest.raises(B.DpError, match="cuda:1"):
         B._stream_on(torch.device("cuda", 1), "here")
     assert [c for c in calls if not c.endswith(("_size", "_string"))] == []
+
+
+@pytest.mark.parametrize("shape", [(64,), (2, 4, 64), (1, 1, 2, 64)])
+def test_what_is_no_matrix_is_named(shape):
+    x = torch.zeros(shape, dtype=torch.bfloat16)
+    q = mx4.Mx4Tensor(torch.zeros(4 * 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8),
+                      4, 64, "mxfp4")
+    for call in (lambda: mx4.linear(x, [q]), lambda: mx4.quantize(x), lambda: mx4.quantize([x])):
+        with pytest.raises(ValueError, match=r"need a matrix, got \(.*\): flatten"):
+            call()
