@@ -577,8 +577,10 @@ DP_API dp_status_t dp_reducer_wait(dp_reducer_t* r, dp_stream_t stream);
  * max_norm > 0 (infinity: coef is 1).  An empty list has norm 0.
  * Squares are summed in fp32 over 32 elements, pairs of such sums are added
  * in fp32, and the rest is in double; the order is fixed by the sizes and
- * alignments, so a list gives the same bits under any CTA limit.  A gradient
- * above 1.8e19 in magnitude overflows its square and makes the norm infinite.
+ * alignments, so a list gives the same bits under any CTA limit.  fp32 bounds
+ * the squares: one element above 1.8e19, or 64 that are summed together above
+ * 2.3e18, make the norm infinite (and coef NaN); below 1e-19 squares lose bits,
+ * below 2.6e-23 they are 0.  In between the norm is within 17 * 2^-24 of itself.
  *
  * workspace: device memory of at least dp_grad_norm_workspace_size(n) bytes,
  * 16-byte aligned, overlapping nothing; its first 4 bytes are zero before

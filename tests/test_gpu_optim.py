@@ -454,3 +454,27 @@ def test_left_out_steps_of_a_replayed_graph():
     ref.step(grad_scale=torch.ones(1, device=DEV), schedule=sched)
     assert int(opt.skipped) == 2 and int(ref.skipped) == 0
     assert torch.equal(opt.params[0], ref.params[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [5000, 4096])
+def test_the_range_of_the_norm(n, dtype):
+    """What fp32 squares hold, as the header says: every element up to 2.3e18 in magnitude, a single
+    one up to 1.8e19, none above; tiny ones lose bits, and 0 is left below half of 2^-149."""
+    norm = lambda x: [float(v) for v in optim.GradNorm([x], 1.0)()]  # noqa: E731
+    x = torch.full((n,), 2.25e18, dtype=dtype, device=DEV)
+    want = np.sqrt((host(x) ** 2).sum())
+    got, coef = norm(x)
+    assert abs(got - want) <= 19 * U * want and abs(coef - 1 / want) <= 24 * U / want
+    got, coef = norm(torch.full((n,), 4e18, dtype=dtype, device=DEV))
+    assert np.isinf(got) and np.isnan(coef)
+    x.zero_()
+    x[77] = 1.8e19
+    assert abs(norm(x)[0] - float(x[77])) <= 19 * U * 1.8e19
+    x[77] = 1.9e19
+    assert np.isinf(norm(x)[0])
+    x.fill_(2e-19)
+    want = np.sqrt((host(x) ** 2).sum())
+    assert abs(norm(x)[0] - want) <= 19 * U * want
+    assert norm(x.fill_(2.5e-23))[0] == 0
+    assert norm(x.fill_(2.8e-23))[0] > 0
