@@ -2,7 +2,9 @@
 its clip coefficient, and AdamW with 32- or 8-bit states over a list of
 tensors.  The tensors are those of a training step: parameter shards with the
 gradients that a reduce-scatter or the Reducer leaves in place each step, so
-each object takes them once and a step passes no lists.
+each object takes them once and a step passes no lists.  It works on the memory
+that they have when it is made, and keeps that memory: a tensor that is given
+other storage later (``p.data = ...``, ``module.to(...)``) is not followed.
 
     clip = GradNorm(grads, max_norm=1.0)
     opt = AdamW(params, grads, lr=3e-4, states="8bit", copies=bf16_shards)
@@ -39,6 +41,12 @@ def _check_list(name, ts, numels=None, dtype=None, device=None):
     return ts
 
 
+def _storages(*lists):
+    """What the addresses of some tensors point into, kept from being freed when a
+    tensor is given other storage (``p.data = ...``, ``module.to(...)``)."""
+    return [t.untyped_storage() for ts in lists if ts is not None for t in ts]
+
+
 class GradNorm:
     """The global norm of a list of gradients and its clip coefficient.
 
@@ -60,6 +68,7 @@ class GradNorm:
                                device=dev)
         self._dtype = _code(self.grads[0])
         self._ptrs = B._parray(self.grads)
+        self._held = _storages(self.grads)
         self._numels = B._sizes(g.numel() for g in self.grads)
 
     def __call__(self, stream=None):
@@ -125,6 +134,8 @@ class AdamW:
         self.exp_avg_sq_scale = kept("exp_avg_sq_scale", exp_avg_sq_scale, blocks,
                                      torch.float32) if eight else None
         self.lr, self.betas, self.eps, self.steps = lr, tuple(betas), eps, int(step)
+        self._held = _storages(self.params, self.grads, self.copies, self.exp_avg,
+                               self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale)
         none = [None] * len(numels)
         rows = list(zip(self.params, self.grads, self.copies or none, self.exp_avg,
                         self.exp_avg_sq, self.exp_avg_scale or none,

@@ -173,3 +173,16 @@ def test_steps_on_host_tensors_are_refused():
         with pytest.raises(B.DpError, match="tensors on cpu, which is not the current"):
             call()
     assert opt.steps == 0
+
+
+def test_the_memory_of_a_list_outlives_a_tensor_that_leaves_it():
+    """A step writes through the addresses it was made with: their storage is not freed before it."""
+    p, g = [torch.zeros(1000), torch.zeros(70)], [torch.ones(1000), torch.ones(70)]
+    c, m = [x.bfloat16() for x in p], [torch.zeros_like(x) for x in p]
+    was = [t.data_ptr() for ts in (p, g, c, m) for t in ts]
+    opt, norm = optim.AdamW(p, g, copies=c, exp_avg=m), optim.GradNorm(g)
+    for ts in (p, g, c, m):
+        for t in ts:
+            t.data = torch.zeros_like(t)
+    assert set(was) <= {s.data_ptr() for s in opt._held}
+    assert {x for x in was[2:4]} == {s.data_ptr() for s in norm._held}
