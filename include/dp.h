@@ -631,6 +631,14 @@ DP_API dp_status_t dp_grad_norm_workspace_size(int n, size_t* bytes);
  * largest magnitude of the block), and a sqrt(v) above zero keeps at least
  * the smallest code (2^-9).  Of a block whose largest magnitude is below
  * 2^-110 m is dropped.
+ * Half a code's step is 3 to 6 % of a root, and a stored root moves only in a
+ * step that changes it by that much; smaller changes are rounded away each time,
+ * and the root follows its block's scale.  At beta2 <= 0.95 roots follow v (the
+ * middle nine tenths are within 0.9 to 1.25 times theirs).  Nearer to 1 they do
+ * not follow a v that shrinks: where the gradients of half of each block fell to
+ * a tenth, those roots were 3.4 times too large (median) 3000 steps later at
+ * beta2 = 0.999, 13 times at 0.99, and the block's other roots 0.8 and 1.4 times
+ * theirs.  32-bit states have none of this.
  * grad_scale: NULL or a device float (dp_grad_norm's coef).  A NaN there
  * leaves every buffer as it is: the step is left out.
  * schedule: NULL, or 3 device floats (lr, 1 - beta1^t, 1 - beta2^t) that are

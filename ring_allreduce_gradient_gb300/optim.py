@@ -92,7 +92,10 @@ class AdamW:
     * ``states="f32"``: ``exp_avg`` and ``exp_avg_sq``, fp32;
     * ``states="8bit"``: ``exp_avg`` and ``exp_avg_sq`` are float8_e4m3fn codes
       of m and of sqrt(v), with ``exp_avg_scale`` / ``exp_avg_sq_scale``, one
-      fp32 scale for each 256 elements of a tensor.
+      fp32 scale for each 256 elements of a tensor.  Made for beta2 of 0.95 or
+      less: nearer to 1 (the default among them) a step's change of v is below
+      the codes' rounding, and stored roots stay several times too large where
+      gradients shrink (figures: ``include/dp.h``).
 
     ``steps`` counts the calls of ``step``; ``skipped``, one int32 on the device,
     those that a NaN coefficient left out, which the bias corrections do not

@@ -478,3 +478,39 @@ def test_the_range_of_the_norm(n, dtype):
     assert abs(norm(x)[0] - want) <= 19 * U * want
     assert norm(x.fill_(2.5e-23))[0] == 0
     assert norm(x.fill_(2.8e-23))[0] > 0
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.999])
+def test_adamw_8bit_states_over_a_long_run(beta2):
+    """After 1200 steps, half of each block's gradients a tenth from step 600 on: the next step is
+    still the formula's from the stored states, and its states the nearest codes.  At beta2 = 0.95
+    the stored roots follow v: a code is held until it is off by half a code's step (6 %) and v
+    itself wanders between steps, so three quarters of the 1.25 in the header bound the median."""
+    n = 64 * BLOCK
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    params, grads = [torch.zeros(n, device=DEV)], [torch.zeros(n, device=DEV)]
+    opt = optim.AdamW(params, grads, lr=LR, betas=(BETAS[0], beta2), eps=EPS, weight_decay=0.0,
+                      states="8bit")
+    low = torch.arange(n, device=DEV) % BLOCK < BLOCK // 2
+    v = torch.zeros(n, dtype=torch.float64, device=DEV)
+    for t in range(1, 1202):
+        g = torch.randn(n, device=DEV, generator=gen) * 1e-3
+        grads[0].copy_(torch.where(low, g * 0.1, g) if t > 600 else g)
+        v.mul_(beta2).addcmul_(grads[0].double(), grads[0].double(), value=1 - beta2)
+        if t == 1201:
+            old = [host(params[0]), host(grads[0]), decode(opt.exp_avg[0], opt.exp_avg_scale[0]),
+                   decode(opt.exp_avg_sq[0], opt.exp_avg_sq_scale[0]) ** 2]
+        opt.step()
+    p, g, m, v0 = old
+    m1, v1 = BETAS[0] * m + (1 - BETAS[0]) * g, beta2 * v0 + (1 - beta2) * g * g
+    size = LR / (1 - BETAS[0] ** 1201) / (np.sqrt(v1 / (1 - beta2 ** 1201)) + EPS)
+    terms = BETAS[0] * np.abs(m) + (1 - BETAS[0]) * np.abs(g)
+    assert np.all(np.abs(host(params[0]) - (p - size * m1)) <=
+                  3 * U * np.abs(p) + 24 * U * size * (np.abs(m1) + terms) + 1e-38)
+    check_codes(opt.exp_avg[0], opt.exp_avg_scale[0], m1)
+    check_codes(opt.exp_avg_sq[0], opt.exp_avg_sq_scale[0], np.sqrt(v1), positive=True)
+    if beta2 == 0.95:
+        ratio = decode(opt.exp_avg_sq[0], opt.exp_avg_sq_scale[0]) / np.sqrt(host(v))
+        for half in (low.cpu().numpy(), ~low.cpu().numpy()):
+            a, b, c = np.quantile(ratio[half], [0.05, 0.5, 0.95])
+            assert 0.85 < a and 0.9 < b < 1.19 and c < 1.35
