@@ -15,8 +15,9 @@ so scaling is weak and no collective is on the data path.
 
 At N=1 it also measures the other rows of the path (all-reduce and
 all-gather at K=8, the fused all-gather + GEMM, and the variable-length
-step) and prints them under "rows".  ``--impl reference`` times the CPU
-oracle instead, on bounded samples of the same workload.
+step): their key figures end the line, all of them (some 20 KB) go to a file,
+``--rows-out``.  ``--impl reference`` times the CPU oracle instead, on bounded
+samples of the same workload.
 """
 from __future__ import annotations
 
@@ -621,11 +622,8 @@ def run_ours(args):
             "cpu_baseline": cpu,
             "gpu_launches": args.steps * launches_per_step,
             "clocks": clk.summary(),
-            "rows": rows,
         }
-        if rows is not None:
-            line["summary"] = rows_summary(rows, cpu)
-        print(json.dumps(line), flush=True)
+        print(report(line, rows, cpu, args.rows_out), flush=True)
     if ws > 1:
         dist.destroy_process_group()
 
@@ -998,6 +996,20 @@ def measure_rows(dev, stream, hbm_peak, bf16_peak, peak_kind, args):
     del wl, grads, tables, accs, o32, o16
     torch.cuda.empty_cache()
     return rows
+
+
+def report(line, rows, cpu, path):
+    """The printed line, with the other rows' key figures; the rows themselves go
+    to ``path``: with them the line was 25 KB, too long for what reads it."""
+    if rows is not None:
+        try:
+            with open(path, "w") as f:
+                json.dump(rows, f)
+                f.write("\n")
+        except OSError as exc:  # the line is printed all the same
+            print(f"warning: {path}: {exc}", file=sys.stderr)
+        line = dict(line, summary=rows_summary(rows, cpu))
+    return json.dumps(line)
 
 
 def rows_summary(rows, cpu):
@@ -1557,6 +1569,8 @@ def main():
                                            "ddp25", "ddp100"],
                     default="rs", help="rs (the headline) or one other row on its own")
     ap.add_argument("--no-rows", action="store_true", help="skip the other rows' measurements")
+    ap.add_argument("--rows-out", default=os.path.join(ROOT, "bench_rows.json"),
+                    help="the file that gets the other rows' measurements (JSON)")
     ap.add_argument("--c3-only", action="store_true",
                     help="print only the collective || GEMM concurrency measurements")
     ap.add_argument("--pipeline-only", action="store_true",

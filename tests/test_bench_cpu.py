@@ -91,3 +91,18 @@ def test_rows_summary_is_small_and_ends_with_the_gemm():
     assert "sample" not in s["cpu_oracle_rows"]
     assert len(json.dumps(s)) < 2000
     assert bench.rows_summary(None, None) == {"rows": "not measured"}
+
+
+def test_the_line_stays_short(tmp_path):
+    """The rows go to their file, whole; the line keeps their summary and is one line of JSON."""
+    rows = {f"row{i}": {"ms": 0.1, "note": "x" * 200} for i in range(100)}
+    rows["agmm_b"] = {"TFLOP/s": 1600.0, "frac_bf16": 0.83, "ms": 0.171}
+    head = {"metric": "m", "value": 1.0, "unit": "GB/s"}
+    text = bench.report(head, rows, None, str(tmp_path / "rows.json"))
+    line = json.loads(text)
+    assert "\n" not in text and len(text) < 2500 and "rows" not in line
+    assert line["value"] == 1.0 and list(line["summary"])[-1] == "agmm_b"
+    assert json.loads((tmp_path / "rows.json").read_text()) == rows
+    assert json.loads(bench.report(head, None, None, str(tmp_path / "none"))) == head
+    assert not (tmp_path / "none").exists()
+    assert "summary" in json.loads(bench.report(head, rows, None, str(tmp_path / "no" / "such")))
