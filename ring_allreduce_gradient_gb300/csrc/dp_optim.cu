@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_kernel(const __grid_cons
       return;
     }
     const float norm = (float)sqrt(all);
-    const float c = __fmul_rn(__frcp_rn(__fadd_rn(norm, 1e-6f)), a.max_norm);
+    const float c = __fdiv_rn(a.max_norm, __fadd_rn(norm, 1e-6f));
     if (a.norm) *a.norm = norm;
     if (a.coef)
       *a.coef = isfinite(norm) ? fminf(c, 1.0f) : __uint_as_float(0x7fffffffu);

@@ -514,3 +514,13 @@ def test_adamw_8bit_states_over_a_long_run(beta2):
         for half in (low.cpu().numpy(), ~low.cpu().numpy()):
             a, b, c = np.quantile(ratio[half], [0.05, 0.5, 0.95])
             assert 0.85 < a and 0.9 < b < 1.19 and c < 1.35
+
+
+def test_the_coefficient_is_the_rounded_quotient():
+    """max_norm / (norm + 1e-6) rounded once from the fp32 norm, at ordinary and at extreme limits."""
+    rng = np.random.default_rng(21)
+    for size, limit in [(rng.uniform(0.5, 2), rng.uniform(0.1, 0.5)) for _ in range(40)] + \
+            [(1.7e19, 3e-20), (1.7e19, 1e18), (1e-18, 1e-9)]:
+        norm, coef = optim.GradNorm([torch.full((1,), float(size), device=DEV)], float(limit))()
+        want = np.float32(limit) / (np.float32(norm.item()) + np.float32(1e-6))
+        assert np.float32(coef.item()) == min(want, np.float32(1))
