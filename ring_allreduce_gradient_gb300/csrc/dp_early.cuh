@@ -1,6 +1,6 @@
 // dp_early.cuh -- launches that overlap the end of the kernel before them: the
 // CTAs come up while the last kernel of the stream drains.  Measured on calls
-// in a row, plain launches against these: the gradient norm of a 7 Mi-element
+// in a row when these came, plain launches against these: the gradient norm of a 7 Mi-element
 // list 9.3 -> 7.1 us, an 8-bit AdamW step of it 24.5 -> 21.8, decoding a
 // 128x512 matrix (from a graph) 1.7 -> 1.3.
 #pragma once

@@ -22,9 +22,11 @@
 // exchange, a lane ends with 32 contiguous bytes of each of its two output
 // rows, and the four warps of a CTA, one below the other, with a 128-byte
 // line.  Neither goes through shared memory.  Measured on 8192 x 4096 bf16
-// (GB300, launches in a CUDA graph): rows 14.1 us to nvfp4 and 11.2 to mxfp4
-// (6.1 and 7.7 TB/s, part of it from L2), transposed 16.5 and 12.4, decoding
-// 12.0; the nvfp4 forms are held by their arithmetic, two divisors a block.
+// (GB300, launches in a CUDA graph): rows 13.9 us to nvfp4 and 10.8 to mxfp4
+// (6.2 and 7.9 TB/s, part of it from L2), transposed 16.3 and 11.9, decoding
+// 11.7.  The nvfp4 forms have two divisors a block more to compute, and no unit
+// at its limit: 60 % of the SM and 70 % of DRAM for rows, 46 and 59 % transposed
+// with a third of the warps resident, whose loads and arithmetic alternate.
 
 #include "dp_early.cuh"
 #include "dp_launch.h"

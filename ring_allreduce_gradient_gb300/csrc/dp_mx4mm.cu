@@ -29,8 +29,9 @@
 // stage is.  With the scales two accumulators of 256 columns do not fit.
 //
 // Measured (GB300, launches in a CUDA graph): x[8192,4096] . w[4096,4096]^T
-// 50 us in mxfp4 (5.5 PFLOP/s) and 58 us in nvfp4 (4.8); x[8192,8192] .
-// w[8192,8192]^T 160 and 187 us.  What bounds it: the MMAs alone (loads of all
+// 50 us in mxfp4 (5.5 PFLOP/s) and 58 us in nvfp4 (4.7); x[8192,8192] .
+// w[8192,8192]^T 160 and 187 us (up to 200 on general values, which take more
+// power).  What bounds it: the MMAs alone (loads of all
 // stages but the first four left out) take 139 us of the 160; the rest is
 // operand intake, 48 KiB of values a stage, and between tiles the 1300 clocks
 // in which the accumulator is drained.  nvfp4 has twice the scales: reading

@@ -209,8 +209,8 @@ __device__ __forceinline__ float code_factor(float top) {
 }
 
 // Eight CTAs of four warps on an SM, which is 64 registers: eight 8 Mi shards
-// with 8-bit states 173 us, against 179 us at the 80 registers the kernel would
-// take; ragged bf16 parameters with 8-bit states 95 us, against 107 us.
+// with 8-bit states 174 us, against 192 us at the 80 registers the kernel would
+// take; ragged bf16 parameters with 8-bit states 97 us, against 108 us.
 constexpr int kAdamwCtas = 8;
 
 template <typename PT, typename GT, bool S8, int CAP>
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, kAdamwCtas) adamw_kernel(const __gri
     const bool vec = x.vec_ok && left >= kUnit;
     const int len = left < kUnit ? (int)left : kUnit;
     // on its way ahead of the unit's loads (read before the loop it stays in a
-    // register across it: eight 8 Mi shards 181 us, against 175; without a count 173)
+    // register across it: eight 8 Mi shards 181 us, against 174; without a count 172)
     const unsigned skipped = a.skips ? *a.skips : 0u;
     float p[8], g[8], m[8], v[8], root[8];
     uint32_t mc[2], rc[2];
