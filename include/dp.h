@@ -721,10 +721,10 @@ DP_API void dp_adamw_destroy(dp_adamw_t* o);
  * x [M, D] and K weight shards [F_shard, D]; block-scaled tensor-core
  * products accumulated in fp32, the sum times the tensors' scales (times their
  * fp32 product: two scales whose product is below 2^-126 lose bits, or are 0, and
- * above 2^128 infinite), one rounding to y_dtype.  y: row-major [M, K*F_shard].  Requires D % 32 == 0,
- * F_shard % 16 == 0, 16-byte aligned buffers; y overlaps no operand.  The
- * summation order over d follows from the sizes; under a CTA limit the result
- * is the same.  D == 0 writes zeros.
+ * above 2^128 infinite), one rounding to y_dtype.  y: row-major [M, K*F_shard].
+ * Requires D % 32 == 0, F_shard % 16 == 0, 16-byte aligned buffers; y overlaps no
+ * operand.  The summation order over d follows from the sizes; under a CTA limit
+ * the result is the same.  D == 0 writes zeros.
  *
  * dp_allgather_linear_mx4: the same with x [M, D] of x_dtype, rows ld elements
  * apart, quantised on the way (dp_mx4_quantize with tensor scale x_scale) into
