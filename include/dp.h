@@ -87,6 +87,14 @@ typedef enum { DP_FP32 = 0, DP_BF16 = 1 } dp_dtype_t;
 /* Microscaled 4-bit formats (see dp_mx4_quantize). */
 typedef enum { DP_MXFP4 = 0, DP_NVFP4 = 1 } dp_mx4_format_t;
 
+/* What dp_rms_norm quantises its output to. */
+typedef enum {
+  DP_NORM_PLAIN = 0,  /* nothing: y only */
+  DP_NORM_MXFP4 = 1,
+  DP_NORM_NVFP4 = 2,
+  DP_NORM_MXFP8 = 3
+} dp_norm_format_t;
+
 /* How an optimizer keeps its states. */
 typedef enum { DP_STATE_FP32 = 0, DP_STATE_8BIT = 1 } dp_state_t;
 
@@ -762,6 +770,74 @@ DP_API dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long lon
                                            dp_stream_t stream);
 DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_format_t format,
                                                           size_t* bytes);
+
+/*
+ * The 8-bit microscaled form of activations (mxfp8), for products whose x keeps
+ * more bits than the weights.  A matrix [rows, cols], cols a multiple of 32, has
+ *   codes    rows x cols bytes: e4m3 values
+ *   scales   one byte for each 32 consecutive columns, 2^(byte - 127), 255 is
+ *            NaN, in the tiles of the 4-bit forms (dp_mx4_scales_size(rows,
+ *            cols, DP_MXFP4) bytes)
+ * Both device buffers are 16-byte aligned.
+ *
+ * dp_mx8_quantize: x [rows, cols] of x_dtype, rows ld elements apart.  With a
+ * the largest magnitude of a block, its scale is the smallest 2^e, e >= -127,
+ * with a <= 448 * 2^e, so no value saturates; codes are x / 2^e rounded to the
+ * nearest e4m3, ties to even.  A block of zeros has scale byte 0, a block with a
+ * NaN or an infinity codes 0 and a NaN scale.
+ * dp_mx8_dequantize: out [rows, cols] of out_dtype, the values rounded once.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ */
+DP_API dp_status_t dp_mx8_quantize(const void* x, int rows, int cols, long long ld,
+                                   dp_dtype_t x_dtype, void* codes, void* scales,
+                                   dp_stream_t stream);
+DP_API dp_status_t dp_mx8_dequantize(const void* codes, const void* scales, int rows, int cols,
+                                     void* out, dp_dtype_t out_dtype, dp_stream_t stream);
+
+/*
+ * The root-mean-square norm of a layer's input, with the residual's addition and
+ * the operand of the 4-bit products in the same pass:
+ *   h = x + residual                       rounded to dtype
+ *   rstd = 1 / sqrt(mean over D of h^2 + eps)
+ *   y = h * rstd * weight
+ * x, residual: [M, D] of dtype, rows ldx / ldr elements apart; weight: D of
+ * weight_dtype.  Without a residual (NULL, and h NULL) h is x.  Any element
+ * alignment; fastest where every row starts on a 32-byte boundary.
+ * Outputs, contiguous: h and y [M, D] of dtype; rstd M floats, or NULL; with a
+ * format, codes and scales of y as dp_mx4_quantize (tensor_scale: nvfp4's, or
+ * NULL for 1) and dp_mx8_quantize define them, from the unrounded y.  y may then
+ * be NULL; without a format codes and scales are.
+ * Arithmetic in fp32: squares are summed 16 or 32 to a thread in order, the rest
+ * pairwise; magnitudes above 1.8e19 make the mean infinite, and then y is 0.  A
+ * row with a NaN is NaN throughout.
+ * Requires D <= 32768, and D % 32 == 0 with a format; eps >= 0 and finite.
+ *
+ * dp_rms_norm_backward: from dy (the gradient of y) and dh (that which reaches h
+ * past the norm, or NULL: none), both [M, D] of dtype,
+ *   g = dy * weight,  xh = h * rstd
+ *   dx = rstd * (g - xh * mean over D of (g * xh)) + dh      of dtype, contiguous
+ *   dweight = sum over rows of dy * xh                       D floats
+ * dx is the gradient of x and of the residual alike.  A quantised y's gradient
+ * passes straight through.  dweight is summed in fp32 over at most 456 sets of
+ * rows, then over those; the order follows from M and D, so a repeated call gives
+ * the same bits under any CTA limit.  M == 0 writes zeros to dweight.
+ * workspace: device memory of dp_rms_norm_backward_workspace_size(M, D) bytes,
+ * 32-byte aligned, any contents; free again in stream order.
+ * Nothing that is written may overlap anything else.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ */
+DP_API dp_status_t dp_rms_norm(const void* x, long long ldx, const void* residual, long long ldr,
+                               int M, int D, dp_dtype_t dtype, const void* weight,
+                               dp_dtype_t weight_dtype, float eps, void* h, void* y, float* rstd,
+                               dp_norm_format_t format, const float* tensor_scale, void* codes,
+                               void* scales, dp_stream_t stream);
+DP_API dp_status_t dp_rms_norm_backward(const void* dy, long long ldy, const void* h,
+                                        long long ldh, const void* dh, long long ldd, int M, int D,
+                                        dp_dtype_t dtype, const void* weight,
+                                        dp_dtype_t weight_dtype, const float* rstd, void* dx,
+                                        float* dweight, void* workspace, size_t workspace_bytes,
+                                        dp_stream_t stream);
+DP_API dp_status_t dp_rms_norm_backward_workspace_size(int M, int D, size_t* bytes);
 
 /*
  * The parameter all-gather on the GPU's copy engines instead of its SMs

@@ -19,6 +19,10 @@ DP_MAX_K = 16
 DP_MAX_MICROBATCHES = 16
 DP_MXFP4 = 0
 DP_NVFP4 = 1
+DP_NORM_PLAIN = 0
+DP_NORM_MXFP4 = 1
+DP_NORM_NVFP4 = 2
+DP_NORM_MXFP8 = 3
 DP_STATE_FP32 = 0
 DP_STATE_8BIT = 1
 DP_STATE_BLOCK = 256  # elements that share one scale of an 8-bit state
@@ -131,6 +135,14 @@ def load() -> ctypes.CDLL:
                                         ctypes.POINTER(Mx4), i32, i32, i32, vp, i32, vp, sz, vp],
             "dp_allgather_linear_mx4_workspace_size": [i32, i32, i32,
                                                        ctypes.POINTER(ctypes.c_size_t)],
+            "dp_mx8_quantize": [vp, i32, i32, ctypes.c_longlong, i32, vp, vp, vp],
+            "dp_mx8_dequantize": [vp, vp, i32, i32, vp, i32, vp],
+            "dp_rms_norm": [vp, ctypes.c_longlong, vp, ctypes.c_longlong, i32, i32, i32, vp, i32,
+                            f32, vp, vp, vp, i32, vp, vp, vp, vp],
+            "dp_rms_norm_backward": [vp, ctypes.c_longlong, vp, ctypes.c_longlong, vp,
+                                     ctypes.c_longlong, i32, i32, i32, vp, i32, vp, vp, vp, vp, sz,
+                                     vp],
+            "dp_rms_norm_backward_workspace_size": [i32, i32, ctypes.POINTER(ctypes.c_size_t)],
             "dp_adamw_create": [ctypes.POINTER(AdamwTensor), i32, i32, i32, i32,
                                 ctypes.POINTER(ctypes.c_void_p)],
             "dp_adamw_count_skips": [vp, vp],
@@ -628,6 +640,45 @@ def dp_allgather_linear_mx4_workspace_size(M, D, fmt) -> int:
     b = ctypes.c_size_t(0)
     _ret(load().dp_allgather_linear_mx4_workspace_size(M, D, fmt, ctypes.byref(b)),
          "dp_allgather_linear_mx4_workspace_size", True)
+    return int(b.value)
+
+
+def dp_mx8_quantize(x, rows, cols, ld, x_dtype, codes, scales, stream=None, check=True) -> int:
+    st = load().dp_mx8_quantize(_ptr(x), rows, cols, ld, dtype_code(x_dtype), _ptr(codes),
+                                _ptr(scales), _stream(stream))
+    return _ret(st, "dp_mx8_quantize", check)
+
+
+def dp_mx8_dequantize(codes, scales, rows, cols, out, out_dtype, stream=None, check=True) -> int:
+    st = load().dp_mx8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out),
+                                  dtype_code(out_dtype), _stream(stream))
+    return _ret(st, "dp_mx8_dequantize", check)
+
+
+def dp_rms_norm(x, ldx, residual, ldr, M, D, dtype, weight, weight_dtype, eps, h, y, rstd,
+                format=DP_NORM_PLAIN, tensor_scale=None, codes=None, scales=None, stream=None,
+                check=True) -> int:
+    st = load().dp_rms_norm(_ptr(x), ldx, _ptr(residual), ldr, M, D, dtype_code(dtype),
+                            _ptr(weight), dtype_code(weight_dtype), eps, _ptr(h), _ptr(y),
+                            _ptr(rstd), format, _ptr(tensor_scale), _ptr(codes), _ptr(scales),
+                            _stream(stream))
+    return _ret(st, "dp_rms_norm", check)
+
+
+def dp_rms_norm_backward(dy, ldy, h, ldh, dh, ldd, M, D, dtype, weight, weight_dtype, rstd, dx,
+                         dweight, workspace, workspace_bytes=None, stream=None,
+                         check=True) -> int:
+    wp, wb = _ws(workspace, workspace_bytes)
+    st = load().dp_rms_norm_backward(_ptr(dy), ldy, _ptr(h), ldh, _ptr(dh), ldd, M, D,
+                                     dtype_code(dtype), _ptr(weight), dtype_code(weight_dtype),
+                                     _ptr(rstd), _ptr(dx), _ptr(dweight), wp, wb, _stream(stream))
+    return _ret(st, "dp_rms_norm_backward", check)
+
+
+def dp_rms_norm_backward_workspace_size(M, D) -> int:
+    b = ctypes.c_size_t(0)
+    _ret(load().dp_rms_norm_backward_workspace_size(M, D, ctypes.byref(b)),
+         "dp_rms_norm_backward_workspace_size", True)
     return int(b.value)
 
 

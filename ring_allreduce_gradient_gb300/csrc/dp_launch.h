@@ -24,6 +24,14 @@ inline Span span_of(const void* p, size_t n, bool written = false) {
 inline bool clash(const Span& a, const Span& b) {
   return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo;
 }
+// True if a written range overlaps any other of a few (no allocation).
+template <size_t N>
+bool any_clash(const Span (&s)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = i + 1; j < N; ++j)
+      if ((s[i].written || s[j].written) && clash(s[i], s[j])) return true;
+  return false;
+}
 // True if a written range overlaps any other range of the list.
 inline bool spans_clash(std::vector<Span>& s) {
   std::sort(s.begin(), s.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });

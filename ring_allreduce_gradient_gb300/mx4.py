@@ -173,7 +173,7 @@ def _rows(x):
         raise ValueError(f"need a matrix, got {tuple(x.shape)}: flatten the other dimensions first")
     rows, cols = x.shape
     ld, unit = x.stride()
-    if unit != 1 and cols > 1:
+    if unit != 1 and cols > 1 and rows:
         raise ValueError("need a matrix with unit stride along its rows")
     if rows <= 1:
         return x, cols
