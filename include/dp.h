@@ -772,6 +772,27 @@ DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_f
                                                           size_t* bytes);
 
 /*
+ * A few tokens times 4-bit weight shards, the tokens as they are:
+ *   y[m, f] = tw * sum_d x[m, d] * w[f, d]
+ * x [M, D] bf16, rows ld elements apart, any alignment (fastest where rows start
+ * on 16-byte boundaries); w_shards, K, F_shard, format and y as for
+ * dp_allgather_matmul_mx4, y of any alignment.  For the single tokens of a model
+ * that is served: it reads the weights once for each 32 tokens, and is bound by
+ * that up to about 32; for many tokens the products of quantised x are faster.
+ * Weights are decoded exactly; x is exact down to 2^-27 of its row's largest
+ * magnitude, and below it within 2^-35 of that magnitude (mxfp4: weights likewise,
+ * within a row of w); products are summed in fp32, in an order that follows from
+ * the sizes; tw, the shard's tensor scale, multiplies the sum.  x holding a NaN or
+ * an infinity gives that token NaN or infinities.  D == 0 writes zeros.
+ * Requires D % 32 == 0, F_shard % 16 == 0, M <= 524280.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ */
+DP_API dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
+                                          const dp_mx4_t* w_shards, int K, int F_shard,
+                                          dp_mx4_format_t format, void* y, dp_dtype_t y_dtype,
+                                          dp_stream_t stream);
+
+/*
  * The 8-bit microscaled form of activations (mxfp8), for products whose x keeps
  * more bits than the weights.  A matrix [rows, cols], cols a multiple of 32, has
  *   codes    rows x cols bytes: e4m3 values

@@ -19,7 +19,7 @@ LIB_NAME = "libdp_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["dp_api.cu", "dp_stream.cu", "dp_odc.cu", "dp_agmm.cu", "dp_bucket.cu", "dp_reducer.cu",
            "dp_tma.cu", "dp_noalloc.cu", "dp_pipe.cu", "dp_optim.cu",
-           "dp_mx4.cu", "dp_mx4mm.cu", "dp_mx8.cu", "dp_norm.cu"]
+           "dp_mx4.cu", "dp_mx4mm.cu", "dp_mx8.cu", "dp_norm.cu", "dp_w4.cu"]
 HEADERS = [os.path.join(CSRC, "dp_common.cuh"), os.path.join(CSRC, "dp_launch.h"),
            os.path.join(CSRC, "dp_stream_common.cuh"), os.path.join(CSRC, "dp_tc.cuh"),
            os.path.join(CSRC, "dp_early.cuh"), os.path.join(CSRC, "dp_mx4.cuh"),

@@ -3,6 +3,7 @@ and gradients, and the all-gather product of two such operands.
 
     wq = [quantize(w, "nvfp4", tensor_scale=tensor_scale(w)) for w in shards]
     y = linear(x, wq, x_scale=x_scale)            # y = x . w^T, both in 4 bits
+    y = linear_w4(x, wq)                          # a few tokens, x as it is
     # backward, in 4 bits too: blocks along the contracted dimension
     wt = quantize(shards, "nvfp4", tensor_scale=s, transpose=True)   # [D, F], gathered
     dx = linear(dy, [wt])                                            # dy . w
@@ -262,4 +263,31 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
         y.data_ptr(), _DT[y_dtype], ws.data_ptr(), nbytes, B._stream_on(dev, "linear"))
     if st:
         raise B.DpError(st, "dp_allgather_linear_mx4")
+    return y
+
+
+def linear_w4(x: torch.Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y = x . w^T with x [M, D] (bf16) as it is and only the weights in 4 bits: for
+    one token or a few, where the weights' bytes are all that counts.  Many tokens
+    are faster with both operands quantised (``linear``).  Records no gradient."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return linear_w4(x, w_shards, y_dtype)
+    x, ld = _rows(x)
+    M, D = x.shape
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x: bf16, not {x.dtype}")
+    if y_dtype not in _DT:
+        raise TypeError(f"unsupported dtype {y_dtype}")
+    if not w_shards:
+        raise ValueError("need at least one shard")
+    dev, K = x.device, len(w_shards)
+    F, _, format, _ = w_shards[0]._kind
+    arr = _shards(w_shards, D, format, dev)
+    y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
+    st = (B._lib or B.load()).dp_allgather_linear_w4(
+        x.data_ptr(), M, D, ld, arr, K, F, FORMATS[format], y.data_ptr(), _DT[y_dtype],
+        B._stream_on(dev, "linear_w4"))
+    if st:
+        raise B.DpError(st, "dp_allgather_linear_w4")
     return y

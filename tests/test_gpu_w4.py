@@ -1,0 +1,196 @@
+"""A few tokens times 4-bit shards, against the decoded weights in 64 bits.
+
+Every product of an f16 weight and an f16 x is exact, so y differs from the sum by
+the fp32 additions: at most D + 8 of them (the tensor core's within an instruction,
+an instruction a step, the shares'), 2^-24 of the sum of magnitudes each and twice
+that where the tensor core truncates; plus what x and mxfp4's scales lose below
+2^-27 of the largest, 2^-35 of it, and one rounding of y.  With small integers all
+of it is exact.
+"""
+import numpy as np
+import pytest
+import torch
+
+from ring_allreduce_gradient_gb300 import mx4
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda", 0)
+U = 2.0 ** -24
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def shards_of(w, K, fmt, t=None):
+    return [mx4.quantize(s.contiguous(), fmt, t) for s in w.chunk(K)]
+
+
+def check(x, shards, y_dtype=torch.float32):
+    """The call against 64 bits on what is stored; returns y."""
+    y = mx4.linear_w4(x, shards, y_dtype)
+    w = np.concatenate([f64(mx4.dequantize(q, torch.float32)) for q in shards])
+    x64 = f64(x)
+    want, size = x64 @ w.T, np.abs(x64) @ np.abs(w).T
+    D = x.shape[1]
+    lost = D * 2.0 ** -35 * 2 * np.abs(x64).max(1, initial=0)[:, None] * \
+        np.abs(w).max(1, initial=0)[None, :]
+    tol = 2 * (D + 8) * U * size + lost
+    if y_dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want)
+    assert y.dtype == y_dtype and y.shape == want.shape
+    assert np.all(np.abs(f64(y) - want) <= tol + 2.0 ** -140)
+    return y
+
+
+def normal(shape, seed, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(shape, device=DEV, generator=g) * scale
+
+
+SHAPES = [  # M, D, K, F_shard
+    (1, 32, 1, 16), (1, 64, 2, 48), (1, 96, 1, 128), (2, 128, 1, 144), (3, 160, 4, 16),
+    (8, 512, 8, 64), (9, 544, 2, 208), (16, 1056, 1, 336), (17, 1024, 3, 80), (32, 4096, 1, 64),
+    (33, 288, 2, 32), (70, 96, 1, 256), (1, 4096, 8, 512), (5, 1120, 2, 4112), (12, 640, 1, 20000),
+    (24, 224, 4, 5008), (7, 16384, 1, 32)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,D,K,Fs", SHAPES)
+def test_values(M, D, K, Fs, fmt):
+    w = normal((K * Fs, D), M + D, 0.02)
+    x = normal((M, D), M * D) * torch.exp(2 * normal((M, 1), 3))
+    t = mx4.tensor_scale(w) if fmt == "nvfp4" else None
+    s = shards_of(w, K, fmt, t)
+    a = check(x.bfloat16(), s)
+    b = check(x.bfloat16(), s, torch.bfloat16)
+    assert torch.equal(a.bfloat16(), b)
+    assert torch.equal(a, mx4.linear_w4(x.bfloat16(), s, torch.float32))   # the same bits again
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,D,K,Fs", [(1, 64, 1, 16), (5, 416, 2, 144), (20, 256, 1, 20000),
+                                      (11, 1024, 2, 96)])
+def test_integers_are_exact(M, D, K, Fs, fmt):
+    """Weights that their form holds exactly, x of small integers: every sum is exact."""
+    rng = np.random.default_rng(D)
+    vals = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])
+    w = rng.choice(vals, (K * Fs, D)) * rng.choice([-1, 1], (K * Fs, D))
+    w[:, ::16] = 6                      # every block's scale is 1 in both forms
+    x = rng.integers(-8, 9, (M, D))
+    s = shards_of(torch.from_numpy(w).float().to(DEV), K, fmt)
+    y = mx4.linear_w4(torch.from_numpy(x).to(DEV).bfloat16(), s, torch.float32)
+    assert np.array_equal(f64(y), x @ w.T)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M", [1, 10, 30])
+def test_growing_and_shrinking_magnitudes(M, fmt):
+    """x and the weights' scales rise and fall along d, past what f16 spans."""
+    D, F = 2048, 160
+    ramp = torch.linspace(-40, 40, D, device=DEV)
+    w = normal((F, D), 1)
+    for dx, dw in ((ramp, 0 * ramp), (-ramp, 0 * ramp), (0 * ramp, ramp), (0 * ramp, -ramp),
+                   (ramp, -ramp), (-ramp, ramp), (ramp.abs(), ramp)):
+        if fmt == "nvfp4":
+            dw = dw.clamp(-5, 5)        # its block scales span 2^17
+        s = shards_of(w * torch.exp2(dw), 1, fmt, torch.tensor([1.0], device=DEV) if fmt == "nvfp4"
+                      else None)
+        check((normal((M, D), 2) * torch.exp2(dx)).bfloat16(), s)
+
+
+def test_extreme_magnitudes():
+    """Tokens and weights at the ends of bf16 and of the scales."""
+    D, F = 256, 48
+    w, x = normal((F, D), 1), normal((4, D), 2)
+    for sw in (2.0 ** -100, 1.0, 2.0 ** 100):
+        s = shards_of(w * sw, 1, "mxfp4")
+        for sx in (2.0 ** -120, 2.0 ** -20, 1.0, 2.0 ** 20, 2.0 ** 110):
+            if 2.0 ** -90 < sw * sx < 2.0 ** 110:      # where fp32 holds the sums
+                check((x * sx).bfloat16(), s)
+    rows = x.bfloat16()
+    rows[0] = 0
+    rows[1, 1:] = 0
+    y = check(rows, shards_of(w, 1, "mxfp4"))
+    assert (y[0] == 0).all()
+    z = shards_of(torch.zeros(F, D, device=DEV), 1, "nvfp4")
+    assert (check(rows, z) == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_not_finite(fmt):
+    D, F = 512, 96
+    w = normal((F, D), 1)
+    x = normal((5, D), 2).bfloat16()
+    clean = mx4.linear_w4(x, shards_of(w, 1, fmt), torch.float32)
+    x[1, 300] = float("nan")
+    x[3, 7] = float("inf")
+    y = mx4.linear_w4(x, shards_of(w, 1, fmt), torch.float32)
+    assert y[1].isnan().all() and not y[3].isfinite().any()
+    for i in (0, 2, 4):
+        assert torch.equal(y[i], clean[i])
+    x = normal((5, D), 2).bfloat16()
+    w[17, 200] = float("nan")           # a NaN block: that feature, and no other
+    y = mx4.linear_w4(x, shards_of(w, 1, fmt), torch.float32)
+    assert y[:, 17].isnan().all()
+    keep = [f for f in range(F) if f != 17]
+    assert torch.equal(y[:, keep], clean[:, keep])
+
+
+def test_strides_and_alignment():
+    D, F = 320, 112
+    s = shards_of(normal((F, D), 1), 1, "nvfp4")
+    x = normal((6, D), 2).bfloat16()
+    want = mx4.linear_w4(x, s)
+    for ld, off in ((D + 8, 0), (D + 1, 0), (D, 1), (2 * D, 3), (D + 4, 4)):
+        buf = torch.full((off + 6 * ld + 8,), float("nan"), dtype=torch.bfloat16, device=DEV)
+        v = buf[off:off + 6 * ld].view(6, ld)[:, :D]
+        v.copy_(x)
+        assert torch.equal(mx4.linear_w4(v, s), want)
+    assert torch.equal(mx4.linear_w4(x[:1].expand(9, D), s), want[:1].expand(9, F))
+
+
+def test_empty():
+    s = shards_of(normal((32, 64), 1), 1, "mxfp4")
+    assert mx4.linear_w4(torch.zeros(0, 64, dtype=torch.bfloat16, device=DEV), s).shape == (0, 32)
+    z = mx4.quantize(torch.zeros(16, 0, device=DEV), "mxfp4")
+    y = mx4.linear_w4(torch.zeros(3, 0, dtype=torch.bfloat16, device=DEV), [z])
+    assert y.shape == (3, 16) and (y == 0).all()
+
+
+def test_nothing_else_is_written_and_streams_and_graphs():
+    from ring_allreduce_gradient_gb300 import binding as B
+    D, F, M = 544, 224, 9
+    s = shards_of(normal((F, D), 1), 2, "nvfp4")
+    x = normal((M, D), 2).bfloat16()
+    want = mx4.linear_w4(x, s)
+    torch.cuda.synchronize()
+    buf = torch.full((M * F * 2 + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+    B.dp_allgather_linear_w4(x, M, D, D, [q._c for q in s], 2, F // 2, B.DP_NVFP4,
+                             buf.data_ptr() + 256, B.DP_BF16)
+    assert (buf[:256] == 0xA5).all() and (buf[-256:] == 0xA5).all()
+    assert torch.equal(buf[256:-256].view(torch.bfloat16).view(M, F), want)
+    side = torch.cuda.Stream()
+    got = mx4.linear_w4(x, s, stream=side)
+    other = mx4.linear_w4(x, s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(other, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = mx4.linear_w4(x, s)
+    x.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, mx4.linear_w4(x, s)) and torch.equal(y.float(), want.float() * 2)
+
+
+def test_same_bits_as_one_token_at_a_time():
+    """Tokens in one call are the tokens alone: each is scaled by itself.  (The instruction's
+    columns do not meet; the shares of d are those of the same rule.)"""
+    D, F = 1024, 96
+    s = shards_of(normal((F, D), 1), 1, "mxfp4")
+    x = (normal((30, D), 2) * torch.exp2(10 * normal((30, 1), 3))).bfloat16()
+    all_at_once = mx4.linear_w4(x, s, torch.float32)
+    for i in (0, 7, 8, 29):
+        assert torch.equal(mx4.linear_w4(x[i:i + 1], s, torch.float32), all_at_once[i:i + 1])

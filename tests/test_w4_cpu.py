@@ -1,0 +1,61 @@
+"""Refusals of the few-token product, made on the host before any device call."""
+import pytest
+import torch
+
+from ring_allreduce_gradient_gb300 import binding as B
+from ring_allreduce_gradient_gb300 import build as cuda_build
+from ring_allreduce_gradient_gb300 import mx4
+
+BASE = 0x7F0000000000
+OK, INVALID, UNSUPPORTED, ALIAS = (B.DP_OK, B.DP_ERR_INVALID_ARG, B.DP_ERR_UNSUPPORTED,
+                                   B.DP_ERR_ALIAS)
+MX, NV = B.DP_MXFP4, B.DP_NVFP4
+
+
+def fake(i, off=0):
+    return BASE + (i << 26) + off
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    cuda_build.build()
+    return B.load()
+
+
+def test_checks():
+    ws = [(fake(2 * k + 2), fake(2 * k + 3), None) for k in range(2)]
+
+    def m(x=fake(0), M=4, D=64, ld=64, w=ws, K=2, Fs=32, fmt=MX, y=fake(20), dt=B.DP_BF16):
+        return B.dp_allgather_linear_w4(x, M, D, ld, w, K, Fs, fmt, y, dt, stream=0, check=False)
+
+    assert m(K=0) == INVALID and m(K=17) == INVALID
+    assert m(M=-1) == INVALID and m(D=-32) == INVALID and m(Fs=-16) == INVALID
+    assert m(ld=63) == INVALID and m(x=None) == INVALID and m(y=None) == INVALID
+    assert m(w=[ws[0], (None, fake(5), None)]) == INVALID
+    assert m(w=[ws[0], (fake(4), None, None)]) == INVALID
+    assert m(w=[ws[0], (fake(4), fake(5), fake(9))]) == INVALID    # a tensor scale with mxfp4
+    assert m(fmt=2) == UNSUPPORTED and m(dt=5) == UNSUPPORTED
+    assert m(D=48, ld=48) == UNSUPPORTED and m(Fs=24) == UNSUPPORTED
+    assert m(M=65535 * 8 + 1) == UNSUPPORTED and m(K=16, w=ws * 8, Fs=0x8000000) == UNSUPPORTED
+    assert m(x=fake(0, 1)) == UNSUPPORTED and m(y=fake(20, 1)) == UNSUPPORTED
+    assert m(y=fake(20, 2), dt=B.DP_FP32) == UNSUPPORTED
+    assert m(w=[(fake(2, 8), fake(3), None), ws[1]]) == UNSUPPORTED
+    assert m(w=[(fake(2), fake(3, 4), None), ws[1]]) == UNSUPPORTED
+    assert m(fmt=NV, w=[(fake(2), fake(3), fake(9, 2)), ws[1]]) == UNSUPPORTED
+    assert m(y=fake(0)) == ALIAS and m(y=fake(2, 16)) == ALIAS and m(y=fake(5, 16)) == ALIAS
+    assert m(fmt=NV, w=[(fake(2), fake(3), fake(20, 4)), ws[1]]) == ALIAS
+    assert m(M=0, y=None) == OK and m(Fs=0, y=None) == OK
+
+
+def test_the_helper_checks():
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    q = mx4.Mx4Tensor(u8(16 * 32), u8(512), 16, 64, "mxfp4")
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for args, err, word in [((x.float(), [q]), TypeError, "bf16"),
+                            ((x, [q], torch.float16), TypeError, "dtype"),
+                            ((x, []), ValueError, "at least one shard"),
+                            ((x[:, :32], [q]), ValueError, "columns"),
+                            ((x[0], [q]), ValueError, "need a matrix"),
+                            ((x, [q]), B.DpError, "not the current CUDA device")]:
+        with pytest.raises(err, match=word):
+            mx4.linear_w4(*args)
