@@ -807,13 +807,32 @@ DP_API dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long
  * nearest e4m3, ties to even.  A block of zeros has scale byte 0, a block with a
  * NaN or an infinity codes 0 and a NaN scale.
  * dp_mx8_dequantize: out [rows, cols] of out_dtype, the values rounded once.
- * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ *
+ * dp_allgather_matmul_mx8: dp_allgather_matmul_mx4 with x [M, D] in this form
+ * (tensor_scale NULL) and the weight shards in DP_MXFP4: the tensor cores multiply
+ * e4m3 by e2m1 values with both blocks' scales exactly and accumulate in fp32.
+ * Requirements, y and errors are that call's.
+ * dp_allgather_linear_mx8: the same with x [M, D] of x_dtype, rows ld elements
+ * apart, quantised on the way (dp_mx8_quantize) into workspace: device memory of
+ * dp_allgather_linear_mx8_workspace_size(M, D) bytes, as for
+ * dp_allgather_linear_mx4.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA;
+ * DP_ERR_TIMEOUT later from dp_get_device_error if a pipeline wait expired.
  */
 DP_API dp_status_t dp_mx8_quantize(const void* x, int rows, int cols, long long ld,
                                    dp_dtype_t x_dtype, void* codes, void* scales,
                                    dp_stream_t stream);
 DP_API dp_status_t dp_mx8_dequantize(const void* codes, const void* scales, int rows, int cols,
                                      void* out, dp_dtype_t out_dtype, dp_stream_t stream);
+DP_API dp_status_t dp_allgather_matmul_mx8(const dp_mx4_t* x, int M, int D,
+                                           const dp_mx4_t* w_shards, int K, int F_shard, void* y,
+                                           dp_dtype_t y_dtype, dp_stream_t stream);
+DP_API dp_status_t dp_allgather_linear_mx8(const void* x, int M, int D, long long ld,
+                                           dp_dtype_t x_dtype, const dp_mx4_t* w_shards, int K,
+                                           int F_shard, void* y, dp_dtype_t y_dtype,
+                                           void* workspace, size_t workspace_bytes,
+                                           dp_stream_t stream);
+DP_API dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* bytes);
 
 /*
  * The root-mean-square norm of a layer's input, with the residual's addition and
@@ -906,12 +925,12 @@ DP_API int dp_get_collective_variant(void);
  * Process-wide upper bounds on the CTAs one launch may use: gemm_ctas for
  * the tensor-core kernels (dp_allgather_matmul, dp_matmul_*,
  * dp_wgrad_reduce_scatter*; the weight gradient's workspace size follows the
- * limit; dp_allgather_matmul_mx4 and dp_allgather_linear_mx4, which where they
- * split a tile over a cluster of 2, 4 or 8 CTAs use one cluster at least),
+ * limit; dp_allgather_matmul_mx4, dp_allgather_linear_mx4 and their mx8 forms,
+ * which where they split a tile over a cluster of 2, 4 or 8 CTAs use one cluster at least),
  * stream_ctas for the streaming collectives (reduce-scatter, all-gather,
  * all-reduce, accumulate, bucket and variable-length kernels), the gradient
- * norm, AdamW and the 4-bit quantisation; 0 means no limit (the
- * default: one resident grid over every SM).  Lets a caller leave SMs free
+ * norm, AdamW, the 4- and 8-bit quantisation and the RMS norm;
+ * dp_allgather_linear_w4 has no limit; 0 means no limit (the default: one resident grid over every SM).  Lets a caller leave SMs free
  * for a kernel on another stream -- the resource-partitioning experiment of
  * "Optimizing ML Concurrent Computation and Communication with GPU DMA
  * Engines" (Q2, "Resource Partitioning").  Results do not depend on the

@@ -139,6 +139,11 @@ def load() -> ctypes.CDLL:
                                        i32, i32, vp, i32, vp],
             "dp_mx8_quantize": [vp, i32, i32, ctypes.c_longlong, i32, vp, vp, vp],
             "dp_mx8_dequantize": [vp, vp, i32, i32, vp, i32, vp],
+            "dp_allgather_matmul_mx8": [ctypes.POINTER(Mx4), i32, i32, ctypes.POINTER(Mx4), i32,
+                                        i32, vp, i32, vp],
+            "dp_allgather_linear_mx8": [vp, i32, i32, ctypes.c_longlong, i32, ctypes.POINTER(Mx4),
+                                        i32, i32, vp, i32, vp, sz, vp],
+            "dp_allgather_linear_mx8_workspace_size": [i32, i32, ctypes.POINTER(ctypes.c_size_t)],
             "dp_rms_norm": [vp, ctypes.c_longlong, vp, ctypes.c_longlong, i32, i32, i32, vp, i32,
                             f32, vp, vp, vp, i32, vp, vp, vp, vp],
             "dp_rms_norm_backward": [vp, ctypes.c_longlong, vp, ctypes.c_longlong, vp,
@@ -662,6 +667,30 @@ def dp_mx8_dequantize(codes, scales, rows, cols, out, out_dtype, stream=None, ch
     st = load().dp_mx8_dequantize(_ptr(codes), _ptr(scales), rows, cols, _ptr(out),
                                   dtype_code(out_dtype), _stream(stream))
     return _ret(st, "dp_mx8_dequantize", check)
+
+
+def dp_allgather_matmul_mx8(x, M, D, w_shards, K, F_shard, y, y_dtype, stream=None,
+                            check=True) -> int:
+    """``x``: a (codes, scales, None) triple of an 8-bit matrix; ``w_shards``: K mxfp4 ones."""
+    st = load().dp_allgather_matmul_mx8(_mx4_array([x]), M, D, _mx4_array(w_shards), K, F_shard,
+                                        _ptr(y), dtype_code(y_dtype), _stream(stream))
+    return _ret(st, "dp_allgather_matmul_mx8", check)
+
+
+def dp_allgather_linear_mx8(x, M, D, ld, x_dtype, w_shards, K, F_shard, y, y_dtype, workspace,
+                            workspace_bytes=None, stream=None, check=True) -> int:
+    wp, wb = _ws(workspace, workspace_bytes)
+    st = load().dp_allgather_linear_mx8(_ptr(x), M, D, ld, dtype_code(x_dtype),
+                                        _mx4_array(w_shards), K, F_shard, _ptr(y),
+                                        dtype_code(y_dtype), wp, wb, _stream(stream))
+    return _ret(st, "dp_allgather_linear_mx8", check)
+
+
+def dp_allgather_linear_mx8_workspace_size(M, D) -> int:
+    b = ctypes.c_size_t(0)
+    _ret(load().dp_allgather_linear_mx8_workspace_size(M, D, ctypes.byref(b)),
+         "dp_allgather_linear_mx8_workspace_size", True)
+    return int(b.value)
 
 
 def dp_rms_norm(x, ldx, residual, ldr, M, D, dtype, weight, weight_dtype, eps, h, y, rstd,

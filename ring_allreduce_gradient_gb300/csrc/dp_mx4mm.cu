@@ -65,10 +65,19 @@ namespace {
 using namespace dpk;
 
 constexpr int BM = 128;          // weight rows of a tile
-constexpr int BK = 256;          // values of d per stage: one 128-byte swizzle row
-constexpr int kStep = 64;        // values of d per MMA
-constexpr uint32_t kStageW = BM * BK / 2;
+constexpr int kRowBytes = 128;   // of an operand's row in a stage: one swizzle row
+constexpr uint32_t kStageW = BM * kRowBytes;
 constexpr uint32_t kStageSW = 4 * kScaleTile;  // 128 rows x 16 blocks (nvfp4)
+
+// The operands: both mxfp4, both nvfp4, or mxfp4 weights with x in 8 bits (mxfp8).
+enum { kMx4 = 0, kNv4 = 1, kMx8 = 2 };
+template <int KIND>
+struct Kind {
+  static constexpr bool kPow2 = KIND != kNv4;                       // scales are powers of two
+  static constexpr int kBlock = KIND == kNv4 ? kNvBlock : kMxBlock;
+  static constexpr int kBK = KIND == kMx8 ? 128 : 256;              // values of d per stage
+  static constexpr int kStep = kBK / 4;                             // ... per MMA
+};
 constexpr int kOutTokens = 16;   // tokens of one staged store of an epilogue half
 constexpr uint32_t kStageY = kOutTokens * BM * 2;  // per half
 constexpr size_t kBarBytes = 512;
@@ -81,7 +90,7 @@ constexpr size_t kBarBytes = 512;
 template <int BNMAX>
 struct Geo {
   static constexpr int kStages = BNMAX == 256 ? 4 : BNMAX == 128 ? 6 : 8;
-  static constexpr uint32_t kStageX = BNMAX * BK / 2;
+  static constexpr uint32_t kStageX = BNMAX * kRowBytes;
   static constexpr int kXTiles = BNMAX > 128 ? 2 : 1;  // 128-row scale tiles of X
   static constexpr uint32_t kStageSX = kXTiles * 4 * kScaleTile;
   static constexpr int kXCols = 4 * kXTiles;           // TMEM columns of a step's X scales
@@ -93,7 +102,7 @@ struct Geo {
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   static_assert(kScaleCol0 + kStages * kScaleCols <= 512, "TMEM columns");
   static_assert((uint32_t)BNMAX * BM * 4 <= kStages * (kStageW + kStageX), "partial sums");
-  static_assert((4 * kStages + 2) * 8 + 8 <= kBarBytes, "barriers");
+  static_assert((5 * kStages + 2) * 8 + 8 <= kBarBytes, "barriers");
 };
 
 constexpr int kTmemCols = 512;
@@ -105,6 +114,7 @@ constexpr int kMaxSplit = 8;
 struct Mx4mmParams {
   CUtensorMap tmX, tmY;
   CUtensorMap tmW[kMaxK];
+  const uint8_t* w[kMaxK];  // codes (8-bit x; the 4-bit forms load them through tmW)
   const uint8_t* sx;
   const uint8_t* sw[kMaxK];
   const float* tx;
@@ -142,6 +152,10 @@ __device__ __forceinline__ void async_copy16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
                : "memory");
 }
+// Sixteen 4-bit values to the first half of their 16 bytes.
+__device__ __forceinline__ void async_copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void async_copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
@@ -167,13 +181,15 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Instruction descriptor of the block-scaled kinds: A and B e2m1, both
-// K-major; scales ue8m0 (mxfp4) or e4m3.
-__device__ __forceinline__ uint32_t idesc_fp4(bool mx, int n) {
-  return (1u << 7)                      // A format: e2m1
-         | (1u << 10)                   // B format: e2m1
-         | ((uint32_t)(n >> 3) << 17)   // N >> 3
-         | (mx ? 1u << 23 : 0u)         // scale format: ue8m0 / ue4m3
+// Instruction descriptor of the block-scaled kinds: both operands K-major, A
+// e2m1, B e2m1 or e4m3 (the 8-bit kind numbers its formats differently); scales
+// ue8m0 or e4m3.
+template <int KIND>
+__device__ __forceinline__ uint32_t idesc_fp4(int n) {
+  return ((KIND == kMx8 ? 5u : 1u) << 7)      // A format: e2m1
+         | ((KIND == kMx8 ? 0u : 1u) << 10)   // B format: e4m3 / e2m1
+         | ((uint32_t)(n >> 3) << 17)         // N >> 3
+         | (Kind<KIND>::kPow2 ? 1u << 23 : 0u)  // scale format: ue8m0 / ue4m3
          | ((uint32_t)(BM >> 7) << 27); // M >> 7
 }
 
@@ -182,11 +198,20 @@ __device__ __forceinline__ uint32_t idesc_fp4(bool mx, int n) {
 // uniform registers.  Inside an if (lane == 0) each MMA took 73 clocks to
 // issue, and a stage 788 clocks for 548 of MMAs (x[8192,8192] .
 // w[8192,8192]^T, mxfp4: 194 us, against 166).
-template <bool MX>
+template <int KIND>
 __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                         uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
                                         uint32_t accumulate) {
-  if constexpr (MX)
+  if constexpr (KIND == kMx8)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else if constexpr (KIND == kMx4)
     asm volatile(
         "{\n\t.reg .pred p, e;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
@@ -254,15 +279,16 @@ __device__ __forceinline__ bool half_any(int half, bool v) {
   return r != 0;
 }
 
-template <bool MX, int BNMAX>
+template <int KIND, int BNMAX>
 __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_constant__ Mx4mmParams p) {
   using G = Geo<BNMAX>;
   constexpr int kStages = G::kStages, kXCols = G::kXCols;
   constexpr uint32_t kStageX = G::kStageX, kStageSX = G::kStageSX;
   constexpr int kScaleCol0 = G::kScaleCol0, kScaleCols = G::kScaleCols;
   constexpr int kHalfChunks = BNMAX / 32;  // chunks of 16 tokens of an epilogue half, at most
-  constexpr int BLOCK = MX ? kMxBlock : kNvBlock;
-  constexpr int kTilesKb = BK / (4 * BLOCK);          // scale tiles of a stage along d
+  constexpr bool X8 = KIND == kMx8;
+  constexpr int BK = Kind<KIND>::kBK, kStep = Kind<KIND>::kStep;
+  constexpr int kTilesKb = BK / (4 * Kind<KIND>::kBlock);  // scale tiles of a stage along d
   constexpr uint32_t kScaleKb = kTilesKb * kScaleTile;  // bytes, of 128 rows
   extern __shared__ unsigned char smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -276,7 +302,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   uint64_t* empty = full + kStages;
   uint64_t* sfull = empty + kStages;    // a stage's scales are in shared memory
   uint64_t* sempty = sfull + kStages;   // ... and have been read from it
-  uint64_t* tmem_full = sempty + kStages;
+  uint64_t* wfull = sempty + kStages;   // W's copies have landed (8-bit x)
+  uint64_t* tmem_full = wfull + kStages;
   uint64_t* tmem_empty = tmem_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_empty + 1);
   volatile int* aborted = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -291,7 +318,8 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 6);  // W, X, and the four scale warps
+      mbar_init(&full[s], X8 ? 5 : 6);  // W (but for 8-bit x), X, and the four scale warps
+      mbar_init(&wfull[s], 32);  // each lane of warp 0, when its copies have landed
       mbar_init(&empty[s], 1);
       mbar_init(&sempty[s], 4);  // one arrival per scale warp
       mbar_init(&sfull[s], 32);  // each lane of warp 3, when its copies have landed
@@ -313,7 +341,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     prefetch_map(&p.tmX);
     if (!p.y_f32) prefetch_map(&p.tmY);
   }
-  if (warp == 0 && lane < p.K) prefetch_map(&p.tmW[lane]);
+  if (!X8 && warp == 0 && lane < p.K) prefetch_map(&p.tmW[lane]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -323,7 +351,43 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   // that one has ended
   wait_stream();
 
-  if (warp == 0 || warp == 2) {
+  if (X8 && warp == 0) {
+    // ------------------------------ W by copies -------------------------------
+    // The 8-bit kind takes sixteen 4-bit values in the first 8 bytes of 16: each
+    // lane copies 8 bytes to where the swizzle puts their 16.  Rows past the
+    // shard's end read its last and are dropped; what lies past D belongs to no
+    // step.
+    int stage = 0;
+    uint32_t phase = 0;
+    const int c = lane & 7;
+    for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride) {
+      const Tile t = tile_at(p, i);
+      const uint8_t* base = p.w[t.shard] + c * 8;
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        const bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          *aborted = 1;
+          break;
+        }
+        if (kb * BK + c * 16 < p.D) {
+          const uint32_t to = smem_u32(sW + stage * kStageW);
+#pragma unroll 8
+          for (int j = 0; j < BM / 4; ++j) {
+            const int r = 4 * j + (lane >> 3);
+            async_copy8(to + (uint32_t)(r * kRowBytes + ((c ^ (r & 7)) << 4)),
+                        base + (size_t)min(t.f0 + r, p.F_shard - 1) * (p.D / 2) + kb * (BK / 2));
+          }
+        }
+        async_copy_arrive(&wfull[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0 && p.next_early) let_next_start();
+    async_copy_wait_all();  // no copy outlives the CTA
+  } else if (warp == 0 || warp == 2) {
     // ------------------------------ producers ---------------------------------
     if (lane == 0) {
       int stage = 0;
@@ -340,10 +404,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           }
           if (warp == 0) {
             mbar_arrive_expect_tx(&full[stage], kStageW);
-            tma_load_2d(&p.tmW[t.shard], &full[stage], sW + stage * kStageW, kb * (BK / 2), t.f0);
+            tma_load_2d(&p.tmW[t.shard], &full[stage], sW + stage * kStageW, kb * kRowBytes, t.f0);
           } else {
-            mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * (BK / 2));
-            tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * (BK / 2), t.m0);
+            mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * kRowBytes);
+            tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * kRowBytes, t.m0);
           }
           armed[stage] = true;
           armed_phase[stage] = phase;
@@ -400,7 +464,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     async_copy_wait_all();  // no copy outlives the CTA
   } else if (warp == 1) {
     // ------------------------------ MMA issuer --------------------------------
-    const uint32_t idesc = idesc_fp4(MX, p.BN);
+    const uint32_t idesc = idesc_fp4<KIND>(p.BN);
     const uint64_t a0 = sw128_kmajor_desc(smem_u32(sW)), b0 = sw128_kmajor_desc(smem_u32(sX));
     int stage = 0, w = 0;
     uint32_t phase = 0;
@@ -430,13 +494,14 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         const uint32_t tx = tw + 16u;
         const int steps = (p.D - kb * BK + kStep - 1) / kStep;  // the last stage may end early
         // step k: 32 bytes further along the rows.  nvfp4: its four scales
-        // are a tile's; mxfp4: its two are half of a tile's, chosen by the
-        // scale ids of the descriptor
+        // are a tile's; mxfp4: its two are half of a tile's, and with 8-bit x
+        // its one a quarter, chosen by the scale ids of the descriptor
+        constexpr int kPer = KIND == kNv4 ? 1 : X8 ? 4 : 2;  // steps of a scale tile
 #define DP_STEP(k)                                                                          \
-  mma_fp4<MX>(tmem_base, a + 2u * (k), b + 2u * (k),                                        \
-            MX ? idesc | ((uint32_t)((k) & 1) << 5) | ((uint32_t)((k) & 1) << 30) : idesc, \
-            tw + 4u * (MX ? (k) / 2 : (k)), tx + (uint32_t)kXCols * (MX ? (k) / 2 : (k)),               \
-            (k) > 0 || kb > kb_lo ? 1u : 0u)
+  mma_fp4<KIND>(tmem_base, a + 2u * (k), b + 2u * (k),                                      \
+                idesc | (uint32_t)((k) % kPer * (4 / kPer)) * ((1u << 4) | (1u << 29)),     \
+                tw + 4u * ((k) / kPer), tx + (uint32_t)kXCols * ((k) / kPer),               \
+                (k) > 0 || kb > kb_lo ? 1u : 0u)
         if (steps >= 4) {
           DP_STEP(0);
           DP_STEP(1);
@@ -516,11 +581,15 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           break;
         }
         tc_fence_after();
-        if constexpr (MX)
+        if constexpr (kTilesKb == 1)
+          DP_TMEM_ST_X4(tw, w);
+        else if constexpr (kTilesKb == 2)
           DP_TMEM_ST_X8(tw, w);
         else
           DP_TMEM_ST_X16(tw, w);
-        if constexpr (kXCols * kTilesKb == 8) {
+        if constexpr (kXCols * kTilesKb == 4) {
+          DP_TMEM_ST_X4(tw + 16u, x);
+        } else if constexpr (kXCols * kTilesKb == 8) {
           DP_TMEM_ST_X8(tw + 16u, x);
         } else {
           DP_TMEM_ST_X16(tw + 16u, x);
@@ -531,6 +600,15 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         }
         tmem_st_wait();
         tc_fence_before();
+        if constexpr (X8) {
+          // W was written by threads' copies: the MMA's proxy sees them after this
+          const bool here = mbar_wait_bounded(&wfull[stage], phase, p.err, kTimeoutNs);
+          if (!__all_sync(0xffffffffu, here)) {
+            *aborted = 1;
+            break;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[stage]);
         if (++stage == kStages) {
@@ -552,7 +630,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       const Tile t = tile_at(p, i);
       const int shard = t.shard, m0 = t.m0 + c0 * 16;
       float alpha = 1.0f;
-      if constexpr (!MX) {
+      if constexpr (KIND == kNv4) {
         if (p.tx) alpha = *p.tx;
         if (p.tw[shard]) alpha = __fmul_rn(alpha, *p.tw[shard]);
       }
@@ -603,7 +681,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
           for (int q = 0; q < 8; ++q) {
             const float lo = __uint_as_float(r[e * 16 + 2 * q]);
             const float hi = __uint_as_float(r[e * 16 + 2 * q + 1]);
-            h[c + e][q] = MX ? pack_bf16x2_rn(lo, hi)
+            h[c + e][q] = KIND != kNv4 ? pack_bf16x2_rn(lo, hi)
                              : pack_bf16x2_rn(__fmul_rn(lo, alpha), __fmul_rn(hi, alpha));
           }
       };
@@ -656,7 +734,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     const Tile t = tile_at(p, first);
     const int shard = t.shard, f0 = t.f0, m0 = t.m0;
     float alpha = 1.0f;
-    if constexpr (!MX) {
+    if constexpr (KIND == kNv4) {
       if (p.tx) alpha = *p.tx;
       if (p.tw[shard]) alpha = __fmul_rn(alpha, *p.tw[shard]);
     }
@@ -697,10 +775,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   }
 }
 
-template <bool MX, int BNMAX>
+template <int KIND, int BNMAX>
 cudaError_t launch_for(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, cudaStream_t s) {
   constexpr size_t kSmemBytes = Geo<BNMAX>::kSmem;
-  auto kernel = mx4mm_kernel<MX, BNMAX>;
+  auto kernel = mx4mm_kernel<KIND, BNMAX>;
   if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kThreadsM, kSmemBytes,
                           dev.device) < 1)
     return cudaErrorInvalidConfiguration;
@@ -737,12 +815,12 @@ cudaError_t launch_for(Mx4mmParams p, int tiles, const dph::DeviceInfo& dev, cud
   return cudaSuccess;
 }
 
-template <bool MX>
+template <int KIND>
 cudaError_t launch_mx4mm(const Mx4mmParams& p, int tiles, const dph::DeviceInfo& dev,
                          cudaStream_t s) {
-  if (p.BN <= 32) return launch_for<MX, 32>(p, tiles, dev, s);
-  if (p.BN <= 128) return launch_for<MX, 128>(p, tiles, dev, s);
-  return launch_for<MX, 256>(p, tiles, dev, s);
+  if (p.BN <= 32) return launch_for<KIND, 32>(p, tiles, dev, s);
+  if (p.BN <= 128) return launch_for<KIND, 128>(p, tiles, dev, s);
+  return launch_for<KIND, 256>(p, tiles, dev, s);
 }
 
 using dph::aligned;
@@ -754,9 +832,10 @@ using dph::span_of;
 
 namespace {
 
-// The product's checks, on the host alone.
+// The product's checks, on the host alone.  x8: x is in 8 bits.
 dp_status_t check_args(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, int K,
-                       int F_shard, dp_mx4_format_t format, void* y, dp_dtype_t y_dtype) {
+                       int F_shard, dp_mx4_format_t format, bool x8, void* y,
+                       dp_dtype_t y_dtype) {
   if (!x || !w_shards || K < 1 || K > DP_MAX_K) return DP_ERR_INVALID_ARG;
   if (M < 0 || D < 0 || F_shard < 0) return DP_ERR_INVALID_ARG;
   if (format != DP_MXFP4 && format != DP_NVFP4) return DP_ERR_UNSUPPORTED;
@@ -769,29 +848,29 @@ dp_status_t check_args(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards
   const size_t ysz = (size_t)M * K * F_shard * (y_dtype == DP_FP32 ? 4 : 2);
   if (!y && ysz) return DP_ERR_INVALID_ARG;
   const Span out = span_of(y, ysz);
-  const auto check = [&](const dp_mx4_t& a, int rows) -> dp_status_t {
+  const auto check = [&](const dp_mx4_t& a, int rows, size_t row_bytes) -> dp_status_t {
     if (mx && a.tensor_scale) return DP_ERR_INVALID_ARG;
     if ((!a.codes || !a.scales) && rows && D) return DP_ERR_INVALID_ARG;
     if (!aligned(a.codes, 16) || !aligned(a.scales, 16) || !aligned(a.tensor_scale, 4))
       return DP_ERR_UNSUPPORTED;
     size_t sbytes = 0;
     dp_mx4_scales_size(rows, D, format, &sbytes);
-    if (clash(out, span_of(a.codes, (size_t)rows * (D / 2))) ||
+    if (clash(out, span_of(a.codes, (size_t)rows * row_bytes)) ||
         clash(out, span_of(a.scales, sbytes)) ||
         (a.tensor_scale && clash(out, span_of(a.tensor_scale, 4))))
       return DP_ERR_ALIAS;
     return DP_OK;
   };
-  dp_status_t st = check(*x, M);
-  for (int k = 0; k < K && st == DP_OK; ++k) st = check(w_shards[k], F_shard);
+  dp_status_t st = check(*x, M, x8 ? D : D / 2);
+  for (int k = 0; k < K && st == DP_OK; ++k) st = check(w_shards[k], F_shard, D / 2);
   return st;
 }
 
 // The launch parameters of a checked product; nothing is enqueued.  *tiles is
 // 0 where there is nothing to multiply (then *zero_bytes of y are to be zeroed).
 dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, int K, int F_shard,
-                    dp_mx4_format_t format, void* y, dp_dtype_t y_dtype, dph::DeviceInfo* devp,
-                    Mx4mmParams* pp, int* tilesp, size_t* zero_bytes) {
+                    dp_mx4_format_t format, bool x8, void* y, dp_dtype_t y_dtype,
+                    dph::DeviceInfo* devp, Mx4mmParams* pp, int* tilesp, size_t* zero_bytes) {
   *tilesp = 0;
   *zero_bytes = 0;
   const int F = K * F_shard, block = mx4_block(format);
@@ -824,7 +903,8 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   if (M > 128 && tiles_of(256) < dev.sm_count) p.BN = 128;
   while (p.BN > 32 && tiles_of(p.BN) * 2 <= dev.sm_count) p.BN = p.BN > 64 ? 64 : 32;
   p.tiles_m = (M + p.BN - 1) / p.BN;
-  p.num_kb = (D + BK - 1) / BK;
+  const int bk = x8 ? Kind<kMx8>::kBK : Kind<kMx4>::kBK;
+  p.num_kb = (D + bk - 1) / bk;
   p.col_tiles = mx4_col_tiles(D, block);
   p.x_row_tiles = (M + kScaleRows - 1) / kScaleRows;
   if ((long long)all_f * p.tiles_m > 0x3fffffffll) return DP_ERR_UNSUPPORTED;
@@ -851,10 +931,11 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   p.err = dev.err_word;
   if (!p.y_f32 && !dpl::encode_output_shards(&p.tmY, y, M, K, F_shard, kOutTokens))
     return DP_ERR_UNSUPPORTED;
-  if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, D / 2, p.BN)) return DP_ERR_UNSUPPORTED;
+  if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, x8 ? D : D / 2, p.BN)) return DP_ERR_UNSUPPORTED;
   for (int k = 0; k < K; ++k) {
-    if (!dpl::encode_kmajor_bytes(&p.tmW[k], w_shards[k].codes, F_shard, D / 2, BM))
+    if (!x8 && !dpl::encode_kmajor_bytes(&p.tmW[k], w_shards[k].codes, F_shard, D / 2, BM))
       return DP_ERR_UNSUPPORTED;
+    p.w[k] = static_cast<const uint8_t*>(w_shards[k].codes);
     p.sw[k] = static_cast<const uint8_t*>(w_shards[k].scales);
     p.tw[k] = w_shards[k].tensor_scale;
   }
@@ -862,66 +943,69 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   return DP_OK;
 }
 
-dp_status_t enqueue(const Mx4mmParams& p, int tiles, size_t zero_bytes, dp_mx4_format_t format,
+dp_status_t enqueue(const Mx4mmParams& p, int tiles, size_t zero_bytes, int kind,
                     const dph::DeviceInfo& dev, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (zero_bytes)
     e = cudaMemsetAsync(p.y, 0, zero_bytes, s);
   else if (tiles)
-    e = format == DP_MXFP4 ? launch_mx4mm<true>(p, tiles, dev, s)
-                           : launch_mx4mm<false>(p, tiles, dev, s);
+    e = kind == kMx8   ? launch_mx4mm<kMx8>(p, tiles, dev, s)
+        : kind == kMx4 ? launch_mx4mm<kMx4>(p, tiles, dev, s)
+                       : launch_mx4mm<kNv4>(p, tiles, dev, s);
   return e == cudaSuccess ? DP_OK : DP_ERR_CUDA;
 }
 
 // The scratch of the call that quantises x: its codes, then its scales.
-size_t codes_bytes(int M, int D) { return ((size_t)M * (D / 2) + 255) / 256 * 256; }
+size_t codes_bytes(int M, size_t row_bytes) {
+  return ((size_t)M * row_bytes + 255) / 256 * 256;
+}
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards,
-                                    int K, int F_shard, dp_mx4_format_t format, void* y,
-                                    dp_dtype_t y_dtype, dp_stream_t stream) {
-  dph::NvtxRange nvtx_range("dp_allgather_matmul_mx4");
+// The product of quantised operands.
+dp_status_t product(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, int K, int F_shard,
+                    dp_mx4_format_t format, bool x8, void* y, dp_dtype_t y_dtype,
+                    dp_stream_t stream) {
   dph::DeviceInfo dev;
   Mx4mmParams p;
   int tiles;
   size_t zero;
-  dp_status_t st = check_args(x, M, D, w_shards, K, F_shard, format, y, y_dtype);
+  dp_status_t st = check_args(x, M, D, w_shards, K, F_shard, format, x8, y, y_dtype);
   if (st == DP_OK)
-    st = prepare(x, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
+    st = prepare(x, M, D, w_shards, K, F_shard, format, x8, y, y_dtype, &dev, &p, &tiles, &zero);
   if (st != DP_OK) return st;
   p.y = y;
-  return enqueue(p, tiles, zero, format, dev, reinterpret_cast<cudaStream_t>(stream));
+  return enqueue(p, tiles, zero, x8 ? kMx8 : format == DP_MXFP4 ? kMx4 : kNv4, dev,
+                 reinterpret_cast<cudaStream_t>(stream));
 }
 
-dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_format_t format,
-                                                   size_t* bytes) {
+dp_status_t workspace_size(int M, int D, dp_mx4_format_t format, bool x8, size_t* bytes) {
   if (!bytes) return DP_ERR_INVALID_ARG;
   *bytes = 0;
   if (M < 0 || D < 0) return DP_ERR_INVALID_ARG;
   size_t scales = 0;
   const dp_status_t st = dp_mx4_scales_size(M, D, format, &scales);
   if (st != DP_OK) return st;
-  *bytes = codes_bytes(M, D) + scales;
+  *bytes = codes_bytes(M, x8 ? D : D / 2) + scales;
   return DP_OK;
 }
 
-dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long long ld, dp_dtype_t x_dtype,
-                                    const float* x_scale, const dp_mx4_t* w_shards, int K,
-                                    int F_shard, dp_mx4_format_t format, void* y,
-                                    dp_dtype_t y_dtype, void* workspace, size_t workspace_bytes,
-                                    dp_stream_t stream) {
-  dph::NvtxRange nvtx_range("dp_allgather_linear_mx4");
+// ... with x quantised on the way.
+dp_status_t linear(const void* x, int M, int D, long long ld, dp_dtype_t x_dtype,
+                   const float* x_scale, const dp_mx4_t* w_shards, int K, int F_shard,
+                   dp_mx4_format_t format, bool x8, void* y, dp_dtype_t y_dtype, void* workspace,
+                   size_t workspace_bytes, dp_stream_t stream) {
   size_t need = 0;
-  dp_status_t st = dp_allgather_linear_mx4_workspace_size(M, D, format, &need);
+  dp_status_t st = workspace_size(M, D, format, x8, &need);
   if (st != DP_OK) return st;
   if (workspace_bytes < need || (!workspace && need)) return DP_ERR_INVALID_ARG;
-  const dp_mx4_t q{workspace, static_cast<uint8_t*>(workspace) + codes_bytes(M, D), x_scale};
+  const dp_mx4_t q{workspace, static_cast<uint8_t*>(workspace) + codes_bytes(M, x8 ? D : D / 2),
+                   x_scale};
   // everything is checked before the first launch; the workspace, written by
   // the quantisation, must leave the weights alone too, and y the unquantised x
-  st = check_args(&q, M, D, w_shards, K, F_shard, format, y, y_dtype);
+  st = check_args(&q, M, D, w_shards, K, F_shard, format, x8, y, y_dtype);
   if (st != DP_OK) return st;
   const Span ws = span_of(workspace, need);
   size_t sbytes = 0;
@@ -939,13 +1023,61 @@ dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long long ld, d
   Mx4mmParams p;
   int tiles;
   size_t zero;
-  st = prepare(&q, M, D, w_shards, K, F_shard, format, y, y_dtype, &dev, &p, &tiles, &zero);
+  st = prepare(&q, M, D, w_shards, K, F_shard, format, x8, y, y_dtype, &dev, &p, &tiles, &zero);
   if (st != DP_OK) return st;
-  st = dp_mx4_quantize(&x, 1, M, D, ld, x_dtype, format, 0, x_scale, workspace,
-                       const_cast<void*>(q.scales), stream);
+  void* scales = const_cast<void*>(q.scales);
+  st = x8 ? dp_mx8_quantize(x, M, D, ld, x_dtype, workspace, scales, stream)
+          : dp_mx4_quantize(&x, 1, M, D, ld, x_dtype, format, 0, x_scale, workspace, scales, stream);
   if (st != DP_OK) return st;
   p.y = y;
-  return enqueue(p, tiles, zero, format, dev, reinterpret_cast<cudaStream_t>(stream));
+  return enqueue(p, tiles, zero, x8 ? kMx8 : format == DP_MXFP4 ? kMx4 : kNv4, dev,
+                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+dp_status_t dp_allgather_matmul_mx4(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards,
+                                    int K, int F_shard, dp_mx4_format_t format, void* y,
+                                    dp_dtype_t y_dtype, dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_allgather_matmul_mx4");
+  return product(x, M, D, w_shards, K, F_shard, format, false, y, y_dtype, stream);
+}
+
+dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_format_t format,
+                                                   size_t* bytes) {
+  return workspace_size(M, D, format, false, bytes);
+}
+
+dp_status_t dp_allgather_linear_mx4(const void* x, int M, int D, long long ld, dp_dtype_t x_dtype,
+                                    const float* x_scale, const dp_mx4_t* w_shards, int K,
+                                    int F_shard, dp_mx4_format_t format, void* y,
+                                    dp_dtype_t y_dtype, void* workspace, size_t workspace_bytes,
+                                    dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_allgather_linear_mx4");
+  return linear(x, M, D, ld, x_dtype, x_scale, w_shards, K, F_shard, format, false, y, y_dtype,
+                workspace, workspace_bytes, stream);
+}
+
+dp_status_t dp_allgather_matmul_mx8(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards,
+                                    int K, int F_shard, void* y, dp_dtype_t y_dtype,
+                                    dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_allgather_matmul_mx8");
+  return product(x, M, D, w_shards, K, F_shard, DP_MXFP4, true, y, y_dtype, stream);
+}
+
+dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* bytes) {
+  return workspace_size(M, D, DP_MXFP4, true, bytes);
+}
+
+dp_status_t dp_allgather_linear_mx8(const void* x, int M, int D, long long ld, dp_dtype_t x_dtype,
+                                    const dp_mx4_t* w_shards, int K, int F_shard, void* y,
+                                    dp_dtype_t y_dtype, void* workspace, size_t workspace_bytes,
+                                    dp_stream_t stream) {
+  dph::NvtxRange nvtx_range("dp_allgather_linear_mx8");
+  return linear(x, M, D, ld, x_dtype, nullptr, w_shards, K, F_shard, DP_MXFP4, true, y, y_dtype,
+                workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -107,6 +107,11 @@ __device__ __forceinline__ void tmem_st_wait() {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])   \
       : "memory")
 
+#define DP_TMEM_ST_X4(taddr, r)                                                               \
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),     \
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])                                     \
+               : "memory")
+
 }  // namespace dpk
 
 namespace dpl {

@@ -15,7 +15,7 @@ import torch
 
 from . import binding as B
 from .collectives import _DT, _code
-from .mx4 import _on, _rows, _scale_bytes
+from .mx4 import _on, _rows, _scale_bytes, _shards
 
 
 class Mx8Tensor:
@@ -98,3 +98,45 @@ def dequantize(q: Mx8Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     B.dp_mx8_dequantize(q._c.codes, q._c.scales, rows, cols, out, _DT[dtype],
                         stream=B._stream_on(dev, "dequantize"))
     return out
+
+
+def matmul(x: Mx8Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y = x . w^T with w the row concatenation of the mxfp4 shards."""
+    M, D, dev = x._kind
+    if stream is not None:
+        with _on(stream, dev):
+            return matmul(x, w_shards, y_dtype)
+    if y_dtype not in _DT:
+        raise TypeError(f"unsupported dtype {y_dtype}")
+    arr = _shards(w_shards, D, "mxfp4", dev)
+    K, F = len(w_shards), w_shards[0].rows
+    y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
+    B.dp_allgather_matmul_mx8(x._c, M, D, arr, K, F, y, _DT[y_dtype],
+                              stream=B._stream_on(dev, "matmul"))
+    return y
+
+
+def linear(x: torch.Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """y = x . w^T with x [M, D] quantised to 8 bits on the way and w the row
+    concatenation of the mxfp4 shards, in one call.  Records no gradient."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return linear(x, w_shards, y_dtype)
+    x, ld = _rows(x)
+    M, D = x.shape
+    if y_dtype not in _DT:
+        raise TypeError(f"unsupported dtype {y_dtype}")
+    dev, code = x.device, _code(x)
+    arr = _shards(w_shards, D, "mxfp4", dev)
+    K, F = len(w_shards), w_shards[0].rows
+    here = B._stream_on(dev, "linear")
+    # scratch of this call alone: the allocator hands it on in stream order
+    nbytes = -(-M * D // 256) * 256 + _scale_bytes(M, D, "mxfp4")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
+    st = (B._lib or B.load()).dp_allgather_linear_mx8(
+        x.data_ptr(), M, D, ld, code, arr, K, F, y.data_ptr(), _DT[y_dtype], ws.data_ptr(), nbytes,
+        here)
+    if st:
+        raise B.DpError(st, "dp_allgather_linear_mx8")
+    return y

@@ -1,10 +1,10 @@
-"""Refusals of the few-token product, made on the host before any device call."""
+"""Refusals of the few-token product and of the products of 8-bit x, made on the host before any device call."""
 import pytest
 import torch
 
 from ring_allreduce_gradient_gb300 import binding as B
 from ring_allreduce_gradient_gb300 import build as cuda_build
-from ring_allreduce_gradient_gb300 import mx4
+from ring_allreduce_gradient_gb300 import mx4, mx8
 
 BASE = 0x7F0000000000
 OK, INVALID, UNSUPPORTED, ALIAS = (B.DP_OK, B.DP_ERR_INVALID_ARG, B.DP_ERR_UNSUPPORTED,
@@ -59,3 +59,54 @@ def test_the_helper_checks():
                             ((x, [q]), B.DpError, "not the current CUDA device")]:
         with pytest.raises(err, match=word):
             mx4.linear_w4(*args)
+
+
+def test_eight_bit_product_checks():
+    ws = [(fake(2 * k + 2), fake(2 * k + 3), None) for k in range(2)]
+    x = (fake(0), fake(1), None)
+
+    def m(x=x, M=64, D=64, w=ws, K=2, Fs=32, y=fake(20), dt=B.DP_BF16):
+        return B.dp_allgather_matmul_mx8(x, M, D, w, K, Fs, y, dt, stream=0, check=False)
+
+    assert m(K=0) == INVALID and m(K=17) == INVALID and m(M=-1) == INVALID
+    assert m(x=(None, fake(1), None)) == INVALID and m(x=(fake(0), None, None)) == INVALID
+    assert m(x=(fake(0), fake(1), fake(9))) == INVALID and m(y=None) == INVALID
+    assert m(w=[ws[0], (None, fake(5), None)]) == INVALID
+    assert m(D=48) == UNSUPPORTED and m(Fs=24) == UNSUPPORTED and m(dt=5) == UNSUPPORTED
+    assert m(x=(fake(0, 8), fake(1), None)) == UNSUPPORTED and m(y=fake(20, 4)) == UNSUPPORTED
+    assert m(y=fake(0)) == ALIAS and m(y=fake(0, 64 * 64 - 16)) == ALIAS    # 8 bits: 64 x 64 bytes
+    assert m(y=fake(1)) == ALIAS and m(y=fake(4, 512)) == ALIAS and m(y=fake(5)) == ALIAS
+    assert m(M=0, y=None) == OK and m(Fs=0, y=None) == OK
+
+    need = B.dp_allgather_linear_mx8_workspace_size(64, 64)
+    assert need == 64 * 64 + 512
+
+    def lin(x=fake(0), M=64, D=64, ld=64, xdt=B.DP_BF16, w=ws, Fs=32, y=fake(20), dt=B.DP_BF16,
+            work=fake(30), wb=need):
+        return B.dp_allgather_linear_mx8(x, M, D, ld, xdt, w, 2, Fs, y, dt, work, wb, stream=0,
+                                         check=False)
+
+    assert lin(work=None) == INVALID and lin(wb=need - 1) == INVALID and lin(M=-1) == INVALID
+    assert lin(work=fake(30, 8)) == UNSUPPORTED and lin(D=48, ld=48) == UNSUPPORTED
+    assert lin(work=fake(20)) == ALIAS and lin(work=fake(2)) == ALIAS and lin(work=fake(3)) == ALIAS
+    assert lin(y=fake(0, 64)) == ALIAS
+
+
+def test_the_eight_bit_helpers_check():
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    w = mx4.Mx4Tensor(u8(16 * 32), u8(512), 16, 64, "mxfp4")
+    nv = mx4.Mx4Tensor(u8(16 * 32), u8(512), 16, 64, "nvfp4")
+    q = mx8.Mx8Tensor(u8(4 * 64), u8(512), 4, 64)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call, a in ((mx8.linear, x), (mx8.matmul, q)):
+        for args, err, word in [((a, [w], torch.float16), TypeError, "dtype"),
+                                ((a, []), ValueError, "at least one shard"),
+                                ((a, [nv]), ValueError, "mxfp4"),
+                                ((a, [w, nv]), ValueError, "one shape"),
+                                ((a, [w]), B.DpError, "not the current CUDA device")]:
+            with pytest.raises(err, match=word):
+                call(*args)
+    with pytest.raises(TypeError, match="dtype"):
+        mx8.linear(x.half(), [w])
+    with pytest.raises(ValueError, match="columns"):
+        mx8.linear(x[:, :32], [w])
