@@ -858,7 +858,7 @@ DP_API dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* 
  *   dx = rstd * (g - xh * mean over D of (g * xh)) + dh      of dtype, contiguous
  *   dweight = sum over rows of dy * xh                       D floats
  * dx is the gradient of x and of the residual alike.  A quantised y's gradient
- * passes straight through.  dweight is summed in fp32 over at most 456 sets of
+ * passes straight through.  dweight is summed in fp32 over at most 304 sets of
  * rows, then over those; the order follows from M and D, so a repeated call gives
  * the same bits under any CTA limit.  M == 0 writes zeros to dweight.
  * workspace: device memory of dp_rms_norm_backward_workspace_size(M, D) bytes,

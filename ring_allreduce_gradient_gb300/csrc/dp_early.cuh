@@ -33,13 +33,14 @@ namespace dph {
 
 template <typename P>
 cudaError_t launch_early(void (*kernel)(P), const P& p, unsigned grid, unsigned threads,
-                         cudaStream_t s) {
+                         cudaStream_t s, size_t smem = 0) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

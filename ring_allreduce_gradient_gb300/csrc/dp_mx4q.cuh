@@ -96,6 +96,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // The tensor's scale, and a block's: its byte from the block's largest
 // magnitude, and eight of its values to codes.
 template <int BLOCK>
@@ -236,17 +242,19 @@ struct Scale8 {
     byte = bad ? 255u : (uint32_t)max(e, 0);
     f = __uint_as_float((254u - byte) << 23);
   }
-  // Four values to four codes, the first in the lowest byte.
-  __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
-    if (bad) return 0u;
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(lo)
-        : "f"(__fmul_rn(b, f)), "f"(__fmul_rn(a, f)));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(hi)
-        : "f"(__fmul_rn(d, f)), "f"(__fmul_rn(c, f)));
-    return (uint32_t)lo | (uint32_t)hi << 16;
+  // Four values, in pairs, to four codes, the first in the lowest byte.
+  __device__ __forceinline__ uint32_t codes(uint64_t ab, uint64_t cd) const {
+    float a, b, c, d;
+    unpair(mul2(ab, pair(f, f)), a, b);
+    unpair(mul2(cd, pair(f, f)), c, d);
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return bad ? 0u : r;
   }
 };
 

@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(kThreads) quant8_kernel(const __grid_constant_
         for (int h = 0; h < 2; ++h) {
           float w[8];
           v[g].widen(h, w);
-          c[2 * h] = s.codes(w[0], w[1], w[2], w[3]);
-          c[2 * h + 1] = s.codes(w[4], w[5], w[6], w[7]);
+          c[2 * h] = s.codes(pair(w[0], w[1]), pair(w[2], w[3]));
+          c[2 * h + 1] = s.codes(pair(w[4], w[5]), pair(w[6], w[7]));
         }
         *reinterpret_cast<uint4*>(p.codes + (size_t)r * p.L + e) = make_uint4(c[0], c[1], c[2], c[3]);
       }

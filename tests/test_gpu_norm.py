@@ -6,15 +6,15 @@ Tolerances, with u = 2^-24:
   * rstd: a sum of squares is 8 products to an accumulator, 2 additions to join
     four, 5 among lanes and 5 among warps, each within u: 20 u of a sum of
     positive terms; mean, eps, root and quotient add 4 roundings, the root halves
-    what came before: within 16 u.
+    what came before: within 16 u.  (The correction of the quotient only lowers it.)
   * y: two products more, 18 u, and the rounding to the dtype, eps / 2.
   * quantised y: the oracle's value, unless y lies within 32 u of a tie or its
     block's largest within 32 u of where the scale changes.
   * dx: g and xh are within u and 2 u; their products' sum within 22 u of the sum
     S of magnitudes, c within 24 u S / D of itself; the difference is one rounding
     of g - xh c, the product with rstd and the addition of dh one each.
-  * dw: a chain of `rows of a set` products, then at most 15 + 5 additions, and the
-    factor's 2 u, of the sum of magnitudes.
+  * dw: a chain of `rows of a set` products, the 8 or fewer rows that a CTA takes at
+    once, then at most 15 + 5 additions, and the factor's 2 u, of the sum of magnitudes.
 """
 import numpy as np
 import pytest
@@ -298,9 +298,9 @@ def backward(dy, h, w, rstd, dh):
                   2 * U * (np.abs(want) + np.abs(d)) + HALF[h.dtype] * np.abs(want))
     tol += 2.0 ** -149
     assert dx.dtype == h.dtype and np.all(np.abs(f64(dx) - want) <= tol)
-    per = 4 if D <= 1024 else 1
-    sets = min(-(-M // per), 456 // per)
-    chain = -(-M // (sets * per)) + 15 + 5 + 2
+    per = 8 // -(-D // 512) if D <= 4096 else 1          # rows of a CTA at once
+    sets = min(-(-M // per), 304 if D <= 4096 else 152)
+    chain = -(-M // (sets * per)) + per + 15 + 5 + 2
     size = np.abs(y * xh).sum(0)
     assert dw.dtype == torch.float32
     assert np.all(np.abs(f64(dw) - (y * xh).sum(0)) <= 1.01 * chain * U * size + 2.0 ** -149)

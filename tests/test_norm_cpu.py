@@ -66,8 +66,9 @@ def test_norm_checks():
 
 def test_backward_checks(lib):
     need = B.dp_rms_norm_backward_workspace_size(64, 64)
-    assert need == 64 * 64 * 4
-    assert B.dp_rms_norm_backward_workspace_size(100000, 4096) == 456 * 4096 * 4
+    assert need == 8 * 64 * 4                      # sets of eight rows
+    assert B.dp_rms_norm_backward_workspace_size(100000, 4096) == 304 * 4096 * 4
+    assert B.dp_rms_norm_backward_workspace_size(100000, 8192) == 152 * 8192 * 4
     assert B.dp_rms_norm_backward_workspace_size(0, 64) == 0
 
     def bwd(dy=fake(0), ldy=64, h=fake(1), ldh=64, dh=None, ldd=0, M=64, D=64, dt=B.DP_BF16,
