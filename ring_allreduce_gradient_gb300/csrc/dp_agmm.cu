@@ -841,6 +841,18 @@ bool encode_kmajor_bytes(CUtensorMap* map, const void* base, int rows, int row_b
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_kmajor_padded4(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
+  if (!get_encoder()) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols / 2};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_output_shards(CUtensorMap* map, void* base, int M, int K, int F_shard, int box_rows) {
   if (!get_encoder()) return false;
   cuuint64_t dims[3] = {(cuuint64_t)F_shard, (cuuint64_t)K, (cuuint64_t)M};

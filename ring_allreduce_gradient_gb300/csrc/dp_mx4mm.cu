@@ -102,7 +102,7 @@ struct Geo {
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   static_assert(kScaleCol0 + kStages * kScaleCols <= 512, "TMEM columns");
   static_assert((uint32_t)BNMAX * BM * 4 <= kStages * (kStageW + kStageX), "partial sums");
-  static_assert((5 * kStages + 2) * 8 + 8 <= kBarBytes, "barriers");
+  static_assert((4 * kStages + 2) * 8 + 8 <= kBarBytes, "barriers");
 };
 
 constexpr int kTmemCols = 512;
@@ -131,6 +131,7 @@ struct Mx4mmParams {
   int split;              // CTAs of a cluster that share a tile
   int y_f32;
   int next_early;         // let the next kernel move in before this one's end
+  int w_copies;           // 8-bit x: W comes by threads' copies instead of TMA
 };
 
 // Tile i of this launch.
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   constexpr int BK = Kind<KIND>::kBK, kStep = Kind<KIND>::kStep;
   constexpr int kTilesKb = BK / (4 * Kind<KIND>::kBlock);  // scale tiles of a stage along d
   constexpr uint32_t kScaleKb = kTilesKb * kScaleTile;  // bytes, of 128 rows
+  const bool copies = X8 && p.w_copies;
   extern __shared__ unsigned char smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -300,10 +302,9 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   uint8_t* sY = sSX + kStages * kStageSX;
   uint64_t* full = reinterpret_cast<uint64_t*>(sY + 2 * kStageY);
   uint64_t* empty = full + kStages;
-  uint64_t* sfull = empty + kStages;    // a stage's scales are in shared memory
+  uint64_t* sfull = empty + kStages;    // a stage's scales (and W, if by copies) are in shared memory
   uint64_t* sempty = sfull + kStages;   // ... and have been read from it
-  uint64_t* wfull = sempty + kStages;   // W's copies have landed (8-bit x)
-  uint64_t* tmem_full = wfull + kStages;
+  uint64_t* tmem_full = sempty + kStages;
   uint64_t* tmem_empty = tmem_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tmem_empty + 1);
   volatile int* aborted = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -318,11 +319,10 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], X8 ? 5 : 6);  // W (but for 8-bit x), X, and the four scale warps
-      mbar_init(&wfull[s], 32);  // each lane of warp 0, when its copies have landed
+      mbar_init(&full[s], 6);  // W, X, and the four scale warps
       mbar_init(&empty[s], 1);
       mbar_init(&sempty[s], 4);  // one arrival per scale warp
-      mbar_init(&sfull[s], 32);  // each lane of warp 3, when its copies have landed
+      mbar_init(&sfull[s], 32);  // each lane of warp 3 (W by copies: 0), when its copies have landed
     }
     mbar_init(tmem_full, 1);
     mbar_init(tmem_empty, kEpiWarps);
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
     prefetch_map(&p.tmX);
     if (!p.y_f32) prefetch_map(&p.tmY);
   }
-  if (!X8 && warp == 0 && lane < p.K) prefetch_map(&p.tmW[lane]);
+  if (!copies && warp == 0 && lane < p.K) prefetch_map(&p.tmW[lane]);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -351,18 +351,28 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
   // that one has ended
   wait_stream();
 
-  if (X8 && warp == 0) {
+  if (copies && warp == 0) {
     // ------------------------------ W by copies -------------------------------
-    // The 8-bit kind takes sixteen 4-bit values in the first 8 bytes of 16: each
-    // lane copies 8 bytes to where the swizzle puts their 16.  Rows past the
-    // shard's end read its last and are dropped; what lies past D belongs to no
-    // step.
+    // What TMA does for the 8-bit kind where its rules (rows of whole 128 values)
+    // do not hold: sixteen 4-bit values go to the first 8 bytes of 16, so each lane
+    // copies 8 bytes to where the swizzle puts their 16.  Rows past the shard's end
+    // read its last and are dropped; what lies past D belongs to no step.
     int stage = 0;
     uint32_t phase = 0;
-    const int c = lane & 7;
+    const int c = lane & 7, r0 = lane >> 3;  // chunk of the row, first row of every four
+    const size_t row = (size_t)(p.D / 2);
+    const uint32_t at = (uint32_t)(r0 * kRowBytes);
+    const uint32_t even = at + (uint32_t)((c ^ r0) << 4), odd = at + (uint32_t)((c ^ (r0 + 4)) << 4);
     for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride) {
       const Tile t = tile_at(p, i);
-      const uint8_t* base = p.w[t.shard] + c * 8;
+      const uint8_t* tile = p.w[t.shard] + (size_t)t.f0 * row + c * 8;
+      const int last = p.F_shard - 1 - t.f0;
+      const uint8_t* gw =
+          p.sw[t.shard] + (size_t)(t.f0 / kScaleRows) * p.col_tiles * kScaleTile + lane * 16;
+      const int x0 = t.m0 / kScaleRows;
+      const uint8_t* gx = p.sx + (size_t)x0 * p.col_tiles * kScaleTile + lane * 16;
+      const int rows =
+          min((t.m0 % kScaleRows + p.BN + kScaleRows - 1) / kScaleRows, p.x_row_tiles - x0);
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         const bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -371,14 +381,28 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         }
         if (kb * BK + c * 16 < p.D) {
           const uint32_t to = smem_u32(sW + stage * kStageW);
+          const uint8_t* from = tile + kb * (BK / 2);
+          if (last >= BM - 1) {
+            from += r0 * row;
+#pragma unroll
+            for (int j = 0; j < BM / 4; ++j, from += 4 * row)
+              async_copy8(to + (uint32_t)(j * 4 * kRowBytes) + (j & 1 ? odd : even), from);
+          } else {
 #pragma unroll 8
-          for (int j = 0; j < BM / 4; ++j) {
-            const int r = 4 * j + (lane >> 3);
-            async_copy8(to + (uint32_t)(r * kRowBytes + ((c ^ (r & 7)) << 4)),
-                        base + (size_t)min(t.f0 + r, p.F_shard - 1) * (p.D / 2) + kb * (BK / 2));
+            for (int j = 0; j < BM / 4; ++j)
+              async_copy8(to + (uint32_t)(j * 4 * kRowBytes) + (j & 1 ? odd : even),
+                          from + (size_t)min(4 * j + r0, last) * row);
           }
         }
-        async_copy_arrive(&wfull[stage]);
+        // the stage's scales with it: they have been read where the stage is empty
+        if (kb < p.col_tiles) {
+          async_copy16(sSW + stage * kStageSW + lane * 16, gw + (size_t)kb * kScaleTile);
+          async_copy16(sSX + stage * kStageSX + lane * 16, gx + (size_t)kb * kScaleTile);
+          if (G::kXTiles > 1 && rows > 1)
+            async_copy16(sSX + stage * kStageSX + kScaleKb + lane * 16,
+                         gx + ((size_t)p.col_tiles + kb) * kScaleTile);
+        }
+        async_copy_arrive(&sfull[stage]);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
@@ -403,8 +427,9 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
             break;
           }
           if (warp == 0) {
-            mbar_arrive_expect_tx(&full[stage], kStageW);
-            tma_load_2d(&p.tmW[t.shard], &full[stage], sW + stage * kStageW, kb * kRowBytes, t.f0);
+            // (8-bit x: half of the bytes, which TMA spreads over the stage's)
+            mbar_arrive_expect_tx(&full[stage], X8 ? kStageW / 2 : kStageW);
+            tma_load_2d(&p.tmW[t.shard], &full[stage], sW + stage * kStageW, kb * 128, t.f0);
           } else {
             mbar_arrive_expect_tx(&full[stage], (uint32_t)p.BN * kRowBytes);
             tma_load_2d(&p.tmX, &full[stage], sX + stage * kStageX, kb * kRowBytes, t.m0);
@@ -423,6 +448,27 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
       for (int s = 0; s < kStages; ++s)
         if (armed[s]) (void)mbar_wait_bounded(&full[s], armed_phase[s], p.err, kTimeoutNs);
     }
+  } else if (copies && warp == 3) {
+    // ------------------------------ W to the MMA's proxy ----------------------
+    // W was written by threads' copies; the MMA sees them after this fence.
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = first; i < p.tiles && !__any_sync(0xffffffffu, *aborted); i += stride)
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        const bool ok = mbar_wait_bounded(&sfull[stage], phase, p.err, kTimeoutNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          *aborted = 1;
+          break;
+        }
+        if (lane == 0) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive(&full[stage]);
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
   } else if (warp == 3) {
     // ------------------------------ scales into shared memory -----------------
     int stage = 0;
@@ -573,12 +619,14 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
             x[o] = b.x, x[o + 1] = b.y, x[o + 2] = b.z, x[o + 3] = b.w;
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty[stage]);  // the next ones can come while these wait
-        const bool free = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs);
-        if (!__all_sync(0xffffffffu, free)) {
-          *aborted = 1;
-          break;
+        if (!copies) {  // (else the scales came after the stage was empty)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[stage]);  // the next ones can come while these wait
+          const bool free = mbar_wait_bounded(&empty[stage], phase ^ 1u, p.err, kTimeoutNs);
+          if (!__all_sync(0xffffffffu, free)) {
+            *aborted = 1;
+            break;
+          }
         }
         tc_fence_after();
         if constexpr (kTilesKb == 1)
@@ -600,15 +648,6 @@ __global__ void __launch_bounds__(kThreadsM, 1) mx4mm_kernel(const __grid_consta
         }
         tmem_st_wait();
         tc_fence_before();
-        if constexpr (X8) {
-          // W was written by threads' copies: the MMA's proxy sees them after this
-          const bool here = mbar_wait_bounded(&wfull[stage], phase, p.err, kTimeoutNs);
-          if (!__all_sync(0xffffffffu, here)) {
-            *aborted = 1;
-            break;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[stage]);
         if (++stage == kStages) {
@@ -932,8 +971,13 @@ dp_status_t prepare(const dp_mx4_t* x, int M, int D, const dp_mx4_t* w_shards, i
   if (!p.y_f32 && !dpl::encode_output_shards(&p.tmY, y, M, K, F_shard, kOutTokens))
     return DP_ERR_UNSUPPORTED;
   if (!dpl::encode_kmajor_bytes(&p.tmX, x->codes, M, x8 ? D : D / 2, p.BN)) return DP_ERR_UNSUPPORTED;
+  if (x8) {
+    p.w_copies = D % 128 != 0;
+    for (int k = 0; k < K; ++k) p.w_copies |= !aligned(w_shards[k].codes, 32);
+  }
   for (int k = 0; k < K; ++k) {
-    if (!x8 && !dpl::encode_kmajor_bytes(&p.tmW[k], w_shards[k].codes, F_shard, D / 2, BM))
+    if (x8 ? !p.w_copies && !dpl::encode_kmajor_padded4(&p.tmW[k], w_shards[k].codes, F_shard, D, BM)
+           : !dpl::encode_kmajor_bytes(&p.tmW[k], w_shards[k].codes, F_shard, D / 2, BM))
       return DP_ERR_UNSUPPORTED;
     p.w[k] = static_cast<const uint8_t*>(w_shards[k].codes);
     p.sw[k] = static_cast<const uint8_t*>(w_shards[k].scales);

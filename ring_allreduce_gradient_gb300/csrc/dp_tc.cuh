@@ -118,6 +118,9 @@ namespace dpl {
 // An operand map for packed 4-bit values; false where it cannot be encoded.
 bool encode_kmajor_bytes(CUtensorMap* map, const void* base, int rows, int row_bytes,
                          int box_rows);
+// An operand map for 4-bit values beside 8-bit ones: sixteen of them to 16 bytes of
+// shared memory, in the first 8.  base: 32-byte aligned; cols a multiple of 128.
+bool encode_kmajor_padded4(CUtensorMap* map, const void* base, int rows, int cols, int box_rows);
 // An output map of bf16 y [M, K * F_shard] as (f of a shard, shard, row): boxes
 // of 128 f of one shard x box_rows rows, clipped at the shard's end.
 bool encode_output_shards(CUtensorMap* map, void* base, int M, int K, int F_shard, int box_rows);
