@@ -61,12 +61,13 @@ struct W4Params {
   int y_f32;
 };
 
-template <int MT, int NT>
+template <bool MX, int MT, int NT>
 struct W4Geo {
-  static constexpr int kStages = NT == 4 ? 2 : MT == 4 ? 3 : 4;
+  static constexpr int kStages = NT == 4 || MT == 4 ? 2 : 3;
   static constexpr int kWarps = MT == 4 ? 4 : 8;              // of a CTA, at most
   static constexpr uint32_t kCodes = 2 * MT * 512;            // bytes of a stage, for a warp
-  static constexpr uint32_t kScales = (MT / 2) * 512;
+  static constexpr uint32_t kScaleSet = MX ? 128 : 256;       // of eight neighbouring rows
+  static constexpr uint32_t kScales = (MT / 2) * kScaleSet;
   static constexpr uint32_t kX = NT * 2048;
   static constexpr uint32_t kStage = kCodes + kScales + kX;
   static constexpr uint32_t kWarp = kStages * kStage;
@@ -139,8 +140,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 template <bool MX, int MT, int NT>
-__global__ void __launch_bounds__((W4Geo<MT, NT>::kWarps * 32)) w4_kernel(const __grid_constant__ W4Params p) {
-  using G = W4Geo<MT, NT>;
+__global__ void __launch_bounds__((W4Geo<MX, MT, NT>::kWarps * 32)) w4_kernel(const __grid_constant__ W4Params p) {
+  using G = W4Geo<MX, MT, NT>;
   constexpr int R = 2 * MT;                 // rows of a lane
   constexpr int kUnits = 128 / (16 * MT);   // units of a scale tile
   extern __shared__ __align__(16) uint8_t smem[];
@@ -149,7 +150,10 @@ __global__ void __launch_bounds__((W4Geo<MT, NT>::kWarps * 32)) w4_kernel(const 
   const int kw = warp % p.split;
   const int unit = (int)(blockIdx.x * ((blockDim.x >> 5) / p.split)) + warp / p.split;
   const int m0 = (int)blockIdx.y * 8 * NT;
-  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * G::kWarp + (uint32_t)lane * 16;
+  const uint32_t mine = smem_u32(smem) + (uint32_t)warp * G::kWarp;
+  const uint32_t ring = mine + (uint32_t)lane * 16;
+  // the scales of the lane's rows: one copy for the lanes that share them
+  const uint32_t srow = mine + G::kCodes + (uint32_t)(MX ? 0 : (t >> 1) * 128) + (uint32_t)g * 16;
   stream_order();
 
   const bool live_unit = unit < p.units;
@@ -178,9 +182,10 @@ __global__ void __launch_bounds__((W4Geo<MT, NT>::kWarps * 32)) w4_kernel(const 
         for (int r = 0; r < R; ++r) copy16(at + r * 512, code[r] + k / 2);
       }
       const int ct = min(MX ? c : 2 * c + (t >> 1), p.col_tiles - 1);
+      if (t == 0 || (!MX && t == 2))
 #pragma unroll
-      for (int h = 0; h < MT / 2; ++h)
-        copy16(at + G::kCodes + h * 512, scale + (size_t)ct * kScaleTile + h * 128);
+        for (int h = 0; h < MT / 2; ++h)
+          copy16(srow + (at - ring) + h * G::kScaleSet, scale + (size_t)ct * kScaleTile + h * 128);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int m = m0 + n * 8 + g;
@@ -223,6 +228,7 @@ __global__ void __launch_bounds__((W4Geo<MT, NT>::kWarps * 32)) w4_kernel(const 
   for (int s = 0; s < G::kStages - 1; ++s) fetch(c_lo + s);
   for (int c = c_lo; c < c_hi; ++c) {
     copy_wait<G::kStages - 2>();
+    __syncwarp();  // the scales are other lanes' copies, too
     fetch(c + G::kStages - 1);  // to where the step before this one was
     const uint32_t at = ring + (uint32_t)((c - c_lo) % G::kStages) * G::kStage;
     const bool live = c * kStep + t * 32 < p.D;
@@ -272,7 +278,7 @@ __global__ void __launch_bounds__((W4Geo<MT, NT>::kWarps * 32)) w4_kernel(const 
     uint32_t s[R][MX ? 1 : 2];
 #pragma unroll
     for (int h = 0; h < MT / 2; ++h) {
-      const uint4 v = lds16(at + G::kCodes + h * 512);
+      const uint4 v = lds16(srow + (at - ring) + h * G::kScaleSet);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__((W4Geo<MT, NT>::kWarps * 32)) w4_kernel(const 
 template <bool MX, int MT, int NT>
 cudaError_t launch_for(const W4Params& p, int warps, const dph::DeviceInfo& dev, cudaStream_t s) {
   auto kernel = w4_kernel<MX, MT, NT>;
-  using G = W4Geo<MT, NT>;
+  using G = W4Geo<MX, MT, NT>;
   if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), G::kWarps * 32,
                           (size_t)G::kWarps * G::kWarp, dev.device) < 1)
     return cudaErrorInvalidConfiguration;
