@@ -785,11 +785,16 @@ DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_f
  * the sizes; tw, the shard's tensor scale, multiplies the sum.  x holding a NaN or
  * an infinity gives that token NaN or infinities.  D == 0 writes zeros.
  * Requires D % 32 == 0, F_shard % 16 == 0, M <= 524280.
+ * workspace: device memory of dp_allgather_linear_w4_workspace_size(M, D) bytes
+ * (none for M <= 8), 16-byte aligned, any contents, overlapping nothing else; free
+ * again in stream order.
  * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
  */
+DP_API dp_status_t dp_allgather_linear_w4_workspace_size(int M, int D, size_t* bytes);
 DP_API dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
                                           const dp_mx4_t* w_shards, int K, int F_shard,
                                           dp_mx4_format_t format, void* y, dp_dtype_t y_dtype,
+                                          void* workspace, size_t workspace_bytes,
                                           dp_stream_t stream);
 
 /*

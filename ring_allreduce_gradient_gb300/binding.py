@@ -136,7 +136,8 @@ def load() -> ctypes.CDLL:
             "dp_allgather_linear_mx4_workspace_size": [i32, i32, i32,
                                                        ctypes.POINTER(ctypes.c_size_t)],
             "dp_allgather_linear_w4": [vp, i32, i32, ctypes.c_longlong, ctypes.POINTER(Mx4), i32,
-                                       i32, i32, vp, i32, vp],
+                                       i32, i32, vp, i32, vp, sz, vp],
+            "dp_allgather_linear_w4_workspace_size": [i32, i32, ctypes.POINTER(ctypes.c_size_t)],
             "dp_mx8_quantize": [vp, i32, i32, ctypes.c_longlong, i32, vp, vp, vp],
             "dp_mx8_dequantize": [vp, vp, i32, i32, vp, i32, vp],
             "dp_allgather_matmul_mx8": [ctypes.POINTER(Mx4), i32, i32, ctypes.POINTER(Mx4), i32,
@@ -650,11 +651,19 @@ def dp_allgather_linear_mx4_workspace_size(M, D, fmt) -> int:
     return int(b.value)
 
 
-def dp_allgather_linear_w4(x, M, D, ld, w_shards, K, F_shard, fmt, y, y_dtype, stream=None,
-                           check=True) -> int:
+def dp_allgather_linear_w4(x, M, D, ld, w_shards, K, F_shard, fmt, y, y_dtype, workspace=None,
+                           workspace_bytes=None, stream=None, check=True) -> int:
+    wp, wb = _ws(workspace, workspace_bytes)
     st = load().dp_allgather_linear_w4(_ptr(x), M, D, ld, _mx4_array(w_shards), K, F_shard, fmt,
-                                       _ptr(y), dtype_code(y_dtype), _stream(stream))
+                                       _ptr(y), dtype_code(y_dtype), wp, wb, _stream(stream))
     return _ret(st, "dp_allgather_linear_w4", check)
+
+
+def dp_allgather_linear_w4_workspace_size(M, D) -> int:
+    b = ctypes.c_size_t(0)
+    _ret(load().dp_allgather_linear_w4_workspace_size(M, D, ctypes.byref(b)),
+         "dp_allgather_linear_w4_workspace_size", True)
+    return int(b.value)
 
 
 def dp_mx8_quantize(x, rows, cols, ld, x_dtype, codes, scales, stream=None, check=True) -> int:

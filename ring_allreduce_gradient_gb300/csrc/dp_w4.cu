@@ -35,18 +35,29 @@
 #include "dp_mx4q.cuh"
 
 #include <algorithm>
+#include <cstdlib>
 #include <cstring>
 
+#ifndef S1
+#define S1 3
+#define S2 3
+#define S4 2
+#define SLAB 16
+#endif
 namespace {
 
 using namespace dpk;
 
 constexpr int kStep = 128;       // values of d a warp takes at once: 32 a lane
+constexpr int kRows = 32;        // rows of a warp: two instructions' 16
+constexpr int kMaxWarps = 16;    // of a CTA
+constexpr size_t kMaxSmem = 220 << 10;
 constexpr int kXRoom = 5;        // exponents that x may grow by before the sums are scaled down
 constexpr int kSRoom = 9;        // ... and mxfp4's scales
 
 struct W4Params {
-  const uint16_t* x;
+  const uint16_t* x;   // or what prepare_kernel made of it, ld elements (f16) apart
+  const int* xexp;     // ... and the exponents of its tokens
   long long ld;
   const uint8_t* codes[kMaxK];
   const uint8_t* scales[kMaxK];
@@ -55,26 +66,26 @@ struct W4Params {
   int M, D, F, F_shard;
   int tiles_f;     // 128-row scale tiles of a shard
   int col_tiles;
-  int units;       // of all shards
+  int units;       // of 32 rows, of all shards
   int split;       // warps that share a unit's d
+  int slab;        // steps of d whose x is in shared memory at once, for each share
+  int slabs;       // slabs of a share
   int x_vec;       // x's rows start on 16-byte boundaries
   int y_f32;
 };
 
-template <bool MX, int MT, int NT>
-struct W4Geo {
-  static constexpr int kStages = NT == 4 || MT == 4 ? 2 : 3;
-  static constexpr int kWarps = MT == 4 ? 4 : 8;              // of a CTA, at most
-  static constexpr uint32_t kCodes = 2 * MT * 512;            // bytes of a stage, for a warp
-  static constexpr uint32_t kScaleSet = MX ? 128 : 256;       // of eight neighbouring rows
-  static constexpr uint32_t kScales = (MT / 2) * kScaleSet;
-  static constexpr uint32_t kX = NT * 2048;
-  static constexpr uint32_t kStage = kCodes + kScales + kX;
+// Shared memory: each warp's ring of codes and scales, and two slabs of x (one, if
+// there is no other) for each share and token, rows padded so that neighbouring
+// tokens fall into other banks.
+template <bool MX, int NT>
+struct W4Ring {
+  static constexpr int kStages = NT == 1 ? S1 : NT == 2 ? S2 : S4;  // steps of codes in a warp's ring
+  static constexpr uint32_t kCodes = kRows * (kStep / 2);
+  static constexpr uint32_t kStage = kCodes + (MX ? 128 : 256);
   static constexpr uint32_t kWarp = kStages * kStage;
-  static_assert(16 * MT * 8 * NT * 4 <= kWarp, "partial sums");
-  static_assert(kWarps * kWarp <= 232448, "shared memory of a CTA");
+  static_assert(kRows * 8 * NT * 4 <= kWarp, "partial sums");
 };
-
+__host__ __device__ inline uint32_t x_row_bytes(int slab) { return (uint32_t)slab * kStep * 2 + 64; }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -87,8 +98,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
+               : "r"(a));
   return v;
 }
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
@@ -107,11 +117,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// The larger magnitude of each half (with a sign that means nothing).
-__device__ __forceinline__ uint32_t max_mag2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// The largest exponent (biased) of eight bf16 values.
+__device__ __forceinline__ int top_exponent(uint4 v) {
+  uint32_t t = max_abs2(max_abs2(max_abs2(v.x & 0x7fff7fffu, v.y), v.z), v.w);
+  t = max(t >> 16, t & 0xffffu);
+  return (int)(t >> 7);
 }
 // 2^e as fp32, for e in [-126, 127]; 0 below.
 __device__ __forceinline__ float pow2(int e) {
@@ -132,244 +142,376 @@ __device__ __forceinline__ void decode8(uint32_t c, uint32_t (&h)[4]) {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool MX, int MT, int NT>
-__global__ void __launch_bounds__((W4Geo<MX, MT, NT>::kWarps * 32)) w4_kernel(const __grid_constant__ W4Params p) {
-  using G = W4Geo<MX, MT, NT>;
-  constexpr int R = 2 * MT;                 // rows of a lane
-  constexpr int kUnits = 128 / (16 * MT);   // units of a scale tile
+// The place of 16 bytes (eight values from k on) in a slab's row: a step's sixteen
+// pieces are kept so that the four lanes of a token read 64 consecutive bytes.
+__device__ __forceinline__ uint32_t x_place(int k) {
+  const int piece = k / 8 % 16;
+  return (uint32_t)(k / kStep * 256 + piece % 4 * 64 + piece / 4 * 16);
+}
+
+// x as the products of more than eight tokens take it: f16 relative to the token's
+// largest, 2^(137 - exponent) times its values, in steps of 128 (zero past D) whose
+// pieces are in x_place's order.  A CTA for each token.
+struct XParams {
+  const uint16_t* x;
+  long long ld;
+  int D, steps;
+  int x_vec;
+  uint16_t* out;
+  int* xexp;
+};
+__device__ __forceinline__ uint4 load8(const uint16_t* x, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(x);
+  return make_uint4((uint32_t)x[0] | (uint32_t)x[1] << 16, (uint32_t)x[2] | (uint32_t)x[3] << 16,
+                    (uint32_t)x[4] | (uint32_t)x[5] << 16, (uint32_t)x[6] | (uint32_t)x[7] << 16);
+}
+__device__ __forceinline__ uint4 to_f16(uint4 v, float f) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float lo, hi;
+    unpair(mul2(pair(bf16lo(w[q]), bf16hi(w[q])), pair(f, f)), lo, hi);
+    w[q] = pack_f16x2(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+constexpr int kXThreads = 512;
+__global__ void __launch_bounds__(kXThreads) prepare_kernel(const __grid_constant__ XParams p) {
+  __shared__ int tops[kXThreads / 32];
+  stream_order();
+  const uint16_t* x = p.x + (long long)blockIdx.x * p.ld;
+  uint8_t* out = reinterpret_cast<uint8_t*>(p.out) + (size_t)blockIdx.x * p.steps * 256;
+  int e = 0;
+  for (int i = threadIdx.x; i < p.D / 8; i += kXThreads) {
+    const uint4 v = load8(x + 8ll * i, p.x_vec);
+    e = max(e, top_exponent(v));
+  }
+  e = __reduce_max_sync(0xffffffffu, e);
+  if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = e;
+  __syncthreads();
+  e = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < kXThreads / 32 ? tops[threadIdx.x & 31] : 0);
+  e = max(e, 10);
+  const float f = __uint_as_float((uint32_t)(264 - e) << 23);
+  if (threadIdx.x == 0) p.xexp[blockIdx.x] = e;
+  for (int i = threadIdx.x; i < p.steps * 16; i += kXThreads) {
+    const uint4 v = i < p.D / 8 ? to_f16(load8(x + 8ll * i, p.x_vec), f) : make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(out + (size_t)(i / 16) * 256 + x_place(i % 16 * 8)) = v;
+  }
+}
+
+template <bool MX, int NT>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_constant__ W4Params p) {
+  using G = W4Ring<MX, NT>;
+  constexpr int kStages = G::kStages;
+  constexpr bool kReady = NT > 1;  // x has been prepared
   extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int xexp[kReady ? 1 : 2][kReady ? 1 : kMaxWarps][8 * NT];  // slab, share, token
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int kw = warp % p.split;
-  const int unit = (int)(blockIdx.x * ((blockDim.x >> 5) / p.split)) + warp / p.split;
+  const int share = warp % p.split;
+  const int unit = (int)blockIdx.x * (warps / p.split) + warp / p.split;
   const int m0 = (int)blockIdx.y * 8 * NT;
+  const int tokens = min(p.M - m0, 8 * NT);
   const uint32_t mine = smem_u32(smem) + (uint32_t)warp * G::kWarp;
   const uint32_t ring = mine + (uint32_t)lane * 16;
   // the scales of the lane's rows: one copy for the lanes that share them
   const uint32_t srow = mine + G::kCodes + (uint32_t)(MX ? 0 : (t >> 1) * 128) + (uint32_t)g * 16;
-  stream_order();
+  const uint32_t xrow = x_row_bytes(p.slab);
+  const uint32_t xs = smem_u32(smem) + (uint32_t)warps * G::kWarp;
+  const auto x_at = [&](int buf, int s, int m) {
+    return xs + ((uint32_t)((buf * p.split + s) * tokens + m)) * xrow;
+  };
+  if constexpr (!kReady) {
+    for (int i = threadIdx.x; i < 2 * kMaxWarps * 8 * NT; i += blockDim.x)
+      (&xexp[0][0][0])[i] = -1000;
+    stream_order();
+  }
 
   const bool live_unit = unit < p.units;
   const int u = live_unit ? unit : 0;
-  const int tile = u / kUnits, shard = tile / p.tiles_f;
-  const int row0 = (tile - shard * p.tiles_f) * 128 + (u % kUnits) * (4 * MT);
-  const auto row_of = [&](int r) { return row0 + g + (r / 4) * 8 + (r % 4) * 32; };
-  const uint8_t* code[R];
+  const int tile = u / 4, shard = tile / p.tiles_f;
+  const int row0 = (tile - shard * p.tiles_f) * 128 + u % 4 * 8;  // rows g, + 32, + 64, + 96
+  const uint8_t* code[4];
 #pragma unroll
-  for (int r = 0; r < R; ++r)  // rows past the shard's end read its last, and are dropped
-    code[r] = p.codes[shard] + (size_t)min(row_of(r), p.F_shard - 1) * (p.D / 2) + t * 16;
+  for (int r = 0; r < 4; ++r)  // rows past the shard's end read its last, and are dropped
+    code[r] = p.codes[shard] + (size_t)min(row0 + g + 32 * r, p.F_shard - 1) * (p.D / 2) + t * 16;
   const uint8_t* scale =
       p.scales[shard] + (size_t)(row0 / 128) * p.col_tiles * kScaleTile + (row0 % 32 + g) * 16;
 
-  const int chunks = (p.D + kStep - 1) / kStep;
-  const int c_lo = live_unit ? (int)((long long)kw * chunks / p.split) : 0;
-  const int c_hi = live_unit ? (int)((long long)(kw + 1) * chunks / p.split) : 0;
+  // this share's steps of d
+  const int steps = (p.D + kStep - 1) / kStep, per = p.slabs * p.slab;
+  const int c_lo = min(share * per, steps);
+  const int c_hi = live_unit ? min(c_lo + per, steps) : c_lo;
 
+  int slot = 0;  // of the ring, for the next copy
   const auto fetch = [&](int c) {
     if (c < c_hi) {
-      const uint32_t at = ring + (uint32_t)((c - c_lo) % G::kStages) * G::kStage;
-      const bool live = c * kStep + t * 32 < p.D;
-      const int k = live ? c * kStep : 0;  // a lane past the end reads its place at the start
-      if (live || p.D > t * 32) {
+      const uint32_t at = ring + (uint32_t)slot * G::kStage;
+      if (c * kStep + t * 32 < p.D) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) copy16(at + r * 512, code[r] + k / 2);
+        for (int r = 0; r < 4; ++r) copy16(at + r * 512, code[r] + (size_t)c * (kStep / 2));
       }
       const int ct = min(MX ? c : 2 * c + (t >> 1), p.col_tiles - 1);
-      if (t == 0 || (!MX && t == 2))
-#pragma unroll
-        for (int h = 0; h < MT / 2; ++h)
-          copy16(srow + (at - ring) + h * G::kScaleSet, scale + (size_t)ct * kScaleTile + h * 128);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int m = m0 + n * 8 + g;
-        if (live && m < p.M) {
-          const uint16_t* x = p.x + (long long)m * p.ld + c * kStep + t * 32;
-          const uint32_t to = at + G::kCodes + G::kScales + n * 2048;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (p.x_vec) {
-              copy16(to + i * 512, x + 8 * i);
-            } else {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = (uint32_t)x[8 * i + 2 * e] | (uint32_t)x[8 * i + 2 * e + 1] << 16;
-              sts16(to + i * 512, make_uint4(w[0], w[1], w[2], w[3]));
-            }
-          }
-        }
-      }
+      if (t == 0 || (!MX && t == 2)) copy16(srow + (at - ring), scale + (size_t)ct * kScaleTile);
     }
     copy_commit();
+    if (++slot == kStages) slot = 0;
   };
 
-  float acc[MT][NT][4];
+  // x of one slab, a warp for each share and token: first its values as they are
+  // come to their place (cp.async), later they become f16 there, relative to the
+  // token's largest so far.  A lane takes eight values of every other step, both times.
+  const int half = lane >> 4;
+  const uint32_t piece = (uint32_t)half * 256 + x_place((lane & 15) * 8);
+  const auto each_job = [&](auto f) {
+    int s = 0, m = warp;
+    while (m >= tokens) m -= tokens, ++s;
+    while (s < p.split) {
+      f(s, m);
+      m += warps;
+      while (m >= tokens) m -= tokens, ++s;
+    }
+  };
+  const auto x_copy = [&](int slab) {
+    each_job([&](int s, int m) {
+      uint32_t to = x_at(slab & 1, s, m);
+      if constexpr (kReady) {  // whole slabs lie as they are to lie
+        const int step = s * per + slab * p.slab;
+        const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) +
+                           ((size_t)(m0 + m) * steps + min(step, steps)) * 256 + lane * 16;
+        const int n = min(p.slab, steps - step) * 256 - lane * 16;  // bytes that there are
+        to += lane * 16;
+        for (int i = 0; i < p.slab * 256 - lane * 16; i += 512, x += 512, to += 512) {
+          if (i < n)
+            copy16(to, x);
+          else
+            sts16(to, make_uint4(0u, 0u, 0u, 0u));
+        }
+      } else {
+        const int first = (s * per + slab * p.slab + half) * kStep + (lane & 15) * 8;
+        const uint16_t* x = p.x + (long long)(m0 + m) * p.ld + first;
+        to += piece;
+        for (int i = half, k = first; i < p.slab; i += 2, k += 2 * kStep, x += 2 * kStep, to += 512) {
+          if (k >= p.D)
+            sts16(to, make_uint4(0u, 0u, 0u, 0u));
+          else if (p.x_vec)
+            copy16(to, x);
+          else
+            sts16(to, load8(x, false));
+        }
+      }
+    });
+  };
+  const auto x_convert = [&](int slab) {
+    if constexpr (!kReady) {
+      const int buf = slab & 1;
+      each_job([&](int s, int m) {
+        const uint32_t row = x_at(buf, s, m) + piece;
+        int e = 0;
+        for (int i = half, o = 0; i < p.slab; i += 2, o += 512) e = max(e, top_exponent(lds16(row + o)));
+        __syncwarp();
+        e = __reduce_max_sync(0xffffffffu, e);
+        const int was = xexp[buf ^ 1][s][m];
+        const int to = e > was + kXRoom ? max(e, 10) : was;
+        const float f = __uint_as_float((uint32_t)(264 - to) << 23);  // 2^(137 - to)
+        for (int i = half, o = 0; i < p.slab; i += 2, o += 512)
+          sts16(row + o, to_f16(lds16(row + o), f));
+        __syncwarp();
+        if (lane == 0) xexp[buf][s][m] = to;
+      });
+    }
+  };
+
+  float acc[2][NT][4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
-  int xref[NT];   // the exponent (biased) of token g of each eight that goes to 2^10
-  int sref[R];    // mxfp4: the scale byte of each row that goes to 2^4
+  int xref[NT][2];  // the exponents (biased) of tokens 2t, 2t + 1 of each eight that go to 2^10
+  int sbase[4];     // mxfp4: the scale byte of each row that goes to 2^4, less 18
 #pragma unroll
-  for (int n = 0; n < NT; ++n) xref[n] = -1000;
+  for (int n = 0; n < NT; ++n) xref[n][0] = xref[n][1] = -1000;
 #pragma unroll
-  for (int r = 0; r < R; ++r) sref[r] = -1000;
+  for (int r = 0; r < 4; ++r) sbase[r] = -18;
+  // which bytes of the 16 rows' word of four are this lane's
+  const uint32_t take = MX ? 0x4440u + (uint32_t)t : t & 1 ? 0x4432u : 0x4410u;
+  const int last_step = steps - 1;
 
+  if constexpr (kReady) {
+    // The kernel before this one is prepare_kernel, which let this one start when all
+    // before it had ended: the weights may be read already, x not yet.
 #pragma unroll
-  for (int s = 0; s < G::kStages - 1; ++s) fetch(c_lo + s);
-  for (int c = c_lo; c < c_hi; ++c) {
-    copy_wait<G::kStages - 2>();
-    __syncwarp();  // the scales are other lanes' copies, too
-    fetch(c + G::kStages - 1);  // to where the step before this one was
-    const uint32_t at = ring + (uint32_t)((c - c_lo) % G::kStages) * G::kStage;
-    const bool live = c * kStep + t * 32 < p.D;
-
-    // x: 32 values of a token, as f16 relative to the token's largest so far
-    uint32_t b[NT][16];
+    for (int s = 0; s < kStages - 1; ++s) fetch(c_lo + s);
+    stream_order();
+    for (int i = threadIdx.x; i < 8 * NT; i += blockDim.x)
+      xexp[0][0][i] = i < tokens ? p.xexp[m0 + i] : 0;
+    x_copy(0);
+    copy_commit();
+    copy_wait<0>();
+  } else {
+    __syncthreads();  // xexp
+    x_copy(0);
+    copy_commit();
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(c_lo + s);
+    copy_wait<kStages - 1>();
+    x_convert(0);
+  }
+  __syncthreads();
+  if constexpr (kReady) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const bool have = live && m0 + n * 8 + g < p.M;
+      xref[n][0] = xexp[0][0][n * 8 + 2 * t];
+      xref[n][1] = xexp[0][0][n * 8 + 2 * t + 1];
+    }
+  }
+  int c = c_lo, read = 0;
+  for (int slab = 0; slab < p.slabs; ++slab) {
+    // the next slab's x is on its way while this one is worked on: its copies belong
+    // to the group of the first step's fetch, which the kStages-th step waits for
+    if (slab + 1 < p.slabs) x_copy(slab + 1);
+    const int buf = slab & 1;
+    uint32_t xtok[NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (have) v = lds16(at + G::kCodes + G::kScales + n * 2048 + i * 512);
-        b[n][4 * i] = v.x, b[n][4 * i + 1] = v.y, b[n][4 * i + 2] = v.z, b[n][4 * i + 3] = v.w;
-      }
-      uint32_t top = b[n][0];
+    for (int n = 0; n < NT; ++n) {
+      xtok[n] = x_at(buf, share, min(n * 8 + g, tokens - 1));
+      if constexpr (kReady) continue;
+      const int e0 = xexp[kReady ? 0 : buf][kReady ? 0 : share][n * 8 + 2 * t], e1 = xexp[kReady ? 0 : buf][kReady ? 0 : share][n * 8 + 2 * t + 1];
+      if (__any_sync(0xffffffffu, e0 != xref[n][0] || e1 != xref[n][1])) {
+        const float d0 = pow2(xref[n][0] - e0), d1 = pow2(xref[n][1] - e1);
+        xref[n][0] = e0;
+        xref[n][1] = e1;
 #pragma unroll
-      for (int i = 1; i < 16; ++i) top = max_mag2(top, b[n][i]);
-      int e = max((int)(top >> 23) & 255, (int)(top >> 7) & 255);
-      if (__any_sync(0xffffffffu, e > xref[n] + kXRoom)) {
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-        const int to = e > xref[n] + kXRoom ? max(e, 10) : xref[n];
-        const float down = pow2(xref[n] - to);
-        xref[n] = to;
-        const float d0 = __shfl_sync(0xffffffffu, down, 8 * t);
-        const float d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
+        for (int i = 0; i < 2; ++i) {
           acc[i][n][0] = __fmul_rn(acc[i][n][0], d0);
           acc[i][n][1] = __fmul_rn(acc[i][n][1], d1);
           acc[i][n][2] = __fmul_rn(acc[i][n][2], d0);
           acc[i][n][3] = __fmul_rn(acc[i][n][3], d1);
         }
       }
-      const float f = __uint_as_float((uint32_t)(264 - xref[n]) << 23);  // 2^(137 - xref)
-      const uint64_t ff = pair(f, f);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float lo, hi;
-        unpair(mul2(pair(bf16lo(b[n][i]), bf16hi(b[n][i])), ff), lo, hi);
-        b[n][i] = pack_f16x2(lo, hi);
-      }
     }
-
-    // the rows' scales as pairs of f16: one block (mxfp4) or two (nvfp4)
-    uint32_t s[R][MX ? 1 : 2];
-#pragma unroll
-    for (int h = 0; h < MT / 2; ++h) {
-      const uint4 v = lds16(srow + (at - ring) + h * G::kScaleSet);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * h + j;
+    for (int k = 0; k < p.slab; ++k, ++c) {
+      copy_wait<kStages - 2>();
+      __syncwarp();  // the scales are other lanes' copies, too
+      fetch(c + kStages - 1);  // to where the step before this one was
+      if (c >= c_hi) continue;  // past this share's end: only the groups go on
+      const uint32_t at = ring + (uint32_t)read * G::kStage;
+      if (++read == kStages) read = 0;
+      // the rows' scales as pairs of f16: one block (mxfp4) or two (nvfp4)
+      uint32_t s[4][MX ? 1 : 2];
+      {
+        const uint4 v = lds16(srow + (at - ring));
+        uint32_t word[4] = {v.x, v.y, v.z, v.w};
+        if (c == last_step && c * kStep + t * 32 >= p.D)  // a lane past the end: any finite ones
+          word[0] = word[1] = word[2] = word[3] = 0u;
         if constexpr (MX) {
-          s[r][0] = live ? (w[j] >> (8 * t)) & 255u : 0u;
+          // A scale relative to the row's: exponent byte - sref + 4, as f16 bits.  What
+          // f16 cannot hold takes the long way, but for byte 0 far below: that is a
+          // block of zeros, or of values below 2^-124.
+          int d[4];
+          bool far = false;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int byte = (int)__byte_perm(word[r], 0u, take);
+            d[r] = byte - sbase[r];
+            far |= (uint32_t)d[r] > kSRoom + 18u && byte != 0;
+            s[r][0] = (uint32_t)(max(d[r], -1) + 1) * 0x04000400u;
+          }
+          if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int byte = d[r] + sbase[r], sref = sbase[r] + 18;
+              int e = byte == 255 ? 0 : byte;
+              e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+              e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+              const int to = e > sref + kSRoom ? e : sref;
+              const float down = pow2(sref - to);
+              sbase[r] = to - 18;
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float* a = &acc[r / 2][n][(r % 2) * 2];
+                a[0] = __fmul_rn(a[0], down);
+                a[1] = __fmul_rn(a[1], down);
+              }
+              // 2^(byte - sref + 4): at most 2^13, below f16's smallest 0
+              const float f = __uint_as_float((uint32_t)max(byte - to + 131, 0) << 23);
+              s[r][0] = byte == 255 ? 0x7fff7fffu : pack_f16x2(f, f);
+            }
+          }
         } else {
-          const uint16_t two = live ? (uint16_t)(w[j] >> (16 * (t & 1))) : (uint16_t)0;
-          uint32_t f;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(two));
-          s[r][0] = __byte_perm(f, f, 0x1010);
-          s[r][1] = __byte_perm(f, f, 0x3232);
-        }
-      }
-    }
-    if constexpr (MX) {
-      bool above = false;
 #pragma unroll
-      for (int r = 0; r < R; ++r) above |= s[r][0] != 255u && (int)s[r][0] > sref[r] + kSRoom;
-      if (__any_sync(0xffffffffu, above)) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          int e = s[r][0] == 255u ? 0 : (int)s[r][0];
-          e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-          e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-          const int to = e > sref[r] + kSRoom ? e : sref[r];
-          const float down = pow2(sref[r] - to);
-          sref[r] = to;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float* a = &acc[r / 2][n][(r % 2) * 2];
-            a[0] = __fmul_rn(a[0], down);
-            a[1] = __fmul_rn(a[1], down);
+          for (int r = 0; r < 4; ++r) {
+            uint32_t f;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"((uint16_t)__byte_perm(word[r], 0u, take)));
+            s[r][0] = __byte_perm(f, f, 0x1010);
+            s[r][1] = __byte_perm(f, f, 0x3232);
           }
         }
       }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        // 2^(byte - sref + 4): at most 2^13, below f16's smallest 0
-        const float f = __uint_as_float((uint32_t)max((int)s[r][0] - sref[r] + 131, 0) << 23);
-        const uint32_t v = pack_f16x2(f, f);
-        s[r][0] = s[r][0] == 255u ? 0x7fff7fffu : live ? v : 0u;
-      }
-    }
 
+      uint32_t w[4][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const uint4 va = lds16(at + (2 * i) * 512), vb = lds16(at + (2 * i + 1) * 512);
-      const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+      for (int r = 0; r < 4; ++r) {
+        const uint4 v = lds16(at + r * 512);
+        w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+      }
+      const uint32_t xk = (uint32_t)(k * 256 + t * 16);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t ha[4], hb[4];
-        decode8(wa[j], ha);
-        decode8(wb[j], hb);
-        const uint32_t sa = s[2 * i][MX ? 0 : j / 2], sb = s[2 * i + 1][MX ? 0 : j / 2];
+        uint32_t h[4][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ha[e] = mul_f16x2(ha[e], sa);
-          hb[e] = mul_f16x2(hb[e], sb);
+        for (int r = 0; r < 4; ++r) {
+          decode8(w[r][j], h[r]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[r][e] = mul_f16x2(h[r][e], s[r][MX ? 0 : j / 2]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma16816(acc[i][n], ha[0], hb[0], ha[1], hb[1], b[n][4 * j], b[n][4 * j + 1]);
-          mma16816(acc[i][n], ha[2], hb[2], ha[3], hb[3], b[n][4 * j + 2], b[n][4 * j + 3]);
+          // (columns past the last token hold the last one's, and are dropped)
+          const uint4 b = lds16(xtok[n] + xk + j * 64);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma16816(acc[i][n], h[2 * i][0], h[2 * i + 1][0], h[2 * i][1], h[2 * i + 1][1], b.x, b.y);
+            mma16816(acc[i][n], h[2 * i][2], h[2 * i + 1][2], h[2 * i][3], h[2 * i + 1][3], b.z, b.w);
+          }
         }
       }
+    }
+    if (slab + 1 < p.slabs) {
+      if (p.slab < kStages) copy_wait<1>();  // (a longer slab's steps have waited for it)
+      x_convert(slab + 1);
+      __syncthreads();
     }
   }
   copy_wait<0>();
 
   // the sums as they are: back from the powers of two
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int x0 = __shfl_sync(0xffffffffu, xref[n], 8 * t);
-    const int x1 = __shfl_sync(0xffffffffu, xref[n], 8 * t + 4);
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        int to = (e & 1 ? x1 : x0) - 137;
-        if (MX) to += sref[2 * i + e / 2] - 131;
+        int to = xref[n][e & 1] - 137;
+        if (MX) to += sbase[2 * i + e / 2] + 18 - 131;
         acc[i][n][e] = ldexpf(acc[i][n][e], to);
       }
-  }
   float alpha = 1.0f;
   if constexpr (!MX)
     if (p.tw[shard]) alpha = *p.tw[shard];
-  const auto store = [&](int r, int col, float v) {  // row r of lane row g: f of the shard
+  const auto store = [&](int f, int col, float v) {  // f of the shard
     const int m = m0 + col;
-    if (r < p.F_shard && m < p.M) {
-      const size_t o = (size_t)m * p.F + (size_t)shard * p.F_shard + r;
+    if (f < p.F_shard && m < p.M) {
+      const size_t o = (size_t)m * p.F + (size_t)shard * p.F_shard + f;
       v = __fmul_rn(v, alpha);
       if (p.y_f32)
         static_cast<float*>(p.y)[o] = v;
@@ -382,10 +524,10 @@ __global__ void __launch_bounds__((W4Geo<MX, MT, NT>::kWarps * 32)) w4_kernel(co
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          store(row_of(2 * i + e / 2), n * 8 + 2 * t + (e & 1), acc[i][n][e]);
+          store(row0 + g + 32 * (2 * i + e / 2), n * 8 + 2 * t + (e & 1), acc[i][n][e]);
     return;
   }
   // partial sums [token][row of the unit], row r * 8 + g, each warp in its own ring
@@ -394,47 +536,75 @@ __global__ void __launch_bounds__((W4Geo<MX, MT, NT>::kWarps * 32)) w4_kernel(co
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        part[(n * 8 + 2 * t + (e & 1)) * (16 * MT) + (2 * i + e / 2) * 8 + g] = acc[i][n][e];
+        part[(n * 8 + 2 * t + (e & 1)) * kRows + (2 * i + e / 2) * 8 + g] = acc[i][n][e];
   __syncthreads();
   if (!live_unit) return;
-  const float* first = reinterpret_cast<const float*>(smem + (size_t)(warp - kw) * G::kWarp);
-  for (int i = kw * 32 + lane; i < 16 * MT * 8 * NT; i += p.split * 32) {
+  const float* first = reinterpret_cast<const float*>(smem + (size_t)(warp - share) * G::kWarp);
+  for (int i = share * 32 + lane; i < kRows * 8 * NT; i += p.split * 32) {
     float v = first[i];
     for (int k = 1; k < p.split; ++k) v = __fadd_rn(v, first[(size_t)k * (G::kWarp / 4) + i]);
-    const int r = i % (16 * MT);
-    store(row0 + r % 8 + (r / 32) * 8 + (r / 8 % 4) * 32, i / (16 * MT), v);
+    store(row0 + i % 8 + i % kRows / 8 * 32, i / kRows, v);
   }
 }
 
-template <bool MX, int MT, int NT>
-cudaError_t launch_for(const W4Params& p, int warps, const dph::DeviceInfo& dev, cudaStream_t s) {
-  auto kernel = w4_kernel<MX, MT, NT>;
-  using G = W4Geo<MX, MT, NT>;
-  if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), G::kWarps * 32,
-                          (size_t)G::kWarps * G::kWarp, dev.device) < 1)
+constexpr int kMaxTokens = 65535 * 8;  // the grid's second dimension
+constexpr int kOwnTokens = 8;          // of a call whose kernel makes f16 of x itself
+
+
+template <bool MX, int NT>
+cudaError_t launch_for(W4Params p, const dph::DeviceInfo& dev, cudaStream_t s) {
+  // Many units: one CTA an SM (or as many rounds of them as it takes), each warp
+  // its own unit, x shared by all.  Few: d is split over warps, up to 16 an SM,
+  // while each share has a step and x fits.
+  const int steps = (p.D + kStep - 1) / kStep, tokens = std::min(p.M, 8 * NT);
+  size_t smem = 0;
+  int warps = 0, per = 0;
+  const int fs = getenv("FSPLIT") ? atoi(getenv("FSPLIT")) : 0, fu = getenv("FUNITS") ? atoi(getenv("FUNITS")) : 0;
+  for (p.split = kMaxWarps; p.split >= 1; p.split /= 2) {
+    if (fs && p.split != fs) continue;
+    if (p.split > 1 && (p.split > steps || (long long)p.units * p.split > 16ll * dev.sm_count))
+      continue;
+    const long long all = (long long)p.units * p.split, full = 16ll * dev.sm_count;
+    const long long ctas = (all + full - 1) / full * dev.sm_count;
+    per = (int)((p.units + ctas - 1) / ctas);  // units of a CTA
+    per = std::max(1, std::min(per, kMaxWarps / p.split));
+    if (fu) per = fu;
+    warps = per * p.split;
+    const int share = (steps + p.split - 1) / p.split;
+    // slabs of 16 steps: longer ones are staged too long before the first step
+    for (p.slab = std::min(SLAB, share);; p.slab = (p.slab + 1) / 2) {
+      p.slabs = (share + p.slab - 1) / p.slab;
+      smem = (size_t)warps * W4Ring<MX, NT>::kWarp +
+             (size_t)(p.slabs > 1 ? 2 : 1) * p.split * tokens * x_row_bytes(p.slab);
+      if (smem <= kMaxSmem || p.slab <= 4) break;
+    }
+    if (smem <= kMaxSmem) break;
+  }
+  auto kernel = w4_kernel<MX, NT>;
+  if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kMaxWarps * 32, kMaxSmem,
+                          dev.device) < 1)
     return cudaErrorInvalidConfiguration;
-  const int per = warps / p.split;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((p.units + per - 1) / per), (unsigned)((p.M + 8 * NT - 1) / (8 * NT)));
   cfg.blockDim = dim3((unsigned)warps * 32);
-  cfg.dynamicSmemBytes = (size_t)warps * G::kWarp;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <bool MX, int MT>
-cudaError_t launch_w4(const W4Params& p, int warps, const dph::DeviceInfo& dev, cudaStream_t s) {
-  if (p.M <= 8) return launch_for<MX, MT, 1>(p, warps, dev, s);
-  if (p.M <= 16) return launch_for<MX, MT, 2>(p, warps, dev, s);
-  return launch_for<MX, MT, 4>(p, warps, dev, s);
+template <bool MX>
+cudaError_t launch_w4(const W4Params& p, const dph::DeviceInfo& dev, cudaStream_t s) {
+  if (p.M <= kOwnTokens) return launch_for<MX, 1>(p, dev, s);
+  if (p.M <= 16) return launch_for<MX, 2>(p, dev, s);
+  return launch_for<MX, 4>(p, dev, s);
 }
 
 using dph::aligned;
@@ -442,16 +612,25 @@ using dph::clash;
 using dph::Span;
 using dph::span_of;
 
-constexpr int kMaxTokens = 65535 * 8;  // the grid's second dimension
+size_t prepared_bytes(int M, int D) { return (size_t)M * (((size_t)D + kStep - 1) / kStep) * 256; }
 
 }  // namespace
 
 extern "C" {
 
+dp_status_t dp_allgather_linear_w4_workspace_size(int M, int D, size_t* bytes) {
+  if (!bytes) return DP_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (M < 0 || D < 0) return DP_ERR_INVALID_ARG;
+  if (M > kMaxTokens || D > 0x7fffff00) return DP_ERR_UNSUPPORTED;
+  if (M > kOwnTokens && D) *bytes = prepared_bytes(M, D) + (size_t)M * sizeof(int);
+  return DP_OK;
+}
+
 dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
                                    const dp_mx4_t* w_shards, int K, int F_shard,
                                    dp_mx4_format_t format, void* y, dp_dtype_t y_dtype,
-                                   dp_stream_t stream) {
+                                   void* workspace, size_t workspace_bytes, dp_stream_t stream) {
   dph::NvtxRange nvtx_range("dp_allgather_linear_w4");
   if (!w_shards || K < 1 || K > DP_MAX_K) return DP_ERR_INVALID_ARG;
   if (M < 0 || D < 0 || F_shard < 0 || ld < D) return DP_ERR_INVALID_ARG;
@@ -465,9 +644,14 @@ dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
   const int F = K * F_shard;
   if (M == 0 || F == 0) return DP_OK;
   if (!y || (!x && D)) return DP_ERR_INVALID_ARG;
+  size_t need = 0;
+  dp_allgather_linear_w4_workspace_size(M, D, &need);
+  if (need && (!workspace || workspace_bytes < need)) return DP_ERR_INVALID_ARG;
+  if (need && !aligned(workspace, 16)) return DP_ERR_UNSUPPORTED;
+  const Span ws = span_of(workspace, need);
   const Span out = span_of(y, (size_t)M * F * ysz);
-  if (D && clash(out, span_of(x, ((size_t)(M - 1) * (size_t)ld + (size_t)D) * 2)))
-    return DP_ERR_ALIAS;
+  const Span xs = span_of(x, D ? ((size_t)(M - 1) * (size_t)ld + (size_t)D) * 2 : 0);
+  if (clash(out, xs) || clash(ws, xs) || clash(ws, out)) return DP_ERR_ALIAS;
   size_t sbytes = 0;
   dp_mx4_scales_size(F_shard, D, format, &sbytes);
   W4Params p;
@@ -478,10 +662,10 @@ dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
     if ((!w.codes || !w.scales) && D) return DP_ERR_INVALID_ARG;
     if (!aligned(w.codes, 16) || !aligned(w.scales, 16) || !aligned(w.tensor_scale, 4))
       return DP_ERR_UNSUPPORTED;
-    if (clash(out, span_of(w.codes, (size_t)F_shard * (D / 2))) ||
-        clash(out, span_of(w.scales, sbytes)) ||
-        (w.tensor_scale && clash(out, span_of(w.tensor_scale, 4))))
-      return DP_ERR_ALIAS;
+    const Span of[3] = {span_of(w.codes, (size_t)F_shard * (D / 2)), span_of(w.scales, sbytes),
+                        span_of(w.tensor_scale, w.tensor_scale ? 4 : 0)};
+    for (const Span& o : of)
+      if (clash(out, o) || clash(ws, o)) return DP_ERR_ALIAS;
     p.codes[k] = static_cast<const uint8_t*>(w.codes);
     p.scales[k] = static_cast<const uint8_t*>(w.scales);
     p.tw[k] = w.tensor_scale;
@@ -499,21 +683,17 @@ dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
   p.col_tiles = mx4_col_tiles(D, mx4_block(format));
   p.x_vec = aligned(x, 16) && ld % 8 == 0;
   p.y_f32 = y_dtype == DP_FP32;
-  // Rows of a warp and the warps that share them: 64 rows (x is converted once
-  // for all of them) while they make 8 warps an SM with d in four shares, else 32;
-  // d in as many shares, up to a CTA's warps, as have a step each.
-  const int chunks = (D + kStep - 1) / kStep;
-  const long long tiles = (long long)K * p.tiles_f;
-  const bool wide = tiles * 2 * 4 >= 8ll * dev.sm_count;
-  p.units = (int)std::min<long long>(tiles * (wide ? 2 : 4), 0x7fffffffll);
-  p.split = wide ? 4 : 8;
-  while (p.split > chunks) p.split /= 2;
-  const int warps = p.split < 4 ? 4 : p.split;
-  cudaError_t e;
-  if (format == DP_MXFP4)
-    e = wide ? launch_w4<true, 4>(p, warps, dev, s) : launch_w4<true, 2>(p, warps, dev, s);
-  else
-    e = wide ? launch_w4<false, 4>(p, warps, dev, s) : launch_w4<false, 2>(p, warps, dev, s);
+  p.units = (int)((long long)K * p.tiles_f * 4);
+  cudaError_t e = cudaSuccess;
+  if (need) {
+    XParams q{p.x, ld, D, (D + kStep - 1) / kStep, p.x_vec, static_cast<uint16_t*>(workspace),
+              reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + prepared_bytes(M, D))};
+    e = dph::launch_early(prepare_kernel, q, (unsigned)M, kXThreads, s);
+    p.x = q.out;
+    p.xexp = q.xexp;
+  }
+  if (e == cudaSuccess)
+    e = format == DP_MXFP4 ? launch_w4<true>(p, dev, s) : launch_w4<false>(p, dev, s);
   return e == cudaSuccess ? DP_OK : DP_ERR_CUDA;
 }
 

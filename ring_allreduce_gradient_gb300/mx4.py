@@ -285,9 +285,14 @@ def linear_w4(x: torch.Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) ->
     F, _, format, _ = w_shards[0]._kind
     arr = _shards(w_shards, D, format, dev)
     y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
+    ws, nbytes = None, 0
+    if M > 8:
+        # scratch of this call alone: the allocator hands it on in stream order
+        nbytes = B.dp_allgather_linear_w4_workspace_size(M, D)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     st = (B._lib or B.load()).dp_allgather_linear_w4(
         x.data_ptr(), M, D, ld, arr, K, F, FORMATS[format], y.data_ptr(), _DT[y_dtype],
-        B._stream_on(dev, "linear_w4"))
+        None if ws is None else ws.data_ptr(), nbytes, B._stream_on(dev, "linear_w4"))
     if st:
         raise B.DpError(st, "dp_allgather_linear_w4")
     return y

@@ -167,8 +167,11 @@ def test_nothing_else_is_written_and_streams_and_graphs():
     want = mx4.linear_w4(x, s)
     torch.cuda.synchronize()
     buf = torch.full((M * F * 2 + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+    need = B.dp_allgather_linear_w4_workspace_size(M, D)
+    ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=DEV)
     B.dp_allgather_linear_w4(x, M, D, D, [q._c for q in s], 2, F // 2, B.DP_NVFP4,
-                             buf.data_ptr() + 256, B.DP_BF16)
+                             buf.data_ptr() + 256, B.DP_BF16, ws.data_ptr() + 256, need)
+    assert (ws[:256] == 0xA5).all() and (ws[-256:] == 0xA5).all()
     assert (buf[:256] == 0xA5).all() and (buf[-256:] == 0xA5).all()
     assert torch.equal(buf[256:-256].view(torch.bfloat16).view(M, F), want)
     side = torch.cuda.Stream()
@@ -185,12 +188,16 @@ def test_nothing_else_is_written_and_streams_and_graphs():
     assert torch.equal(y, mx4.linear_w4(x, s)) and torch.equal(y.float(), want.float() * 2)
 
 
-def test_same_bits_as_one_token_at_a_time():
-    """Tokens in one call are the tokens alone: each is scaled by itself.  (The instruction's
-    columns do not meet; the shares of d are those of the same rule.)"""
+def test_tokens_do_not_meet():
+    """Each token is scaled by itself: tokens of one call, in another order and among others of
+    other magnitudes, keep their bits."""
     D, F = 1024, 96
     s = shards_of(normal((F, D), 1), 1, "mxfp4")
-    x = (normal((30, D), 2) * torch.exp2(10 * normal((30, 1), 3))).bfloat16()
-    all_at_once = mx4.linear_w4(x, s, torch.float32)
-    for i in (0, 7, 8, 29):
-        assert torch.equal(mx4.linear_w4(x[i:i + 1], s, torch.float32), all_at_once[i:i + 1])
+    for M in (8, 30):
+        x = (normal((M, D), 2) * torch.exp2(10 * normal((M, 1), 3))).bfloat16()
+        y = mx4.linear_w4(x, s, torch.float32)
+        order = torch.randperm(M, device=DEV)
+        assert torch.equal(mx4.linear_w4(x[order].contiguous(), s, torch.float32), y[order])
+        x2 = (normal((M, D), 5) * 1e4).bfloat16()
+        x2[3] = x[5]
+        assert torch.equal(mx4.linear_w4(x2, s, torch.float32)[3], y[5])

@@ -1,4 +1,6 @@
 """Refusals of the few-token product and of the products of 8-bit x, made on the host before any device call."""
+import ctypes
+
 import pytest
 import torch
 
@@ -22,11 +24,13 @@ def lib():
     return B.load()
 
 
-def test_checks():
+def test_checks(lib):
     ws = [(fake(2 * k + 2), fake(2 * k + 3), None) for k in range(2)]
 
-    def m(x=fake(0), M=4, D=64, ld=64, w=ws, K=2, Fs=32, fmt=MX, y=fake(20), dt=B.DP_BF16):
-        return B.dp_allgather_linear_w4(x, M, D, ld, w, K, Fs, fmt, y, dt, stream=0, check=False)
+    def m(x=fake(0), M=4, D=64, ld=64, w=ws, K=2, Fs=32, fmt=MX, y=fake(20), dt=B.DP_BF16,
+          work=None, wb=0):
+        return B.dp_allgather_linear_w4(x, M, D, ld, w, K, Fs, fmt, y, dt, work, wb, stream=0,
+                                        check=False)
 
     assert m(K=0) == INVALID and m(K=17) == INVALID
     assert m(M=-1) == INVALID and m(D=-32) == INVALID and m(Fs=-16) == INVALID
@@ -45,6 +49,20 @@ def test_checks():
     assert m(y=fake(0)) == ALIAS and m(y=fake(2, 16)) == ALIAS and m(y=fake(5, 16)) == ALIAS
     assert m(fmt=NV, w=[(fake(2), fake(3), fake(20, 4)), ws[1]]) == ALIAS
     assert m(M=0, y=None) == OK and m(Fs=0, y=None) == OK
+    # more than eight tokens are prepared in a workspace
+    size = B.dp_allgather_linear_w4_workspace_size
+    assert size(8, 64) == 0 and size(9, 0) == 0 and size(9, 64) == 9 * 256 + 9 * 4
+    assert size(20, 160) == 20 * 512 + 20 * 4
+    need = size(9, 64)
+    assert m(M=9) == INVALID and m(M=9, work=fake(30), wb=need - 1) == INVALID
+    assert m(M=9, work=fake(30, 8), wb=need) == UNSUPPORTED
+    for at in (fake(0, 16), fake(20), fake(2), fake(5)):
+        assert m(M=9, work=at, wb=need) == ALIAS
+    assert m(M=9, fmt=NV, w=[(fake(2), fake(3), fake(30, 64)), ws[1]], work=fake(30),
+             wb=need) == ALIAS
+    n = ctypes.c_size_t(3)
+    assert lib.dp_allgather_linear_w4_workspace_size(1, 1, None) == INVALID
+    assert lib.dp_allgather_linear_w4_workspace_size(-1, 1, ctypes.byref(n)) == INVALID
 
 
 def test_the_helper_checks():
