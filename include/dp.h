@@ -777,8 +777,8 @@ DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_f
  * x [M, D] bf16, rows ld elements apart, any alignment (fastest where rows start
  * on 16-byte boundaries); w_shards, K, F_shard, format and y as for
  * dp_allgather_matmul_mx4, y of any alignment.  For the single tokens of a model
- * that is served: it reads the weights once for each 32 tokens, and is bound by
- * that up to about 32; for many tokens the products of quantised x are faster.
+ * that is served: it reads the weights once for each 32 tokens; for more tokens the
+ * products of quantised x are faster.
  * Weights are decoded exactly; x is exact down to 2^-27 of its row's largest
  * magnitude, and below it within 2^-35 of that magnitude (mxfp4: weights likewise,
  * within a row of w); products are summed in fp32, in an order that follows from

@@ -4,10 +4,10 @@
 //
 // With one token, or a few, the product is bound by the weights' bytes, so they
 // go from memory to the tensor core with as little in between as possible:
-//   * A warp takes 16 MT weight rows and its share of d, 128 at a time.  A lane
-//     copies 16 bytes (32 values: whole blocks) of each of its 2 MT rows to its
-//     own place in shared memory (cp.async, several steps ahead) and later reads
-//     the same bytes back: no barrier, and no register waits for memory.
+//   * A warp takes 32 weight rows and d, or its share of it, 128 values at a time.
+//     A lane copies 16 bytes (32 values: whole blocks) of each of its four rows to
+//     its own place in shared memory (cp.async, two steps ahead) and later reads the
+//     same bytes back: no barrier, and no register waits for memory.
 //   * Eight codes become four pairs of f16 (one conversion each), which one
 //     multiplication by the block's scale makes the exact weight: e2m1 has two
 //     significant bits, e4m3 four.  As bf16 the decoding takes 23 instructions
@@ -15,19 +15,34 @@
 //     they arrive (measured in registers: 4.7 against 10.6 words a clock; 5.1
 //     arrive).
 //   * mma.sync m16n8k16 with the weights as the 16 rows: one to eight tokens are
-//     one instruction's eight columns.  Which d a lane's values stand for does not
-//     matter as long as x comes in the same order, so both stay as they lie.
-//   * The rows of a warp are g, g + 32, g + 64, g + 96 of a 128-row scale tile (g
-//     of eight neighbours): their scales are one 16-byte word.
+//     one instruction's eight columns (2.15 clocks each on an SM).  Which d a lane's
+//     values stand for does not matter as long as x comes in the same order.
+//   * The rows of a lane are g, g + 32, g + 64, g + 96 of a 128-row scale tile:
+//     their scales are one 16-byte word.
+//   * x is staged as f16 for all warps of a CTA, a slab of d at a time.  More than
+//     eight tokens are made f16 by a small kernel beforehand, and come by bulk
+//     copies: made by every CTA, they took more instructions than the weights.
 // f16 has less range than bf16 and 2^k scales.  So x is multiplied by a power of
-// two that takes its largest magnitude seen so far to about 2^10, and mxfp4's
-// scales are taken relative to the largest of the row so far; where a larger one
-// comes by more than the headroom, the sums are multiplied down first.  A value
-// of x loses bits only below 2^-27 of that token's largest (and is then off by at
-// most 2^-35 of it), a weight below 2^-27 of its row's.  Sums are fp32.
+// two that takes its largest magnitude (up to eight tokens: the largest so far) to
+// about 2^10, and mxfp4's scales are taken relative to the largest of the row so
+// far; where a larger one comes by more than the headroom, the sums are multiplied
+// down first.  A value of x loses bits only below 2^-27 of that token's largest (and
+// is then off by at most 2^-35 of it), a weight below 2^-27 of its row's.  Sums are
+// fp32.
 //
 // Few rows: d is split over the warps of a CTA, whose partial sums meet in shared
 // memory and are added in order.
+//
+// Measured (GB300, launches in a CUDA graph), w[65536,8192]: one token 58 us in
+// either form (5.2 TB/s of weights in nvfp4), eight 65 us, 16 70 us in mxfp4, 32 112
+// us; 4096 x 4096: one token 7.5 us, 16 8.5 us.  What bounds it: 256 instructions a
+// step of 2 KB, with 3.5 warps to a scheduler (2048 units of 32 rows on 608
+// schedulers), of which four must wait for the slowest: 46 % of the issue slots are
+// used, 55 % of DRAM.  Above 16 tokens the MMAs: 138 clocks of a step for 32, and 87
+// at which its bytes arrive.  Rings of 4 or 5 steps gained nothing.  The steps that
+// led here: x converted by each warp for itself 83 us (one token, nvfp4) and 138 us
+// (16, mxfp4); rings half as large, twice the warps 69 and 128; x staged for the
+// CTA 59 and 91; x prepared beforehand 70 (16).
 
 #include "dp_early.cuh"
 #include "dp_launch.h"
@@ -35,15 +50,8 @@
 #include "dp_mx4q.cuh"
 
 #include <algorithm>
-#include <cstdlib>
 #include <cstring>
 
-#ifndef S1
-#define S1 3
-#define S2 3
-#define S4 2
-#define SLAB 16
-#endif
 namespace {
 
 using namespace dpk;
@@ -51,6 +59,7 @@ using namespace dpk;
 constexpr int kStep = 128;       // values of d a warp takes at once: 32 a lane
 constexpr int kRows = 32;        // rows of a warp: two instructions' 16
 constexpr int kMaxWarps = 16;    // of a CTA
+constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr size_t kMaxSmem = 220 << 10;
 constexpr int kXRoom = 5;        // exponents that x may grow by before the sums are scaled down
 constexpr int kSRoom = 9;        // ... and mxfp4's scales
@@ -72,6 +81,7 @@ struct W4Params {
   int slabs;       // slabs of a share
   int x_vec;       // x's rows start on 16-byte boundaries
   int y_f32;
+  unsigned* err;
 };
 
 // Shared memory: each warp's ring of codes and scales, and two slabs of x (one, if
@@ -79,7 +89,7 @@ struct W4Params {
 // tokens fall into other banks.
 template <bool MX, int NT>
 struct W4Ring {
-  static constexpr int kStages = NT == 1 ? S1 : NT == 2 ? S2 : S4;  // steps of codes in a warp's ring
+  static constexpr int kStages = NT == 4 ? 2 : 3;              // steps of codes in a warp's ring
   static constexpr uint32_t kCodes = kRows * (kStep / 2);
   static constexpr uint32_t kStage = kCodes + (MX ? 128 : 256);
   static constexpr uint32_t kWarp = kStages * kStage;
@@ -206,12 +216,12 @@ __global__ void __launch_bounds__(kXThreads) prepare_kernel(const __grid_constan
   }
 }
 
-template <bool MX, int NT>
+template <bool MX, int NT, bool kReady>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_constant__ W4Params p) {
   using G = W4Ring<MX, NT>;
   constexpr int kStages = G::kStages;
-  constexpr bool kReady = NT > 1;  // x has been prepared
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t xfull[2], xfree[2];  // (x prepared: a slab has landed, has been read)
   __shared__ int xexp[kReady ? 1 : 2][kReady ? 1 : kMaxWarps][8 * NT];  // slab, share, token
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -280,32 +290,38 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
     }
   };
   const auto x_copy = [&](int slab) {
+    if constexpr (kReady) {
+      // whole slabs lie as they are to lie: a lane has one copied (what the share has
+      // of it, which is all that is read)
+      const int q = warp + lane * warps, s = q / tokens, m = q - s * tokens;
+      const int step = s * per + slab * p.slab;
+      const uint32_t n =
+          s < p.split ? (uint32_t)max(0, min(p.slab, steps - step)) * 256u : 0u;
+      const uint32_t all = __reduce_add_sync(0xffffffffu, n);
+      uint64_t* bar = &xfull[slab & 1];
+      if (lane == 0) mbar_arrive_expect_tx(bar, all);
+      __syncwarp();
+      if (n)
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+                "r"(x_at(slab & 1, s, m)),
+            "l"(reinterpret_cast<const uint8_t*>(p.x) + ((size_t)(m0 + m) * steps + step) * 256),
+            "r"(n), "r"(smem_u32(bar))
+            : "memory");
+      return;
+    }
     each_job([&](int s, int m) {
       uint32_t to = x_at(slab & 1, s, m);
-      if constexpr (kReady) {  // whole slabs lie as they are to lie
-        const int step = s * per + slab * p.slab;
-        const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) +
-                           ((size_t)(m0 + m) * steps + min(step, steps)) * 256 + lane * 16;
-        const int n = min(p.slab, steps - step) * 256 - lane * 16;  // bytes that there are
-        to += lane * 16;
-        for (int i = 0; i < p.slab * 256 - lane * 16; i += 512, x += 512, to += 512) {
-          if (i < n)
-            copy16(to, x);
-          else
-            sts16(to, make_uint4(0u, 0u, 0u, 0u));
-        }
-      } else {
-        const int first = (s * per + slab * p.slab + half) * kStep + (lane & 15) * 8;
-        const uint16_t* x = p.x + (long long)(m0 + m) * p.ld + first;
-        to += piece;
-        for (int i = half, k = first; i < p.slab; i += 2, k += 2 * kStep, x += 2 * kStep, to += 512) {
-          if (k >= p.D)
-            sts16(to, make_uint4(0u, 0u, 0u, 0u));
-          else if (p.x_vec)
-            copy16(to, x);
-          else
-            sts16(to, load8(x, false));
-        }
+      const int first = (s * per + slab * p.slab + half) * kStep + (lane & 15) * 8;
+      const uint16_t* x = p.x + (long long)(m0 + m) * p.ld + first;
+      to += piece;
+      for (int i = half, k = first; i < p.slab; i += 2, k += 2 * kStep, x += 2 * kStep, to += 512) {
+        if (k >= p.D)
+          sts16(to, make_uint4(0u, 0u, 0u, 0u));
+        else if (p.x_vec)
+          copy16(to, x);
+        else
+          sts16(to, load8(x, false));
       }
     });
   };
@@ -354,9 +370,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
     stream_order();
     for (int i = threadIdx.x; i < 8 * NT; i += blockDim.x)
       xexp[0][0][i] = i < tokens ? p.xexp[m0 + i] : 0;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&xfull[i], warps);
+        mbar_init(&xfree[i], warps);
+      }
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     x_copy(0);
-    copy_commit();
-    copy_wait<0>();
   } else {
     __syncthreads();  // xexp
     x_copy(0);
@@ -365,8 +387,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
     for (int s = 0; s < kStages - 1; ++s) fetch(c_lo + s);
     copy_wait<kStages - 1>();
     x_convert(0);
+    __syncthreads();
   }
-  __syncthreads();
   if constexpr (kReady) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -378,8 +400,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
   for (int slab = 0; slab < p.slabs; ++slab) {
     // the next slab's x is on its way while this one is worked on: its copies belong
     // to the group of the first step's fetch, which the kStages-th step waits for
-    if (slab + 1 < p.slabs) x_copy(slab + 1);
+    if (!kReady && slab + 1 < p.slabs) x_copy(slab + 1);
     const int buf = slab & 1;
+    if constexpr (kReady)
+      (void)mbar_wait_bounded(&xfull[buf], (uint32_t)(slab >> 1) & 1u, p.err, kTimeoutNs);
     uint32_t xtok[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -403,6 +427,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
       copy_wait<kStages - 2>();
       __syncwarp();  // the scales are other lanes' copies, too
       fetch(c + kStages - 1);  // to where the step before this one was
+      if (kReady && k == p.slab / 2 && slab + 1 < p.slabs) {
+        // every warp is done with the slab before this one: the next takes its place
+        if (slab > 0)
+          (void)mbar_wait_bounded(&xfree[buf ^ 1], (uint32_t)((slab - 1) >> 1) & 1u, p.err,
+                                  kTimeoutNs);
+        __syncwarp();
+        x_copy(slab + 1);
+      }
       if (c >= c_hi) continue;  // past this share's end: only the groups go on
       const uint32_t at = ring + (uint32_t)read * G::kStage;
       if (++read == kStages) read = 0;
@@ -487,9 +519,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
       }
     }
     if (slab + 1 < p.slabs) {
-      if (p.slab < kStages) copy_wait<1>();  // (a longer slab's steps have waited for it)
-      x_convert(slab + 1);
-      __syncthreads();
+      if constexpr (kReady) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xfree[buf]);
+      } else {
+        if (p.slab < kStages) copy_wait<1>();  // (a longer slab's steps have waited for it)
+        x_convert(slab + 1);
+        __syncthreads();
+      }
     }
   }
   copy_wait<0>();
@@ -554,7 +591,7 @@ constexpr int kMaxTokens = 65535 * 8;  // the grid's second dimension
 constexpr int kOwnTokens = 8;          // of a call whose kernel makes f16 of x itself
 
 
-template <bool MX, int NT>
+template <bool MX, int NT, bool READY>
 cudaError_t launch_for(W4Params p, const dph::DeviceInfo& dev, cudaStream_t s) {
   // Many units: one CTA an SM (or as many rounds of them as it takes), each warp
   // its own unit, x shared by all.  Few: d is split over warps, up to 16 an SM,
@@ -562,28 +599,30 @@ cudaError_t launch_for(W4Params p, const dph::DeviceInfo& dev, cudaStream_t s) {
   const int steps = (p.D + kStep - 1) / kStep, tokens = std::min(p.M, 8 * NT);
   size_t smem = 0;
   int warps = 0, per = 0;
-  const int fs = getenv("FSPLIT") ? atoi(getenv("FSPLIT")) : 0, fu = getenv("FUNITS") ? atoi(getenv("FUNITS")) : 0;
   for (p.split = kMaxWarps; p.split >= 1; p.split /= 2) {
-    if (fs && p.split != fs) continue;
     if (p.split > 1 && (p.split > steps || (long long)p.units * p.split > 16ll * dev.sm_count))
       continue;
     const long long all = (long long)p.units * p.split, full = 16ll * dev.sm_count;
     const long long ctas = (all + full - 1) / full * dev.sm_count;
     per = (int)((p.units + ctas - 1) / ctas);  // units of a CTA
     per = std::max(1, std::min(per, kMaxWarps / p.split));
-    if (fu) per = fu;
     warps = per * p.split;
     const int share = (steps + p.split - 1) / p.split;
-    // slabs of 16 steps: longer ones are staged too long before the first step
-    for (p.slab = std::min(SLAB, share);; p.slab = (p.slab + 1) / 2) {
-      p.slabs = (share + p.slab - 1) / p.slab;
-      smem = (size_t)warps * W4Ring<MX, NT>::kWarp +
-             (size_t)(p.slabs > 1 ? 2 : 1) * p.split * tokens * x_row_bytes(p.slab);
-      if (smem <= kMaxSmem || p.slab <= 4) break;
+    // Slabs as long as fit; where the kernel makes f16 of x itself, 64 steps of all
+    // tokens at most (longer ones are staged too long before the first step).
+    const size_t ring = (size_t)warps * W4Ring<MX, NT>::kWarp;
+    const auto fits = [&](int slabs, int slab) {
+      smem = ring + (size_t)(slabs > 1 ? 2 : 1) * p.split * tokens * x_row_bytes(slab);
+      return smem <= kMaxSmem && (READY || slabs == share || slab <= std::max(16, 64 / tokens));
+    };
+    for (p.slabs = 1;; ++p.slabs) {
+      p.slab = (share + p.slabs - 1) / p.slabs;
+      if (fits(p.slabs, p.slab) || p.slab <= 2) break;
     }
+    p.slabs = (share + p.slab - 1) / p.slab;
     if (smem <= kMaxSmem) break;
   }
-  auto kernel = w4_kernel<MX, NT>;
+  auto kernel = w4_kernel<MX, NT, READY>;
   if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kMaxWarps * 32, kMaxSmem,
                           dev.device) < 1)
     return cudaErrorInvalidConfiguration;
@@ -602,9 +641,9 @@ cudaError_t launch_for(W4Params p, const dph::DeviceInfo& dev, cudaStream_t s) {
 
 template <bool MX>
 cudaError_t launch_w4(const W4Params& p, const dph::DeviceInfo& dev, cudaStream_t s) {
-  if (p.M <= kOwnTokens) return launch_for<MX, 1>(p, dev, s);
-  if (p.M <= 16) return launch_for<MX, 2>(p, dev, s);
-  return launch_for<MX, 4>(p, dev, s);
+  if (p.M <= kOwnTokens) return launch_for<MX, 1, false>(p, dev, s);
+  if (p.M <= 16) return launch_for<MX, 2, true>(p, dev, s);
+  return launch_for<MX, 4, true>(p, dev, s);
 }
 
 using dph::aligned;
@@ -683,6 +722,7 @@ dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
   p.col_tiles = mx4_col_tiles(D, mx4_block(format));
   p.x_vec = aligned(x, 16) && ld % 8 == 0;
   p.y_f32 = y_dtype == DP_FP32;
+  p.err = dev.err_word;
   p.units = (int)((long long)K * p.tiles_f * 4);
   cudaError_t e = cudaSuccess;
   if (need) {
