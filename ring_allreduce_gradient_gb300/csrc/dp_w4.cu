@@ -35,14 +35,14 @@
 //
 // Measured (GB300, launches in a CUDA graph), w[65536,8192]: one token 58 us in
 // either form (5.2 TB/s of weights in nvfp4), eight 65 us, 16 70 us in mxfp4, 32 112
-// us; 4096 x 4096: one token 7.5 us, 16 8.5 us.  What bounds it: 256 instructions a
-// step of 2 KB, with 3.5 warps to a scheduler (2048 units of 32 rows on 608
-// schedulers), of which four must wait for the slowest: 46 % of the issue slots are
-// used, 55 % of DRAM.  Above 16 tokens the MMAs: 138 clocks of a step for 32, and 87
-// at which its bytes arrive.  Rings of 4 or 5 steps gained nothing.  The steps that
-// led here: x converted by each warp for itself 83 us (one token, nvfp4) and 138 us
-// (16, mxfp4); rings half as large, twice the warps 69 and 128; x staged for the
-// CTA 59 and 91; x prepared beforehand 70 (16).
+// us; 4096 x 4096: one token 7.5 us, 16 8.5 us.  What bounds it: one token's bytes
+// alone (no decoding, no products) take 52 us and its instructions alone (the same
+// codes again and again) 50; 16 tokens' instructions 66; 32 tokens' MMAs 138 clocks
+// of a step, against the 87 in which its bytes arrive.  Neither rings of 4 or 5 steps
+// nor 28 warps of 72 registers gained anything.  The steps that led here: x
+// converted by each warp for itself 83 us (one token, nvfp4) and 138 us (16, mxfp4);
+// rings half as large, twice the warps 69 and 128; x staged for the CTA 59 and 91; x
+// prepared beforehand 70 (16).
 
 #include "dp_early.cuh"
 #include "dp_launch.h"

@@ -81,8 +81,10 @@ def quantize(x: torch.Tensor, stream=None) -> Mx8Tensor:
     code = _code(x)
     q = Mx8Tensor._empty(rows, cols, x.device)
     c = q._c
-    B.dp_mx8_quantize(x, rows, cols, ld, code, c.codes, c.scales,
-                      stream=B._stream_on(x.device, "quantize"))
+    st = (B._lib or B.load()).dp_mx8_quantize(x.data_ptr(), rows, cols, ld, code, c.codes,
+                                              c.scales, B._stream_on(x.device, "quantize"))
+    if st:
+        raise B.DpError(st, "dp_mx8_quantize")
     return q
 
 
@@ -95,8 +97,11 @@ def dequantize(q: Mx8Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}")
     out = torch.empty((rows, cols), dtype=dtype, device=dev)
-    B.dp_mx8_dequantize(q._c.codes, q._c.scales, rows, cols, out, _DT[dtype],
-                        stream=B._stream_on(dev, "dequantize"))
+    c = q._c
+    st = (B._lib or B.load()).dp_mx8_dequantize(c.codes, c.scales, rows, cols, out.data_ptr(),
+                                                _DT[dtype], B._stream_on(dev, "dequantize"))
+    if st:
+        raise B.DpError(st, "dp_mx8_dequantize")
     return out
 
 

@@ -13,6 +13,7 @@ PyTorch and calls the binding.
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -32,6 +33,9 @@ class Normed(NamedTuple):
     h: torch.Tensor
     rstd: torch.Tensor
     q: Mx4Tensor | Mx8Tensor | None
+
+
+_workspace_size = lru_cache(256)(B.dp_rms_norm_backward_workspace_size)   # of (M, D) alone
 
 
 def _weight(weight, cols, device):
@@ -114,7 +118,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     dx = torch.empty((M, D), dtype=h.dtype, device=dev)
     dw = torch.empty(D, dtype=torch.float32, device=dev)
     # scratch of this call alone: the allocator hands it on in stream order
-    n = B.dp_rms_norm_backward_workspace_size(M, D)
+    n = _workspace_size(M, D)
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     st = (B._lib or B.load()).dp_rms_norm_backward(
         ys.data_ptr(), ldy, hs.data_ptr(), ldh, None if ds is None else ds.data_ptr(), ldd, M, D,
