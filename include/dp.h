@@ -784,7 +784,7 @@ DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_f
  * within a row of w); products are summed in fp32, in an order that follows from
  * the sizes; tw, the shard's tensor scale, multiplies the sum.  x holding a NaN or
  * an infinity gives that token NaN or infinities.  D == 0 writes zeros.
- * Requires D % 32 == 0, F_shard % 16 == 0, M <= 524280.
+ * Requires D % 32 == 0, D <= 2^30, F_shard % 16 == 0, M <= 524280.
  * workspace: device memory of dp_allgather_linear_w4_workspace_size(M, D) bytes
  * (none for M <= 8), 16-byte aligned, any contents, overlapping nothing else; free
  * again in stream order.

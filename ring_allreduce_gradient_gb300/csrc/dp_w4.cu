@@ -588,6 +588,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
 }
 
 constexpr int kMaxTokens = 65535 * 8;  // the grid's second dimension
+constexpr int kMaxD = 1 << 30;         // a share's last slab, past D, still has int positions
 constexpr int kOwnTokens = 8;          // of a call whose kernel makes f16 of x itself
 
 
@@ -661,7 +662,7 @@ dp_status_t dp_allgather_linear_w4_workspace_size(int M, int D, size_t* bytes) {
   if (!bytes) return DP_ERR_INVALID_ARG;
   *bytes = 0;
   if (M < 0 || D < 0) return DP_ERR_INVALID_ARG;
-  if (M > kMaxTokens || D > 0x7fffff00) return DP_ERR_UNSUPPORTED;
+  if (M > kMaxTokens || D > kMaxD) return DP_ERR_UNSUPPORTED;
   if (M > kOwnTokens && D) *bytes = prepared_bytes(M, D) + (size_t)M * sizeof(int);
   return DP_OK;
 }
@@ -676,7 +677,7 @@ dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
   if (format != DP_MXFP4 && format != DP_NVFP4) return DP_ERR_UNSUPPORTED;
   if (y_dtype != DP_FP32 && y_dtype != DP_BF16) return DP_ERR_UNSUPPORTED;
   if (D % 32 || F_shard % 16) return DP_ERR_UNSUPPORTED;
-  if ((long long)K * F_shard > 0x7fffff00ll || M > kMaxTokens || D > 0x7fffff00)
+  if ((long long)K * F_shard > 0x7fffff00ll || M > kMaxTokens || D > kMaxD)
     return DP_ERR_UNSUPPORTED;
   const size_t ysz = y_dtype == DP_FP32 ? 4 : 2;
   if (!aligned(x, 2) || !aligned(y, ysz)) return DP_ERR_UNSUPPORTED;

@@ -33,7 +33,7 @@ class Mx8Tensor:
         if scales.device != codes.device:
             raise ValueError("codes and scales on one device")
         self._store, self._codes, self._scales = None, codes, scales
-        self._kind = (rows, cols, codes.device)
+        self._kind = (rows, cols, "mxfp8", codes.device)
         self._c = B.Mx4(codes.data_ptr(), scales.data_ptr(), None)
 
     @classmethod
@@ -44,7 +44,7 @@ class Mx8Tensor:
         q._store = torch.empty(n + _scale_bytes(rows, cols, "mxfp4"), dtype=torch.uint8,
                                device=device)
         q._codes = q._scales = None      # views, made when they are asked for
-        q._kind = (rows, cols, device)
+        q._kind = (rows, cols, "mxfp8", device)
         at = q._store.data_ptr()
         q._c = B.Mx4(at, at + n, None)
         return q
@@ -64,8 +64,8 @@ class Mx8Tensor:
 
     rows = property(lambda self: self._kind[0])
     cols = property(lambda self: self._kind[1])
-    format = property(lambda self: "mxfp8")
-    device = property(lambda self: self._kind[2])
+    format = property(lambda self: self._kind[2])
+    device = property(lambda self: self._kind[3])
 
     def __repr__(self):
         return f"Mx8Tensor({self.rows} x {self.cols}, {self.device})"
@@ -90,7 +90,9 @@ def quantize(x: torch.Tensor, stream=None) -> Mx8Tensor:
 
 def dequantize(q: Mx8Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values an 8-bit matrix stands for."""
-    rows, cols, dev = q._kind
+    rows, cols, format, dev = q._kind
+    if format != "mxfp8":
+        raise ValueError(f"need an mxfp8 matrix, not {q!r}")
     if stream is not None:
         with _on(stream, dev):
             return dequantize(q, dtype)
@@ -107,7 +109,9 @@ def dequantize(q: Mx8Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
 
 def matmul(x: Mx8Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = x . w^T with w the row concatenation of the mxfp4 shards."""
-    M, D, dev = x._kind
+    M, D, format, dev = x._kind
+    if format != "mxfp8":
+        raise ValueError(f"need an mxfp8 matrix, not {x!r}")
     if stream is not None:
         with _on(stream, dev):
             return matmul(x, w_shards, y_dtype)

@@ -229,6 +229,60 @@ def test_quantised(M, D, dtype, fmt):
     forward(x, w.bfloat16(), None, fmt, None, keep=True)
 
 
+@pytest.mark.parametrize("fmt", [None, "mxfp4", "nvfp4", "mxfp8"])
+@pytest.mark.parametrize("M,D,dtype", [(2600, 4096, torch.bfloat16), (2433, 2080, torch.float32),
+                                       (19500, 64, torch.bfloat16), (40001, 32, torch.float32),
+                                       (2440, 8192, torch.bfloat16), (2440, 9216, torch.float32),
+                                       (2500, 16384, torch.bfloat16), (7300, 1120, torch.bfloat16)])
+def test_many_rows(M, D, dtype, fmt):
+    """Enough rows that they come by bulk copies, several to a CTA, with and without a residual."""
+    rng = np.random.default_rng(M)
+    x, res = matrix(rng, M, D, dtype, ld=D + 16), matrix(rng, M, D, dtype)
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(D)).float().to(DEV)
+    t = torch.tensor([0.004], device=DEV) if fmt == "nvfp4" else None
+    a = norm.rms_norm(x, w, residual=res, eps=EPS, format=fmt, tensor_scale=t, keep=True)
+    b = norm.rms_norm(res, w, eps=EPS, format=fmt, tensor_scale=t)
+    some = torch.from_numpy(np.unique(np.concatenate(
+        [rng.integers(0, M, 40), np.arange(8), np.arange(M - 20, M)]))).to(DEV)
+    # rows do not depend on one another: a few of them, checked as a small call's are
+    one = forward(x[some], w, res[some], fmt, t, keep=True)
+    two = forward(res[some], w, None, fmt, t)
+    for big, small in ((a, one), (b, two)):
+        assert torch.equal(big.rstd[some], small.rstd) and torch.equal(big.h[some], small.h)
+        if small.y is not None:
+            assert torch.equal(big.y[some], small.y)
+        if fmt:
+            assert torch.equal(decoded(big.q)[some], decoded(small.q))
+    # and all of them against the formula, in fp32 on the GPU (its own error: 64 u)
+    h = (x.float() + res.float()).to(dtype)
+    assert torch.equal(a.h, h)
+    want = torch.rsqrt(h.float().square().mean(1) + EPS)
+    assert bool(((a.rstd - want).abs() <= 64 * U * want).all())
+    want = h.float() * want[:, None] * w
+    assert bool(((a.y.float() - want).abs() <= (96 * U + 1.01 * HALF[dtype]) * want.abs()).all())
+    if fmt:
+        assert scale_bytes(a.q)[1] and scale_bytes(b.q)[1]
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows are those of a small call."""
+    M, D = 66000, 32768
+    x = torch.empty(M, D, dtype=torch.bfloat16, device=DEV)
+    x[:-300] = 1
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x[-300:] = torch.randn(300, D, device=DEV, generator=g).bfloat16()
+    w = torch.ones(D, device=DEV)
+    n = norm.rms_norm(x, w, format="mxfp8", keep=True)
+    small = norm.rms_norm(x[-300:].clone(), w, format="mxfp8", keep=True)
+    assert torch.equal(n.y[-300:], small.y) and torch.equal(n.rstd[-300:], small.rstd)
+    assert torch.equal(n.q.codes[-300:], small.q.codes)
+    assert bool((n.y[:-300] == 1).all())
+    del n
+    dx, dw = norm.rms_norm_backward(x, x, w, torch.ones(M, device=DEV))
+    d1, _ = norm.rms_norm_backward(x[-300:].clone(), x[-300:].clone(), w, torch.ones(300, device=DEV))
+    assert torch.equal(dx[-300:], d1)
+
+
 @pytest.mark.parametrize("ld,off", [(64, 0), (96, 0), (65, 0), (64, 1), (100, 7)])
 @pytest.mark.parametrize("fmt", [None, "mxfp8", "nvfp4"])
 def test_strides_and_alignment(ld, off, fmt):
@@ -310,7 +364,8 @@ def backward(dy, h, w, rstd, dh):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,D", [(1, 1), (1, 64), (3, 17), (128, 512), (457, 513), (1031, 1024),
                                  (500, 1601), (459, 2048), (1000, 4096), (13, 8192), (11, 16384),
-                                 (5, 32767), (3, 32768), (5000, 96)])
+                                 (5, 32767), (3, 32768), (5000, 96), (700, 2048), (400, 8192),
+                                 (400, 16384), (200, 32768)])
 def test_backward(M, D, dtype):
     rng = np.random.default_rng(M + D)
     h, dy, dh = (matrix(rng, M, D, dtype) for _ in range(3))
@@ -361,7 +416,7 @@ def test_gradient_against_differences():
 def test_same_bits_under_any_cta_limit():
     rng = np.random.default_rng(4)
     saved = B.dp_get_cta_limits()
-    for M, D in ((700, 512), (700, 4096), (3, 9000)):
+    for M, D in ((700, 512), (700, 4096), (3, 9000), (2600, 4096), (20000, 96)):
         x, dy = matrix(rng, M, D, torch.bfloat16), matrix(rng, M, D, torch.bfloat16)
         w = torch.ones(D, device=DEV)
         fmt = "mxfp8" if D % 32 == 0 else None

@@ -148,7 +148,50 @@ def test_strides_and_alignment():
         v = buf[off:off + 6 * ld].view(6, ld)[:, :D]
         v.copy_(x)
         assert torch.equal(mx4.linear_w4(v, s), want)
-    assert torch.equal(mx4.linear_w4(x[:1].expand(9, D), s), want[:1].expand(9, F))
+    many = normal((19, D), 3).bfloat16()          # prepared beforehand
+    want = mx4.linear_w4(many, s)
+    for ld, off in ((D + 8, 0), (D + 1, 0), (D, 1), (D + 4, 4)):
+        buf = torch.full((off + 19 * ld + 8,), float("nan"), dtype=torch.bfloat16, device=DEV)
+        v = buf[off:off + 19 * ld].view(19, ld)[:, :D]
+        v.copy_(many)
+        assert torch.equal(mx4.linear_w4(v, s), want)
+    one = mx4.linear_w4(many[:1].expand(9, D), s)
+    assert torch.equal(one, one[:1].expand(9, F))
+
+
+def test_offsets_past_32_bits():
+    """A shard of more than 4 GB: its last rows are those of a shard of these rows alone."""
+    D, F, last = 16384, 524288 + 256, 256
+    g = torch.Generator(device=DEV).manual_seed(4)
+    codes = torch.randint(0, 256, (F, D // 2), dtype=torch.uint8, device=DEV, generator=g)
+    tiles = D // 128 * 512
+    scales = torch.randint(118, 131, (F // 128 * tiles,), dtype=torch.uint8, device=DEV, generator=g)
+    big = mx4.Mx4Tensor(codes, scales, F, D, "mxfp4")
+    end = mx4.Mx4Tensor(codes[-last:].clone(), scales[-last // 128 * tiles:].clone(), last, D, "mxfp4")
+    for M in (1, 10):
+        x = normal((M, D), M).bfloat16()
+        y = mx4.linear_w4(x, [big], torch.float32)[:, -last:]
+        want = check(x, [end])
+        # d is split otherwise there, so the sums come in another order: each is within
+        # 2 (D + 8) 2^-24 of the sum of magnitudes of the exact one (see above), and the
+        # two within twice that of one another
+        size = x.double().abs() @ mx4.dequantize(end, torch.float32).double().abs().t()
+        assert bool(((y - want).double().abs() <= 4 * (D + 8) * U * size).all())
+        # rows of another place would be off by the size of y itself
+        assert bool(((y - want).abs() <= 1e-2 * want.abs().amax()).all())
+
+
+def test_two_calls_at_once():
+    D, F = 1024, 4096
+    s = shards_of(normal((F, D), 1), 4, "nvfp4")
+    xs = [normal((M, D), M).bfloat16() for M in (3, 12, 30)]
+    want = [mx4.linear_w4(x, s) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(10):
+        got = [mx4.linear_w4(x, s, stream=st) for x, st in zip(xs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_empty():

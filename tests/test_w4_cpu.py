@@ -40,6 +40,7 @@ def test_checks(lib):
     assert m(w=[ws[0], (fake(4), fake(5), fake(9))]) == INVALID    # a tensor scale with mxfp4
     assert m(fmt=2) == UNSUPPORTED and m(dt=5) == UNSUPPORTED
     assert m(D=48, ld=48) == UNSUPPORTED and m(Fs=24) == UNSUPPORTED
+    assert m(D=(1 << 30) + 32, ld=(1 << 30) + 32) == UNSUPPORTED
     assert m(M=65535 * 8 + 1) == UNSUPPORTED and m(K=16, w=ws * 8, Fs=0x8000000) == UNSUPPORTED
     assert m(x=fake(0, 1)) == UNSUPPORTED and m(y=fake(20, 1)) == UNSUPPORTED
     assert m(y=fake(20, 2), dt=B.DP_FP32) == UNSUPPORTED
@@ -124,6 +125,17 @@ def test_the_eight_bit_helpers_check():
                                 ((a, [w]), B.DpError, "not the current CUDA device")]:
             with pytest.raises(err, match=word):
                 call(*args)
+    # 4-bit matrices where 8-bit ones belong, and the other way round: their buffers differ in size
+    w8 = mx8.Mx8Tensor(u8(16 * 64), u8(512), 16, 64)
+    for call in (lambda: mx8.matmul(w, [w]), lambda: mx8.dequantize(w), lambda: mx8.linear(x, [w8]),
+                 lambda: mx4.matmul(q, [w]), lambda: mx4.matmul(w, [w8]),
+                 lambda: mx8.matmul(q, [w8])):
+        with pytest.raises(ValueError, match="mxfp"):
+            call()
+    for call in (lambda: mx4.dequantize(q), lambda: mx4.linear(x, [w8]), lambda: mx4.matmul(q, [w8]),
+                 lambda: mx4.linear_w4(x, [w8])):
+        with pytest.raises(KeyError, match="mxfp8"):
+            call()
     with pytest.raises(TypeError, match="dtype"):
         mx8.linear(x.half(), [w])
     with pytest.raises(ValueError, match="columns"):
