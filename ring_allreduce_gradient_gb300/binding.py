@@ -135,15 +135,14 @@ def load() -> ctypes.CDLL:
                                         ctypes.POINTER(Mx4), i32, i32, i32, vp, i32, vp, sz, vp],
             "dp_allgather_linear_mx4_workspace_size": [i32, i32, i32,
                                                        ctypes.POINTER(ctypes.c_size_t)],
-            "dp_allgather_linear_w4": [vp, i32, i32, ctypes.c_longlong, ctypes.POINTER(Mx4), i32,
-                                       i32, i32, vp, i32, vp, sz, vp],
+            "dp_allgather_linear_w4": [vp, i32, i32, ctypes.c_longlong, vp, i32, i32, i32, vp, i32,
+                                       vp, sz, vp],
             "dp_allgather_linear_w4_workspace_size": [i32, i32, ctypes.POINTER(ctypes.c_size_t)],
             "dp_mx8_quantize": [vp, i32, i32, ctypes.c_longlong, i32, vp, vp, vp],
             "dp_mx8_dequantize": [vp, vp, i32, i32, vp, i32, vp],
-            "dp_allgather_matmul_mx8": [ctypes.POINTER(Mx4), i32, i32, ctypes.POINTER(Mx4), i32,
-                                        i32, vp, i32, vp],
-            "dp_allgather_linear_mx8": [vp, i32, i32, ctypes.c_longlong, i32, ctypes.POINTER(Mx4),
-                                        i32, i32, vp, i32, vp, sz, vp],
+            "dp_allgather_matmul_mx8": [vp, i32, i32, vp, i32, i32, vp, i32, vp],
+            "dp_allgather_linear_mx8": [vp, i32, i32, ctypes.c_longlong, i32, vp, i32, i32, vp, i32,
+                                        vp, sz, vp],
             "dp_allgather_linear_mx8_workspace_size": [i32, i32, ctypes.POINTER(ctypes.c_size_t)],
             "dp_rms_norm": [vp, ctypes.c_longlong, vp, ctypes.c_longlong, i32, i32, i32, vp, i32,
                             f32, vp, vp, vp, i32, vp, vp, vp, vp],
@@ -620,8 +619,9 @@ def dp_mx4_dequantize(codes, scales, rows, cols, fmt, tensor_scale, out, out_dty
 
 
 def _mx4_array(items):
-    """``items``: Mx4 structures, (codes, scales, tensor_scale) triples, or a ctypes array."""
-    if isinstance(items, ctypes.Array):
+    """``items``: Mx4 structures, (codes, scales, tensor_scale) triples, a ctypes array, or the
+    structures' bytes one after another (for the calls that take those)."""
+    if isinstance(items, (ctypes.Array, bytes)):
         return items
     return (Mx4 * max(1, len(items)))(*[t if type(t) is Mx4 else Mx4(*[_ptr(v) for v in t])
                                         for t in items])

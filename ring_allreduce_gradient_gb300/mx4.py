@@ -41,7 +41,7 @@ class Mx4Tensor:
     ``tensor_scale``: one fp32 device value or None (nvfp4 only).
     """
 
-    __slots__ = ("_codes", "_scales", "_store", "_tensor_scale", "_kind", "_c")
+    __slots__ = ("_codes", "_scales", "_store", "_tensor_scale", "_kind", "_c", "_bytes")
 
     def __init__(self, codes, scales, rows: int, cols: int, format: str, tensor_scale=None):
         _format(format)
@@ -72,6 +72,14 @@ class Mx4Tensor:
         at = q._store.data_ptr()
         q._c = B.Mx4(at, at + n, None if tensor_scale is None else tensor_scale.data_ptr())
         return q
+
+    def _c_bytes(self):
+        """``_c`` as bytes: it does not change, so they are made once."""
+        try:
+            return self._bytes
+        except AttributeError:
+            self._bytes = bytes(self._c)
+            return self._bytes
 
     @property
     def codes(self):
@@ -215,6 +223,22 @@ def _shards(w_shards, cols, format, device):
     return (B.Mx4 * len(w_shards))(*[w._c for w in w_shards])
 
 
+def _shard_bytes(w_shards, cols, format, device):
+    """The shards' structures as bytes, after the same checks: a third of the time of an array."""
+    if not w_shards:
+        raise ValueError("need at least one shard")
+    w0 = w_shards[0]
+    kind = (w0._kind[0], cols, format, device)
+    if w0._kind != kind:
+        raise ValueError(f"x is {format} with {cols} columns on {device}, the shards {w0!r}")
+    parts = []
+    for w in w_shards:
+        if w._kind != kind:
+            raise ValueError("need shards of one shape, format and device")
+        parts.append(w._c_bytes())
+    return b"".join(parts)
+
+
 def matmul(x: Mx4Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = x . w^T with w the row concatenation of the 4-bit shards."""
     M, D, format, dev = x._kind
@@ -283,7 +307,8 @@ def linear_w4(x: torch.Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) ->
         raise ValueError("need at least one shard")
     dev, K = x.device, len(w_shards)
     F, _, format, _ = w_shards[0]._kind
-    arr = _shards(w_shards, D, format, dev)
+    fmt = FORMATS[format]
+    arr = _shard_bytes(w_shards, D, format, dev)
     y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
     ws, nbytes = None, 0
     if M > 8:
@@ -291,7 +316,7 @@ def linear_w4(x: torch.Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) ->
         nbytes = B.dp_allgather_linear_w4_workspace_size(M, D)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     st = (B._lib or B.load()).dp_allgather_linear_w4(
-        x.data_ptr(), M, D, ld, arr, K, F, FORMATS[format], y.data_ptr(), _DT[y_dtype],
+        x.data_ptr(), M, D, ld, arr, K, F, fmt, y.data_ptr(), _DT[y_dtype],
         None if ws is None else ws.data_ptr(), nbytes, B._stream_on(dev, "linear_w4"))
     if st:
         raise B.DpError(st, "dp_allgather_linear_w4")

@@ -11,11 +11,13 @@ No arithmetic happens here: it allocates with PyTorch and calls the binding.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import binding as B
 from .collectives import _DT, _code
-from .mx4 import _on, _rows, _scale_bytes, _shards
+from .mx4 import _on, _rows, _scale_bytes, _shard_bytes
 
 
 class Mx8Tensor:
@@ -117,11 +119,14 @@ def matmul(x: Mx8Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch
             return matmul(x, w_shards, y_dtype)
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
-    arr = _shards(w_shards, D, "mxfp4", dev)
+    arr = _shard_bytes(w_shards, D, "mxfp4", dev)
     K, F = len(w_shards), w_shards[0].rows
     y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
-    B.dp_allgather_matmul_mx8(x._c, M, D, arr, K, F, y, _DT[y_dtype],
-                              stream=B._stream_on(dev, "matmul"))
+    st = (B._lib or B.load()).dp_allgather_matmul_mx8(
+        ctypes.byref(x._c), M, D, arr, K, F, y.data_ptr(), _DT[y_dtype],
+        B._stream_on(dev, "matmul"))
+    if st:
+        raise B.DpError(st, "dp_allgather_matmul_mx8")
     return y
 
 
@@ -136,7 +141,7 @@ def linear(x: torch.Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> to
     if y_dtype not in _DT:
         raise TypeError(f"unsupported dtype {y_dtype}")
     dev, code = x.device, _code(x)
-    arr = _shards(w_shards, D, "mxfp4", dev)
+    arr = _shard_bytes(w_shards, D, "mxfp4", dev)
     K, F = len(w_shards), w_shards[0].rows
     here = B._stream_on(dev, "linear")
     # scratch of this call alone: the allocator hands it on in stream order
