@@ -788,7 +788,8 @@ DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_f
  * workspace: device memory of dp_allgather_linear_w4_workspace_size(M, D) bytes
  * (none for M <= 8), 16-byte aligned, any contents, overlapping nothing else; free
  * again in stream order.
- * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA;
+ * DP_ERR_TIMEOUT later from dp_get_device_error if the wait for a copy expired.
  */
 DP_API dp_status_t dp_allgather_linear_w4_workspace_size(int M, int D, size_t* bytes);
 DP_API dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
@@ -852,8 +853,9 @@ DP_API dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* 
  * format, codes and scales of y as dp_mx4_quantize (tensor_scale: nvfp4's, or
  * NULL for 1) and dp_mx8_quantize define them, from the unrounded y.  y may then
  * be NULL; without a format codes and scales are.
- * Arithmetic in fp32: squares are summed 16 or 32 to a thread in order, the rest
- * pairwise; magnitudes above 1.8e19 make the mean infinite, and then y is 0.  A
+ * Arithmetic in fp32: a thread sums 16 or 32 squares in four chains, the rest is
+ * pairwise (the same bits for a row in any call, but for rows that start off 32-byte
+ * boundaries); magnitudes above 1.8e19 make the mean infinite, and then y is 0.  A
  * row with a NaN is NaN throughout.
  * Requires D <= 32768, and D % 32 == 0 with a format; eps >= 0 and finite.
  *
@@ -869,7 +871,8 @@ DP_API dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* 
  * workspace: device memory of dp_rms_norm_backward_workspace_size(M, D) bytes,
  * 32-byte aligned, any contents; free again in stream order.
  * Nothing that is written may overlap anything else.
- * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA.
+ * Errors: DP_ERR_INVALID_ARG, DP_ERR_UNSUPPORTED, DP_ERR_ALIAS, DP_ERR_CUDA;
+ * DP_ERR_TIMEOUT later from dp_get_device_error if the wait for a copy expired.
  */
 DP_API dp_status_t dp_rms_norm(const void* x, long long ldx, const void* residual, long long ldr,
                                int M, int D, dp_dtype_t dtype, const void* weight,

@@ -1,5 +1,5 @@
 // dp_mx4mm.cu -- the FSDP forward's parameter all-gather fused into the local
-// matmul, with both operands in microscaled 4-bit form:
+// matmul, with both operands in microscaled 4-bit form, or x in 8 bits (below):
 //   y[m, f] = tx * tw * sum_d sx[m, b(d)] x[m, d] * sw[f, b(d)] w[f, d]
 // x, w: e2m1 values; sx, sw: their blocks' scales (b(d) = d / 32 for mxfp4,
 // d / 16 for nvfp4); tx, tw: the tensors' fp32 scales (nvfp4).  The tensor
@@ -44,6 +44,20 @@
 //     233 -> 216 and 225 -> 195 us;
 //   * output through 4 KiB of shared memory a half and TMA instead of 4-byte
 //     stores, which held the MMA issuer up for half a tile.
+//
+// With x in 8 bits (e4m3, blocks of 32) and mxfp4 weights the MMA is the 8-bit kind,
+// 32 values of d at a time: a stage is 128 values, of the same 128 bytes a row, and
+// has a quarter of a scale tile a step.  That kind wants each sixteen 4-bit values in
+// the first half of 16 bytes: TMA spreads them so (and counts the bytes that it
+// read), where rows are whole 128 values and 32-byte aligned; else warp 0 copies
+// them, 8 bytes a lane, and warp 3 hands a landed stage on to the MMA's proxy.
+// Measured: x[8192,4096] . w[4096,4096]^T 83-85 us (3.3 PFLOP/s; 76 % of the tensor
+// pipe, 62 % of L2), with all loads left out 76; x[8192,8192] . w[8192,8192]^T 360.
+// What bounds it is the intake, 40 KiB for the 512 clocks that a stage's MMAs take,
+// and the MMAs.  All weights by warp 0's copies: 105 us (their half-used lines do
+// not stay in the L1 that is left beside the stages).  One token times
+// w[65536,8192] 66 us, and without any load 65: an MMA takes 64 clocks to issue
+// however narrow it is, so tiles are not narrower than 64 tokens.
 //
 // Few tiles: the blocks of d are split over a cluster of 2, 4 or 8 CTAs,
 // whose fp32 partial sums meet in shared memory: each CTA adds a share of the

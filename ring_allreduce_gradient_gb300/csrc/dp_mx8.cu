@@ -4,7 +4,9 @@
 //
 // Bound by memory: 2 bytes read and 1.03 written for each bf16 value, and back.
 // A warp takes G x 512 columns of a row with all its loads issued first, a lane
-// sixteen columns of each 512, so a block is two lanes.
+// sixteen columns of each 512, so a block is two lanes.  Measured on 8192 x 4096 bf16
+// (GB300, launches in a CUDA graph): quantisation 16.5 us (102 MB: 6.2 TB/s),
+// decoding 13.0 (7.8 TB/s, part of it from L2).
 
 #include "dp_early.cuh"
 #include "dp_launch.h"
