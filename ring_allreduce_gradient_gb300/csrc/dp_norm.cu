@@ -20,17 +20,18 @@
 // by bulk copies.  Arithmetic is in pairs of fp32, one instruction each.
 //
 // Measured (GB300, launches in a CUDA graph, inputs larger than L2), 8192 x 4096
-// bf16: forward with residual to 8 bits 39.5 us (236 MB: 6.0 TB/s; 58 % of the
-// issue slots), backward with dh 44.7 us with the sum over 304 sets of rows (268 MB:
-// 6.0 TB/s, 75 % of DRAM under the profiler).  One row of 4096: 2.4 us, 2050 x 1120
-// to nvfp4 9.5 (first loads, and the two divisors of each block of 16), backward of
-// 1031 x 1601 fp32 12 us (scalar accesses).  What led there: a CTA for each row with
-// scalar fp32 arithmetic 49 and 101 us; pairs of fp32 and add.bf16x2 took the
-// forward from 34 to 25 instructions an element; a thread's own 16-byte cp.async
-// pieces touched every sector twice (61 and 87 us); rows ahead in registers spilled
-// (backward 72 us); bulk copies with 2 stages and turns of 6 sets forward (3 stages
-// 41 us, whole share of the GPU in one turn 40.4), 3 stages and 128 registers
-// backward (80 registers, three CTAs an SM, spill: 60; 456 sets of rows 55.7).
+// bf16: forward with residual to 8 bits 39.4 us (236 MB: 6.0 TB/s; 58 % of the
+// issue slots), backward with dh 45 us with the sum over 304 sets of rows (268 MB:
+// 6.0 TB/s, 75 % of DRAM under the profiler).  One row of 4096: 2.1 us, 1000 x 768
+// fp32 4.9, 2050 x 1120 to nvfp4 8.9 (first loads, and the two divisors of each block
+// of 16), backward of 1031 x 1601 fp32 11 us (scalar accesses).  What led there: a CTA
+// for each row with scalar fp32 arithmetic 49 and 101 us; pairs of fp32 and
+// add.bf16x2 took the forward from 34 to 25 instructions an element; a thread's own
+// 16-byte cp.async pieces touched every sector twice (61 and 87 us); rows ahead in
+// registers spilled (backward 72 us); bulk copies with 2 stages and turns of 6 sets
+// forward (3 stages 41 us, the whole share of the GPU in one turn 40.4), 3 stages and
+// 128 registers backward (80 registers, three CTAs an SM, spill: 60; 456 sets of rows
+// 55.7).
 
 #include "dp_early.cuh"
 #include "dp_launch.h"
@@ -151,19 +152,23 @@ __device__ __forceinline__ void load_row(const T* p, bool in, const Place& at, H
   for (int g = 0; g < G; ++g) {
     const int e = at.group(g);
     uint32_t* r = v.r + g * kWords;
-    if (in && at.vec && e < at.D) {
+    if (at.vec) {  // (lanes past the row's end only take zeros, not the other way round)
 #pragma unroll
-      for (int h = 0; h < kWords; h += 8)
-        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[h]), "=r"(r[h + 1]), "=r"(r[h + 2]), "=r"(r[h + 3]), "=r"(r[h + 4]),
-                       "=r"(r[h + 5]), "=r"(r[h + 6]), "=r"(r[h + 7])
-                     : "l"(reinterpret_cast<const uint32_t*>(p + e) + h));
+      for (int h = 0; h < kWords; ++h) r[h] = 0u;
+      if (in && e < at.D) {
+#pragma unroll
+        for (int h = 0; h < kWords; h += 8)
+          asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                       : "=r"(r[h]), "=r"(r[h + 1]), "=r"(r[h + 2]), "=r"(r[h + 3]), "=r"(r[h + 4]),
+                         "=r"(r[h + 5]), "=r"(r[h + 6]), "=r"(r[h + 7])
+                       : "l"(reinterpret_cast<const uint32_t*>(p + e) + h));
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
         const int a = at.element(16 * g + i), b = at.element(16 * g + i + 1);
-        v.put(8 * g + i / 2, pair(in && !at.vec && a < at.D ? widen_scalar(p, a) : 0.0f,
-                                  in && !at.vec && b < at.D ? widen_scalar(p, b) : 0.0f));
+        v.put(8 * g + i / 2, pair(in && a < at.D ? widen_scalar(p, a) : 0.0f,
+                                  in && b < at.D ? widen_scalar(p, b) : 0.0f));
       }
     }
   }
@@ -379,21 +384,24 @@ __device__ __forceinline__ void quantise_row(const NormFwdParams& p, int r, cons
 }
 
 template <typename T, int FMT, int THREADS, int G, bool BULK>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BULK ? 3 : 4) : 1)
     norm_fwd_kernel(const __grid_constant__ NormFwdParams p) {
   __shared__ float part[2][THREADS / 32];
   stream_order();
   const int threads = p.plan.warps * 32, sub = (int)threadIdx.x / threads;
   const Place at{(int)threadIdx.x - sub * threads, threads, sub, p.D, p.plan.vec != 0,
                  FMT != kPlain || p.plan.vec != 0};
-  const float tscale = FMT == kToNv4 && p.tscale ? *p.tscale : 1.0f;
-  const Divisor by_t(tscale);
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[BULK ? 8 * kMaxStages : 1];
   Ring<T, G, 2> ring;
   if constexpr (BULK) ring.init(smem, bars, p.plan, sub, p.D, p.res ? 2 : 1, p.err);
+  // What all rows share.  It is asked for after the first row: unpacking it would
+  // hold the row's loads up for as long as it takes to come (2050 x 1120 to nvfp4 9.5
+  // -> 8.7 us).
   uint64_t w[8 * G];
-  load_weight<G>(p.w, p.w_f32, at, w);
+  float tscale = 1.0f;
+  Divisor by_t(1.0f);
+  bool ready = false;
 
   // This CTA's sets of rows, in turns of `span` sets one after another.
   struct Walk {
@@ -429,6 +437,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
     } else {
       load_row(static_cast<const T*>(p.x) + now.row * p.ldx, in, at, v);
       if (p.res) load_row(static_cast<const T*>(p.res) + now.row * p.ldr, in, at, d);
+    }
+    if (!ready) {
+      load_weight<G>(p.w, p.w_f32, at, w);
+      if (FMT == kToNv4 && p.tscale) {
+        tscale = *p.tscale;
+        by_t = Divisor(tscale);
+      }
+      ready = true;
     }
     if (p.res) {
 #pragma unroll
@@ -474,8 +490,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
   __shared__ uint64_t bars[BULK ? 8 * kMaxStages : 1];
   Ring<T, G, 3> ring;
   if constexpr (BULK) ring.init(smem, bars, p.plan, sub, p.D, p.dh ? 3 : 2, p.err);
-  uint64_t w[8 * G];
-  load_weight<G>(p.w, p.w_f32, at, w);
+  uint64_t w[8 * G];  // (after the first row's loads, as in the forward pass)
+  bool ready = false;
 
   const long long stride = (long long)p.groups * p.plan.rows_cta;
   int turn = 0;
@@ -513,6 +529,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
         load_row(static_cast<const T*>(p.h) + r * p.ldh, in, at, h);
         load_row(static_cast<const T*>(p.dy) + r * p.ldy, in, at, g);
         if (p.dh) load_row(static_cast<const T*>(p.dh) + r * p.ldd, in, at, d);
+      }
+      if (!ready) {
+        load_weight<G>(p.w, p.w_f32, at, w);
+        ready = true;
       }
       const uint64_t rr = pair(rstd, rstd);
       uint64_t s[2] = {0, 0};
@@ -703,8 +723,8 @@ dp_status_t dp_rms_norm(const void* x, long long ldx, const void* residual, long
   const long long sets = ((long long)p.rows + p.plan.rows_cta - 1) / p.plan.rows_cta;
   // A CTA keeps the weights and has rows ahead over a turn of several sets, as long
   // as there are CTAs enough to even out (8192 x 4096: 48.4 us with turns of one,
-  // 41.3 of four, 39.4 of six, 39.5 of nine).
-  p.span = (int)std::max(1ll, std::min(6ll, sets / (dev.sm_count * 8)));
+  // 41.3 of four, 39.4 of six, 39.5 of nine; 4000 x 768 bf16: 10.6 of one, 8.4 of two).
+  p.span = (int)std::max(1ll, std::min(6ll, sets / (dev.sm_count * 3)));
   p.err = dev.err_word;
   const int threads = p.plan.warps * p.plan.rows_cta * 32;
   size_t smem = p.span > 1 ? plan_ring(&p.plan, D, esz, residual ? 2 : 1, 2, 72u << 10) : 0;
