@@ -937,8 +937,9 @@ DP_API int dp_get_collective_variant(void);
  * which where they split a tile over a cluster of 2, 4 or 8 CTAs use one cluster at least),
  * stream_ctas for the streaming collectives (reduce-scatter, all-gather,
  * all-reduce, accumulate, bucket and variable-length kernels), the gradient
- * norm, AdamW, the 4- and 8-bit quantisation and the RMS norm;
- * dp_allgather_linear_w4 has no limit; 0 means no limit (the default: one resident grid over every SM).  Lets a caller leave SMs free
+ * norm, AdamW, the 4- and 8-bit quantisation and the RMS norm; neither is for
+ * dp_allgather_linear_w4.  0 means no limit (the default: one resident grid over
+ * every SM).  Lets a caller leave SMs free
  * for a kernel on another stream -- the resource-partitioning experiment of
  * "Optimizing ML Concurrent Computation and Communication with GPU DMA
  * Engines" (Q2, "Resource Partitioning").  Results do not depend on the

@@ -23,7 +23,7 @@
 // bf16: forward with residual to 8 bits 39.4 us (236 MB: 6.0 TB/s; 58 % of the
 // issue slots), backward with dh 45 us with the sum over 304 sets of rows (268 MB:
 // 6.0 TB/s, 75 % of DRAM under the profiler).  One row of 4096: 2.1 us, 1000 x 768
-// fp32 4.9, 2050 x 1120 to nvfp4 8.9 (first loads, and the two divisors of each block
+// fp32 4.8, 2050 x 1120 to nvfp4 8.7 (first loads, and the two divisors of each block
 // of 16), backward of 1031 x 1601 fp32 11 us (scalar accesses).  What led there: a CTA
 // for each row with scalar fp32 arithmetic 49 and 101 us; pairs of fp32 and
 // add.bf16x2 took the forward from 34 to 25 instructions an element; a thread's own

@@ -33,16 +33,17 @@
 // Few rows: d is split over the warps of a CTA, whose partial sums meet in shared
 // memory and are added in order.
 //
-// Measured (GB300, launches in a CUDA graph), w[65536,8192]: one token 58 us in
-// either form (5.2 TB/s of weights in nvfp4), eight 65 us, 16 70 us in mxfp4, 32 112
-// us; 4096 x 4096: one token 7.5 us, 16 8.5 us.  What bounds it: one token's bytes
+// Measured (GB300, launches in a CUDA graph), w[65536,8192]: one token 57 us in
+// either form (5.3 TB/s of weights in nvfp4), eight 62 us, 16 71 us in mxfp4, 32 116
+// us; 4096 x 4096: one token 6.9 us, 16 8.6 us.  What bounds it: one token's bytes
 // alone (no decoding, no products) take 52 us and its instructions alone (the same
 // codes again and again) 50; 16 tokens' instructions 66; 32 tokens' MMAs 138 clocks
 // of a step, against the 87 in which its bytes arrive.  Neither rings of 4 or 5 steps
 // nor 28 warps of 72 registers gained anything.  The steps that led here: x
 // converted by each warp for itself 83 us (one token, nvfp4) and 138 us (16, mxfp4);
 // rings half as large, twice the warps 69 and 128; x staged for the CTA 59 and 91; x
-// prepared beforehand 70 (16).
+// prepared beforehand 70 (16); divisions and ldexpf around the steps by shifts and
+// products, one token of 4096 x 4096 7.5 -> 6.9.
 
 #include "dp_early.cuh"
 #include "dp_launch.h"
@@ -76,7 +77,8 @@ struct W4Params {
   int tiles_f;     // 128-row scale tiles of a shard
   int col_tiles;
   int units;       // of 32 rows, of all shards
-  int split;       // warps that share a unit's d
+  int split;       // warps that share a unit's d: a power of two, 2^split_bits
+  int split_bits;
   int slab;        // steps of d whose x is in shared memory at once, for each share
   int slabs;       // slabs of a share
   int x_vec;       // x's rows start on 16-byte boundaries
@@ -136,6 +138,12 @@ __device__ __forceinline__ int top_exponent(uint4 v) {
 // 2^e as fp32, for e in [-126, 127]; 0 below.
 __device__ __forceinline__ float pow2(int e) {
   return __uint_as_float(e < -126 ? 0u : (uint32_t)(e + 127) << 23);
+}
+
+// v 2^e, in two steps, for e in [-258, 250]: what pow2 makes 0 of is far below fp32's
+// smallest (an infinite v may become NaN).
+__device__ __forceinline__ float scaled(float v, int e) {
+  return __fmul_rn(__fmul_rn(v, pow2(e >> 1)), pow2(e - (e >> 1)));
 }
 
 // Eight e2m1 codes to four pairs of f16.
@@ -225,8 +233,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
   __shared__ int xexp[kReady ? 1 : 2][kReady ? 1 : kMaxWarps][8 * NT];  // slab, share, token
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int share = warp % p.split;
-  const int unit = (int)blockIdx.x * (warps / p.split) + warp / p.split;
+  const int share = warp & (p.split - 1);
+  const int unit = (int)blockIdx.x * (warps >> p.split_bits) + (warp >> p.split_bits);
   const int m0 = (int)blockIdx.y * 8 * NT;
   const int tokens = min(p.M - m0, 8 * NT);
   const uint32_t mine = smem_u32(smem) + (uint32_t)warp * G::kWarp;
@@ -246,8 +254,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
 
   const bool live_unit = unit < p.units;
   const int u = live_unit ? unit : 0;
-  const int tile = u / 4, shard = tile / p.tiles_f;
-  const int row0 = (tile - shard * p.tiles_f) * 128 + u % 4 * 8;  // rows g, + 32, + 64, + 96
+  int tile = u / 4, shard = 0;
+  while (tile >= p.tiles_f) tile -= p.tiles_f, ++shard;
+  const int row0 = tile * 128 + u % 4 * 8;  // rows g, + 32, + 64, + 96
   const uint8_t* code[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r)  // rows past the shard's end read its last, and are dropped
@@ -280,13 +289,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
   // token's largest so far.  A lane takes eight values of every other step, both times.
   const int half = lane >> 4;
   const uint32_t piece = (uint32_t)half * 256 + x_place((lane & 15) * 8);
+  // q / tokens for q below 1024: 2^16 / tokens rounded up is off by less than 1 / q of it
+  const int per_token = kReady ? 0 : 65536 / tokens + 1;
   const auto each_job = [&](auto f) {
-    int s = 0, m = warp;
-    while (m >= tokens) m -= tokens, ++s;
-    while (s < p.split) {
-      f(s, m);
-      m += warps;
-      while (m >= tokens) m -= tokens, ++s;
+    for (int q = warp; q < tokens * p.split; q += warps) {
+      const int s = (q * per_token) >> 16;
+      f(s, q - s * tokens);
     }
   };
   const auto x_copy = [&](int slab) {
@@ -540,7 +548,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
       for (int e = 0; e < 4; ++e) {
         int to = xref[n][e & 1] - 137;
         if (MX) to += sbase[2 * i + e / 2] + 18 - 131;
-        acc[i][n][e] = ldexpf(acc[i][n][e], to);
+        acc[i][n][e] = scaled(acc[i][n][e], to);
       }
   float alpha = 1.0f;
   if constexpr (!MX)
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
   __syncthreads();
   if (!live_unit) return;
   const float* first = reinterpret_cast<const float*>(smem + (size_t)(warp - share) * G::kWarp);
-  for (int i = share * 32 + lane; i < kRows * 8 * NT; i += p.split * 32) {
+  for (int i = share * 32 + lane; i < kRows * tokens; i += p.split * 32) {
     float v = first[i];
     for (int k = 1; k < p.split; ++k) v = __fadd_rn(v, first[(size_t)k * (G::kWarp / 4) + i]);
     store(row0 + i % 8 + i % kRows / 8 * 32, i / kRows, v);
@@ -623,6 +631,8 @@ cudaError_t launch_for(W4Params p, const dph::DeviceInfo& dev, cudaStream_t s) {
     p.slabs = (share + p.slab - 1) / p.slab;
     if (smem <= kMaxSmem) break;
   }
+  p.split_bits = 0;
+  while ((1 << p.split_bits) < p.split) ++p.split_bits;
   auto kernel = w4_kernel<MX, NT, READY>;
   if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kMaxWarps * 32, kMaxSmem,
                           dev.device) < 1)
