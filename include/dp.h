@@ -855,8 +855,11 @@ DP_API dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* 
  * be NULL; without a format codes and scales are.
  * Arithmetic in fp32: a thread sums 16 or 32 squares in four chains, the rest is
  * pairwise (the same bits for a row in any call, but for rows that start off 32-byte
- * boundaries); magnitudes above 1.8e19 make the mean infinite, and then y is 0.  A
- * row with a NaN is NaN throughout.
+ * boundaries).  That holds magnitudes up to 3.2e18; where the sum passes fp32 the
+ * mean is infinite, rstd 0, and y 0, or NaN where h * weight, which is formed first,
+ * is infinite; in other rows it has to stay within fp32, too.  With an eps below
+ * 1e-30, rows below 5e-19 lose bits of rstd and rows below 1e-23 count as zeros (rstd
+ * is then infinite if eps is 0).  A row with a NaN is NaN throughout.
  * Requires D <= 32768, and D % 32 == 0 with a format; eps >= 0 and finite.
  *
  * dp_rms_norm_backward: from dy (the gradient of y) and dh (that which reaches h

@@ -73,7 +73,8 @@ struct NormFwdParams {
   int M, D, col_tiles;
   int rows;      // M, up to a whole scale tile where there are scales
   int span;      // sets of rows_cta rows that a CTA takes one after another
-  float eps, inv_d;
+  float down;    // a power of two, one over a row's threads or less
+  float eps, inv_d;  // inv_d: 1 / (D down)
   int w_f32;
 };
 
@@ -454,7 +455,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (BULK ? 3 : 4) : 1)
     uint64_t s[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8 * G; ++j) s[j % 2] = fma2(v.two(j), v.two(j), s[j % 2]);
-    const float ss = row_sum(sum4(s[0], s[1]), part[turn] + sub * p.plan.warps, at);
+    // A thread's own 16 G squares have to fit fp32; times `down` the row's then do, too.
+    const float ss =
+        row_sum(__fmul_rn(sum4(s[0], s[1]), p.down), part[turn] + sub * p.plan.warps, at);
     if constexpr (BULK) {  // every thread of the row has read its stage
       if (at.t == 0) fetch(ring.slot);
       ring.next();
@@ -709,7 +712,7 @@ dp_status_t dp_rms_norm(const void* x, long long ldx, const void* residual, long
   p.codes = static_cast<uint8_t*>(codes);
   p.scales = static_cast<uint8_t*>(scales);
   p.tscale = tensor_scale;
-  p.ldx = ldx, p.ldr = ldr, p.M = M, p.D = D, p.eps = eps, p.inv_d = 1.0f / (float)D;
+  p.ldx = ldx, p.ldr = ldr, p.M = M, p.D = D, p.eps = eps;
   p.w_f32 = weight_dtype == DP_FP32;
   p.col_tiles = q ? mx4_col_tiles(D, block) : 0;
   p.rows = q ? (M + kScaleRows - 1) / kScaleRows * kScaleRows : M;
@@ -717,6 +720,10 @@ dp_status_t dp_rms_norm(const void* x, long long ldx, const void* residual, long
                    (!residual || (aligned(residual, 32) && ldr % 16 == 0 && aligned(h, 32))) &&
                    aligned(y, 32);
   p.plan = plan_for(D, vec);
+  int shares = 32;
+  while (shares < p.plan.warps * 32) shares *= 2;
+  p.down = 1.0f / (float)shares;
+  p.inv_d = 1.0f / (float)D * (float)shares;
   dph::DeviceInfo dev;
   if (!dph::current_device(&dev)) return DP_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -505,3 +505,83 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# --- magnitudes far from 1 --------------------------------------------------------------------
+
+def check_range(n, h, w, eps, q=False):
+    """The tolerances of any row: times a power of two a sum is as exact.  Two roundings more
+    for the smallest rows: h w below 2^-126 is 2^-150 off, which an rstd up to 2^62 takes to
+    2^-88; a thread's squares times that power are 2^-150 off at most, of 2^-124 or more (32
+    of them from 5e-19 on, over 1024), within the 16 u whose own terms come to 14."""
+    h64 = f64(h)
+    r64 = 1 / np.sqrt((h64 * h64).mean(1) + eps)
+    y64 = h64 * r64[:, None] * f64(w)
+    assert np.all(np.abs(f64(n.rstd) - r64) <= 16 * U * r64)
+    if n.y is not None:
+        tol = (18 * U + HALF[h.dtype] * (1 + 18 * U)) * np.abs(y64) + 2.0 ** -88
+        assert np.all(np.abs(f64(n.y) - y64) <= tol)
+    if q:
+        check_quantised(n.q, y64)
+
+
+def sized(M, D, sizes, dtype, seed):
+    """Rows of the magnitudes `sizes` (0.5 to 2 times that), others of 1."""
+    rng = np.random.default_rng(seed)
+    a = np.sign(rng.standard_normal((M, D))) * rng.uniform(0.5, 2, (M, D))
+    a[:len(sizes)] *= np.array(sizes)[:, None]
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(D)).float().to(DEV)
+    return torch.from_numpy(a).to(DEV).to(dtype), w
+
+
+@pytest.mark.parametrize("fmt", [None, "mxfp8"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,D", [(9, 96), (9, 513), (9, 4096), (2700, 4096), (9, 6432), (9, 16384),
+                                 (9, 32768)])
+def test_large_rows(M, D, dtype, fmt):
+    """4096 values of 1e18 have a sum of squares past fp32 and a mean of them well inside it."""
+    fmt = fmt if D % 32 == 0 else None
+    sizes = [1e12, 1e16, 1e17, 3e17, 1e18, 1.6e18]
+    x, w = sized(M, D, sizes, dtype, D)
+    n = norm.rms_norm(x, w, eps=EPS, format=fmt, keep=True)
+    few = torch.arange(9, device=DEV)
+    small = norm.rms_norm(x[few].clone(), w, eps=EPS, format=fmt, keep=True)
+    check_range(small, x[few], w, EPS, fmt is not None)
+    assert torch.equal(n.y[few], small.y) and torch.equal(n.rstd[few], small.rstd)
+    check_range(n, x, w, EPS)
+    m = norm.rms_norm(torch.zeros_like(x), w, residual=x, eps=EPS, format=fmt, keep=True)
+    assert torch.equal(m.h, x) and torch.equal(m.y, n.y) and torch.equal(m.rstd, n.rstd)
+    check_range(norm.rms_norm(x, w, eps=1e36), x, w, float(np.float32(1e36)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,D", [(9, 96), (9, 513), (2700, 4096), (9, 16384), (9, 32768)])
+@pytest.mark.parametrize("eps", [0.0, 1e-36, 1e-27])
+def test_small_rows(M, D, dtype, eps):
+    x, w = sized(M, D, [1e-12, 1e-14, 1e-16, 1e-17, 3e-18, 1e-18], dtype, D)
+    check_range(norm.rms_norm(x, w, eps=eps), x, w, float(np.float32(eps)))
+
+
+def test_rows_past_the_range():
+    """What the header says of them: an infinite mean makes y 0; squares that vanish leave eps."""
+    x, w = sized(4, 4096, [1e25, 1e38], torch.float32, 1)
+    n = norm.rms_norm(x, w)
+    fits = (x.double() * w.double()).abs() <= torch.finfo(torch.float32).max
+    assert (n.rstd[:2] == 0).all() and (n.y[:2][fits[:2]] == 0).all()
+    assert fits[0].all() and n.y[~fits].isnan().all()      # h w comes first: infinity times 0
+    x, w = sized(4, 4096, [1e-24, 0.0], torch.float32, 1)
+    n = norm.rms_norm(x, w, eps=0.0)
+    assert n.rstd[:2].isinf().all() and n.y[0].isinf().all() and n.y[1].isnan().all()
+    n = norm.rms_norm(x, w, eps=1e-12)
+    assert bool(((n.rstd[:2] - 1e6).abs() <= 16 * U * 1e6).all()) and (n.y[1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_backward_of_large_and_small_rows(dtype):
+    h, w = sized(9, 4096, [1e18, 1.6e18, 3e17, 1e12, 1e-12, 1e-16, 1e-17], dtype, 3)
+    rng = np.random.default_rng(3)
+    dy, dh = matrix(rng, 9, 4096, dtype), matrix(rng, 9, 4096, dtype)
+    n = norm.rms_norm(h, w, eps=0.0)
+    check_range(n, h, w, 0.0)
+    backward(dy, h, w, n.rstd, dh)
+    backward(dy, h, w, n.rstd, None)
