@@ -861,6 +861,7 @@ DP_API dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* 
  * 1e-30, rows below 5e-19 lose bits of rstd and rows below 1e-23 count as zeros (rstd
  * is then infinite if eps is 0).  A row with a NaN is NaN throughout.
  * Requires D <= 32768, and D % 32 == 0 with a format; eps >= 0 and finite.
+ * M == 0 or D == 0 writes nothing, rstd neither.
  *
  * dp_rms_norm_backward: from dy (the gradient of y) and dh (that which reaches h
  * past the norm, or NULL: none), both [M, D] of dtype,

@@ -61,7 +61,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 
 
     ``format``: "mxfp4", "nvfp4" (``tensor_scale``: its fp32 device value,
     calibrated beforehand) or "mxfp8": y is quantised as it is formed, into ``q``,
-    and is itself kept only with ``keep`` (a weight gradient needs it)."""
+    and is itself kept only with ``keep`` (a weight gradient needs it).  Rows of no
+    elements have rstd NaN."""
     if format is not None and format not in FORMATS:
         raise ValueError(f"format: None, 'mxfp4', 'nvfp4' or 'mxfp8', not {format!r}")
     if stream is not None:
@@ -79,6 +80,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual=None, eps: float = 
     here = B._stream_on(dev, "rms_norm")
     h = x if residual is None else torch.empty((M, D), dtype=x.dtype, device=dev)
     rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    if D == 0:
+        rstd.fill_(float("nan"))     # a mean of nothing; the library writes nothing then
     y = torch.empty((M, D), dtype=x.dtype, device=dev) if keep or format is None else None
     q = c = None
     if format is not None:

@@ -585,3 +585,14 @@ def test_backward_of_large_and_small_rows(dtype):
     check_range(n, h, w, 0.0)
     backward(dy, h, w, n.rstd, dh)
     backward(dy, h, w, n.rstd, None)
+
+
+def test_a_row_of_nothing_has_no_mean():
+    """Rows of no elements: the mean of their squares, and so rstd, is NaN."""
+    held = torch.full((3,), 7.0, device=DEV)     # what the allocator hands out next
+    del held
+    n = norm.rms_norm(torch.zeros(3, 0, device=DEV), torch.ones(0, device=DEV))
+    assert n.rstd.shape == (3,) and n.rstd.dtype == torch.float32 and n.rstd.isnan().all()
+    n = norm.rms_norm(torch.zeros(2, 0, device=DEV), torch.ones(0, device=DEV),
+                      residual=torch.zeros(2, 0, device=DEV), format="mxfp8")
+    assert n.rstd.isnan().all() and n.q.rows == 2 and n.q.cols == 0
