@@ -28,6 +28,20 @@ def _format(name) -> int:
     return FORMATS[name]
 
 
+class OtherFormat(ValueError, KeyError):
+    """A matrix of a form that the call does not take, such as an 8-bit one."""
+
+    __str__ = Exception.__str__      # not KeyError's, which quotes
+
+
+def _code4(q) -> int:
+    """The library's number for a 4-bit matrix's format."""
+    try:
+        return FORMATS[q._kind[2]]
+    except KeyError:
+        raise OtherFormat(f"need an mxfp4 or nvfp4 matrix, not {q._kind[2]}: {q!r}") from None
+
+
 def _scale_bytes(rows: int, cols: int, format: str) -> int:
     """dp_mx4_scales_size."""
     return -(-rows // 128) * -(-cols // (4 * _BLOCK[format])) * 512
@@ -193,7 +207,8 @@ def _rows(x):
 
 def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values a 4-bit matrix stands for."""
-    rows, cols, format, dev = q._kind
+    rows, cols, _, dev = q._kind
+    fmt = _code4(q)
     if stream is not None:
         with _on(stream, dev):
             return dequantize(q, dtype)
@@ -201,7 +216,7 @@ def dequantize(q: Mx4Tensor, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         raise TypeError(f"unsupported dtype {dtype}")
     out = torch.empty((rows, cols), dtype=dtype, device=dev)
     c = q._c
-    st = (B._lib or B.load()).dp_mx4_dequantize(c.codes, c.scales, rows, cols, FORMATS[format],
+    st = (B._lib or B.load()).dp_mx4_dequantize(c.codes, c.scales, rows, cols, fmt,
                                                 c.tensor_scale, out.data_ptr(), _DT[dtype],
                                                 B._stream_on(dev, "dequantize"))
     if st:
@@ -242,6 +257,7 @@ def _shard_bytes(w_shards, cols, format, device):
 def matmul(x: Mx4Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """y = x . w^T with w the row concatenation of the 4-bit shards."""
     M, D, format, dev = x._kind
+    fmt = _code4(x)
     if stream is not None:
         with _on(stream, dev):
             return matmul(x, w_shards, y_dtype)
@@ -250,7 +266,7 @@ def matmul(x: Mx4Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) -> torch
     K = len(w_shards)
     arr = _shards(w_shards, D, format, dev)
     y = torch.empty((M, K * w_shards[0].rows), dtype=y_dtype, device=dev)
-    B.dp_allgather_matmul_mx4(x._c, M, D, arr, K, w_shards[0].rows, FORMATS[format], y,
+    B.dp_allgather_matmul_mx4(x._c, M, D, arr, K, w_shards[0].rows, fmt, y,
                               _DT[y_dtype], stream=B._stream_on(dev, "matmul"))
     return y
 
@@ -274,6 +290,7 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
         raise ValueError("need at least one shard")
     dev, K = x.device, len(w_shards)
     F, _, format, _ = w_shards[0]._kind
+    fmt = _code4(w_shards[0])
     arr = _shards(w_shards, D, format, dev)
     if x_scale is not None:
         _check_scale(x_scale, dev)
@@ -283,7 +300,7 @@ def linear(x: torch.Tensor, w_shards, x_scale=None, y_dtype=torch.bfloat16,
     y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
     st = (B._lib or B.load()).dp_allgather_linear_mx4(
         x.data_ptr(), M, D, ld, _code(x),
-        None if x_scale is None else x_scale.data_ptr(), arr, K, F, FORMATS[format],
+        None if x_scale is None else x_scale.data_ptr(), arr, K, F, fmt,
         y.data_ptr(), _DT[y_dtype], ws.data_ptr(), nbytes, B._stream_on(dev, "linear"))
     if st:
         raise B.DpError(st, "dp_allgather_linear_mx4")
@@ -307,7 +324,7 @@ def linear_w4(x: torch.Tensor, w_shards, y_dtype=torch.bfloat16, stream=None) ->
         raise ValueError("need at least one shard")
     dev, K = x.device, len(w_shards)
     F, _, format, _ = w_shards[0]._kind
-    fmt = FORMATS[format]
+    fmt = _code4(w_shards[0])
     arr = _shard_bytes(w_shards, D, format, dev)
     y = torch.empty((M, K * F), dtype=y_dtype, device=dev)
     ws, nbytes = None, 0

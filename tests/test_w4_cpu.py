@@ -140,3 +140,15 @@ def test_the_eight_bit_helpers_check():
         mx8.linear(x.half(), [w])
     with pytest.raises(ValueError, match="columns"):
         mx8.linear(x[:, :32], [w])
+
+
+def test_matrices_of_another_form_are_named():
+    """An 8-bit matrix where a 4-bit one belongs is refused as other wrong values are, by name."""
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    q = mx8.Mx8Tensor(u8(16 * 64), u8(512), 16, 64)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: mx4.dequantize(q), lambda: mx4.linear(x, [q]), lambda: mx4.matmul(q, [q]),
+                 lambda: mx4.linear_w4(x, [q]), lambda: mx4.dequantize(q, stream=0),
+                 lambda: mx4.matmul(q, [q], stream=0)):
+        with pytest.raises(ValueError, match=r"^need an mxfp4 or nvfp4 matrix, not mxfp8: Mx8Tensor\(16 x 64"):
+            call()
