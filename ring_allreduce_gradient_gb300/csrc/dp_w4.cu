@@ -473,7 +473,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
               int e = byte == 255 ? 0 : byte;
               e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
               e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-              const int to = e > sref + kSRoom ? e : sref;
+              // (no higher than where byte 255, NaN, is out of the room for good)
+              const int to = e > sref + kSRoom ? min(e, 254 - kSRoom) : sref;
               const float down = pow2(sref - to);
               sbase[r] = to - 18;
 #pragma unroll

@@ -244,3 +244,43 @@ def test_tokens_do_not_meet():
         x2 = (normal((M, D), 5) * 1e4).bfloat16()
         x2[3] = x[5]
         assert torch.equal(mx4.linear_w4(x2, s, torch.float32)[3], y[5])
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def made(codes, byte):
+    """An mxfp4 matrix of e2m1 codes [F, D] and scale bytes [F, D / 32], and its values."""
+    F, D = codes.shape
+    Rt, Ct = -(-F // 128), -(-D // 128)
+    full = np.zeros((Rt * 128, Ct * 4), np.uint8)
+    full[:F, :D // 32] = byte
+    tiles = full.reshape(Rt, 4, 32, Ct, 4).transpose(0, 3, 2, 1, 4)
+    packed = (codes[:, ::2] | codes[:, 1::2] << 4).astype(np.uint8)
+    q = mx4.Mx4Tensor(torch.from_numpy(packed).to(DEV),
+                      torch.from_numpy(tiles.reshape(-1).copy()).to(DEV), F, D, "mxfp4")
+    scale = np.where(byte == 255, np.nan, np.exp2(byte - 127.0)).repeat(32, 1)
+    return q, E2M1[codes & 7] * np.where(codes & 8, -1, 1) * scale
+
+
+@pytest.mark.parametrize("M", [1, 10, 20])
+@pytest.mark.parametrize("top", [200, 245, 246, 250, 254])
+def test_a_nan_block_after_one_of_the_largest_scales(top, M):
+    """Byte 255 is NaN whatever scales its row has had; D is long enough that a warp comes to
+    it after them."""
+    rng = np.random.default_rng(top)
+    F, D = 48, 8192
+    byte = np.full((F, D // 32), 120)
+    byte[3] = byte[40] = byte[41] = top
+    codes = rng.integers(0, 16, (F, D))
+    x = torch.from_numpy(rng.integers(-8, 9, (M, D)) * 2.0 ** -40).to(DEV).bfloat16()
+    q, v = made(codes, byte)
+    want, size = f64(x) @ v.T, np.abs(f64(x)) @ np.abs(v).T
+    y = f64(mx4.linear_w4(x, [q], torch.float32))
+    assert np.all(np.abs(y - want) <= 2 * (D + 8) * U * size)
+    byte[3, 5] = byte[40, 250] = 255                 # the second step of a warp; a later one
+    q, v = made(codes, byte)
+    y = f64(mx4.linear_w4(x, [q], torch.float32))
+    assert np.isnan(y[:, [3, 40]]).all()
+    keep = [f for f in range(F) if f not in (3, 40)]
+    assert np.all(np.abs(y - want)[:, keep] <= 2 * (D + 8) * U * size[:, keep])
