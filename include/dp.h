@@ -779,10 +779,10 @@ DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_f
  * dp_allgather_matmul_mx4, y of any alignment.  For the single tokens of a model
  * that is served: it reads the weights once for each 32 tokens; for more tokens the
  * products of quantised x are faster.
- * Weights are decoded exactly; x is exact down to 2^-27 of its row's largest
- * magnitude, and below it within 2^-35 of that magnitude (mxfp4: weights likewise,
- * within a row of w); products are summed in fp32, in an order that follows from
- * the sizes; tw, the shard's tensor scale, multiplies the sum.  x holding a NaN or
+ * Weights are decoded exactly, but for mxfp4 blocks whose scale is below 2^-27 of
+ * the largest scale of their row of w: those within 2^-25 of that scale.  x is exact
+ * down to 2^-27 of its row's largest magnitude, and below it within 2^-35 of that
+ * magnitude.  Products are summed in fp32, in an order that follows from the sizes; tw, the shard's tensor scale, multiplies the sum.  x holding a NaN or
  * an infinity gives that token NaN or infinities.  D == 0 writes zeros.
  * Requires D % 32 == 0, D <= 2^30, F_shard % 16 == 0, M <= 524280.
  * workspace: device memory of dp_allgather_linear_w4_workspace_size(M, D) bytes

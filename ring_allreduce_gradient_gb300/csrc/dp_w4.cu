@@ -27,8 +27,8 @@
 // about 2^10, and mxfp4's scales are taken relative to the largest of the row so
 // far; where a larger one comes by more than the headroom, the sums are multiplied
 // down first.  A value of x loses bits only below 2^-27 of that token's largest (and
-// is then off by at most 2^-35 of it), a weight below 2^-27 of its row's.  Sums are
-// fp32.
+// is then off by at most 2^-35 of it), an mxfp4 weight only where its block's scale is
+// below 2^-27 of its row's largest (by at most 2^-25 of that).  Sums are fp32.
 //
 // Few rows: d is split over the warps of a CTA, whose partial sums meet in shared
 // memory and are added in order.
@@ -64,6 +64,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr size_t kMaxSmem = 220 << 10;
 constexpr int kXRoom = 5;        // exponents that x may grow by before the sums are scaled down
 constexpr int kSRoom = 9;        // ... and mxfp4's scales
+constexpr int kSBelow = 18;      // exponents below the reference that f16 holds as they are
 
 struct W4Params {
   const uint16_t* x;   // or what prepare_kernel made of it, ld elements (f16) apart
@@ -361,11 +362,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
   int xref[NT][2];  // the exponents (biased) of tokens 2t, 2t + 1 of each eight that go to 2^10
-  int sbase[4];     // mxfp4: the scale byte of each row that goes to 2^4, less 18
+  int sbase[4];     // mxfp4: the scale byte of each row that goes to 2^4, less kSBelow
 #pragma unroll
   for (int n = 0; n < NT; ++n) xref[n][0] = xref[n][1] = -1000;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) sbase[r] = -18;
+  for (int r = 0; r < 4; ++r) sbase[r] = -kSBelow;
   // which bytes of the 16 rows' word of four are this lane's
   const uint32_t take = MX ? 0x4440u + (uint32_t)t : t & 1 ? 0x4432u : 0x4410u;
   const int last_step = steps - 1;
@@ -455,28 +456,30 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
           word[0] = word[1] = word[2] = word[3] = 0u;
         if constexpr (MX) {
           // A scale relative to the row's: exponent byte - sref + 4, as f16 bits.  What
-          // f16 cannot hold takes the long way, but for byte 0 far below: that is a
-          // block of zeros, or of values below 2^-124.
+          // f16 cannot hold takes the long way, but for byte 0: that is most often a block
+          // of zeros, and counts as one where its row's reference is 28 or more.
           int d[4];
           bool far = false;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int byte = (int)__byte_perm(word[r], 0u, take);
             d[r] = byte - sbase[r];
-            far |= (uint32_t)d[r] > kSRoom + 18u && byte != 0;
+            far |= (uint32_t)d[r] > (uint32_t)(kSRoom + kSBelow) && byte != 0;
             s[r][0] = (uint32_t)(max(d[r], -1) + 1) * 0x04000400u;
           }
           if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int byte = d[r] + sbase[r], sref = sbase[r] + 18;
+              const int byte = d[r] + sbase[r], sref = sbase[r] + kSBelow;
               int e = byte == 255 ? 0 : byte;
               e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
               e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-              // (no higher than where byte 255, NaN, is out of the room for good)
-              const int to = e > sref + kSRoom ? min(e, 254 - kSRoom) : sref;
+              // (not between, where byte 0 would count as nothing too early, see above, and
+              // no higher than where byte 255, NaN, is out of the room for good)
+              const int up = e <= kSBelow + kSRoom ? kSBelow : min(e, 254 - kSRoom);
+              const int to = e > sref + kSRoom ? up : sref;
               const float down = pow2(sref - to);
-              sbase[r] = to - 18;
+              sbase[r] = to - kSBelow;
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 float* a = &acc[r / 2][n][(r % 2) * 2];
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         int to = xref[n][e & 1] - 137;
-        if (MX) to += sbase[2 * i + e / 2] + 18 - 131;
+        if (MX) to += sbase[2 * i + e / 2] + kSBelow - 131;
         acc[i][n][e] = scaled(acc[i][n][e], to);
       }
   float alpha = 1.0f;

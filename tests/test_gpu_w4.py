@@ -284,3 +284,47 @@ def test_a_nan_block_after_one_of_the_largest_scales(top, M):
     assert np.isnan(y[:, [3, 40]]).all()
     keep = [f for f in range(F) if f not in (3, 40)]
     assert np.all(np.abs(y - want)[:, keep] <= 2 * (D + 8) * U * size[:, keep])
+
+
+@pytest.mark.parametrize("M", [1, 10, 20])
+@pytest.mark.parametrize("top", [9, 10, 18, 19, 27])
+def test_blocks_of_the_smallest_scale_count(top, M):
+    """Scale byte 0 is 2^-127, not nothing: with one of 2^27 times it in the row before."""
+    F, D = 16, 8192
+    codes, byte = np.zeros((F, D), int), np.zeros((F, D // 32), int)
+    codes[:, :32] = 1
+    byte[:, 0] = top
+    codes[:, 4 * 32:5 * 32] = 7
+    q, v = made(codes, byte)
+    x = torch.zeros(M, D, device=DEV, dtype=torch.bfloat16)
+    x[:, 4 * 32:5 * 32] = 2.0 ** 60
+    want = f64(x) @ v.T
+    assert want[0, 0] == 192 * 2.0 ** -67
+    assert np.array_equal(f64(mx4.linear_w4(x, [q], torch.float32)), want)
+
+
+@pytest.mark.parametrize("M", [1, 10, 20])
+@pytest.mark.parametrize("top", [30, 60, 130])
+def test_blocks_far_below_their_rows_largest(top, M):
+    """Blocks down to 2^-27 of the largest scale of their row are exact; below, a weight is off
+    by at most 2^-25 of that scale.  x is nothing where the large ones are, and a power of two
+    elsewhere, so that sums of one block's weights are exact."""
+    rng = np.random.default_rng(top)
+    F, D = 64, 8192
+    codes = rng.integers(0, 8, (F, D))
+    for below in (20, 26, 27, 28, 29, 30, 40):
+        low = top - below
+        if low < 0:
+            continue
+        byte = np.full((F, D // 32), low)
+        byte[:, ::4] = top                            # a block of each step
+        q, v = made(codes, byte)
+        x = torch.zeros(M, D, device=DEV, dtype=torch.bfloat16)
+        at = rng.choice([b for b in range(D // 32) if b % 4], M)
+        for m in range(M):
+            x[m, 32 * at[m]:32 * at[m] + 32] = 1.0
+        y, want = f64(mx4.linear_w4(x, [q], torch.float32)), f64(x) @ v.T
+        if below <= 27:
+            assert np.array_equal(y, want)
+        else:
+            assert np.all(np.abs(y - want) <= 32 * 2.0 ** (top - 127 - 25))
