@@ -782,8 +782,10 @@ DP_API dp_status_t dp_allgather_linear_mx4_workspace_size(int M, int D, dp_mx4_f
  * Weights are decoded exactly, but for mxfp4 blocks whose scale is below 2^-27 of
  * the largest scale of their row of w: those within 2^-25 of that scale.  x is exact
  * down to 2^-27 of its row's largest magnitude, and below it within 2^-35 of that
- * magnitude.  Products are summed in fp32, in an order that follows from the sizes; tw, the shard's tensor scale, multiplies the sum.  x holding a NaN or
- * an infinity gives that token NaN or infinities.  D == 0 writes zeros.
+ * magnitude.  Products are summed in fp32, in an order that follows from the sizes
+ * alone, M among them: a token's last bits may differ between batches.  tw, the
+ * shard's tensor scale, multiplies the sum.  x holding a NaN or an infinity gives that
+ * token NaN or infinities.  D == 0 writes zeros.
  * Requires D % 32 == 0, D <= 2^30, F_shard % 16 == 0, M <= 524280.
  * workspace: device memory of dp_allgather_linear_w4_workspace_size(M, D) bytes
  * (none for M <= 8), 16-byte aligned, any contents, overlapping nothing else; free

@@ -49,6 +49,7 @@
 #include "dp_launch.h"
 #include "dp_mx4.cuh"
 #include "dp_mx4q.cuh"
+#include "dp_w4_plan.h"
 
 #include <algorithm>
 #include <cstring>
@@ -56,12 +57,13 @@
 namespace {
 
 using namespace dpk;
+using w4::kMaxSmem;
+using w4::kMaxWarps;
+using w4::kRows;  // two instructions' 16
+using w4::kStep;
+using w4::x_row_bytes;
 
-constexpr int kStep = 128;       // values of d a warp takes at once: 32 a lane
-constexpr int kRows = 32;        // rows of a warp: two instructions' 16
-constexpr int kMaxWarps = 16;    // of a CTA
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr size_t kMaxSmem = 220 << 10;
 constexpr int kXRoom = 5;        // exponents that x may grow by before the sums are scaled down
 constexpr int kSRoom = 9;        // ... and mxfp4's scales
 constexpr int kSBelow = 18;      // exponents below the reference that f16 holds as they are
@@ -78,27 +80,22 @@ struct W4Params {
   int tiles_f;     // 128-row scale tiles of a shard
   int col_tiles;
   int units;       // of 32 rows, of all shards
-  int split;       // warps that share a unit's d: a power of two, 2^split_bits
-  int split_bits;
-  int slab;        // steps of d whose x is in shared memory at once, for each share
-  int slabs;       // slabs of a share
+  int split, split_bits, slab, slabs;  // (w4::Plan)
   int x_vec;       // x's rows start on 16-byte boundaries
   int y_f32;
   unsigned* err;
 };
 
 // Shared memory: each warp's ring of codes and scales, and two slabs of x (one, if
-// there is no other) for each share and token, rows padded so that neighbouring
-// tokens fall into other banks.
+// there is no other) for each share and token.
 template <bool MX, int NT>
 struct W4Ring {
-  static constexpr int kStages = NT == 4 ? 2 : 3;              // steps of codes in a warp's ring
+  static constexpr int kStages = w4::ring_steps(NT);
   static constexpr uint32_t kCodes = kRows * (kStep / 2);
-  static constexpr uint32_t kStage = kCodes + (MX ? 128 : 256);
+  static constexpr uint32_t kStage = w4::step_bytes(MX);
   static constexpr uint32_t kWarp = kStages * kStage;
   static_assert(kRows * 8 * NT * 4 <= kWarp, "partial sums");
 };
-__host__ __device__ inline uint32_t x_row_bytes(int slab) { return (uint32_t)slab * kStep * 2 + 64; }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -603,40 +600,11 @@ constexpr int kMaxTokens = 65535 * 8;  // the grid's second dimension
 constexpr int kMaxD = 1 << 30;         // a share's last slab, past D, still has int positions
 constexpr int kOwnTokens = 8;          // of a call whose kernel makes f16 of x itself
 
-
 template <bool MX, int NT, bool READY>
 cudaError_t launch_for(W4Params p, const dph::DeviceInfo& dev, cudaStream_t s) {
-  // Many units: one CTA an SM (or as many rounds of them as it takes), each warp
-  // its own unit, x shared by all.  Few: d is split over warps, up to 16 an SM,
-  // while each share has a step and x fits.
-  const int steps = (p.D + kStep - 1) / kStep, tokens = std::min(p.M, 8 * NT);
-  size_t smem = 0;
-  int warps = 0, per = 0;
-  for (p.split = kMaxWarps; p.split >= 1; p.split /= 2) {
-    if (p.split > 1 && (p.split > steps || (long long)p.units * p.split > 16ll * dev.sm_count))
-      continue;
-    const long long all = (long long)p.units * p.split, full = 16ll * dev.sm_count;
-    const long long ctas = (all + full - 1) / full * dev.sm_count;
-    per = (int)((p.units + ctas - 1) / ctas);  // units of a CTA
-    per = std::max(1, std::min(per, kMaxWarps / p.split));
-    warps = per * p.split;
-    const int share = (steps + p.split - 1) / p.split;
-    // Slabs as long as fit; where the kernel makes f16 of x itself, 64 steps of all
-    // tokens at most (longer ones are staged too long before the first step).
-    const size_t ring = (size_t)warps * W4Ring<MX, NT>::kWarp;
-    const auto fits = [&](int slabs, int slab) {
-      smem = ring + (size_t)(slabs > 1 ? 2 : 1) * p.split * tokens * x_row_bytes(slab);
-      return smem <= kMaxSmem && (READY || slabs == share || slab <= std::max(16, 64 / tokens));
-    };
-    for (p.slabs = 1;; ++p.slabs) {
-      p.slab = (share + p.slabs - 1) / p.slabs;
-      if (fits(p.slabs, p.slab) || p.slab <= 2) break;
-    }
-    p.slabs = (share + p.slab - 1) / p.slab;
-    if (smem <= kMaxSmem) break;
-  }
-  p.split_bits = 0;
-  while ((1 << p.split_bits) < p.split) ++p.split_bits;
+  const w4::Plan plan = w4::plan(std::min(p.M, 8 * NT), p.D, p.units, MX, NT, READY);
+  p.split = plan.split, p.split_bits = plan.split_bits;
+  p.slab = plan.slab, p.slabs = plan.slabs;
   auto kernel = w4_kernel<MX, NT, READY>;
   if (dph::prepare_kernel(reinterpret_cast<const void*>(kernel), kMaxWarps * 32, kMaxSmem,
                           dev.device) < 1)
@@ -645,9 +613,10 @@ cudaError_t launch_for(W4Params p, const dph::DeviceInfo& dev, cudaStream_t s) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((p.units + per - 1) / per), (unsigned)((p.M + 8 * NT - 1) / (8 * NT)));
-  cfg.blockDim = dim3((unsigned)warps * 32);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3((unsigned)((p.units + plan.per - 1) / plan.per),
+                     (unsigned)((p.M + 8 * NT - 1) / (8 * NT)));
+  cfg.blockDim = dim3((unsigned)plan.warps * 32);
+  cfg.dynamicSmemBytes = plan.smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

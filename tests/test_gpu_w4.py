@@ -328,3 +328,21 @@ def test_blocks_far_below_their_rows_largest(top, M):
             assert np.array_equal(y, want)
         else:
             assert np.all(np.abs(y - want) <= 32 * 2.0 ** (top - 127 - 25))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_one_token_and_the_same_one_in_a_batch(fmt):
+    """A call's own sizes order its sums, M among them.  Alone and in a batch a token's y are
+    each within 2 (D + 8) 2^-24 of the sum of magnitudes of the exact one, and so within twice
+    that of one another; where d is one step there is one order."""
+    for D, F in ((128, 96), (1024, 96), (2080, 400), (8192, 64)):
+        s = shards_of(normal((F, D), 1), 1, fmt)
+        w = mx4.dequantize(s[0], torch.float32).double()
+        x = normal((40, D), 2).bfloat16()
+        size = x.double().abs() @ w.abs().t()
+        alone = torch.cat([mx4.linear_w4(x[i:i + 1], s, torch.float32) for i in range(40)])
+        for M in (2, 5, 8, 9, 16, 17, 33, 40):
+            y = mx4.linear_w4(x[:M], s, torch.float32)
+            if D == 128:
+                assert torch.equal(y, alone[:M])
+            assert bool(((y - alone[:M]).double().abs() <= 4 * (D + 8) * U * size[:M]).all())

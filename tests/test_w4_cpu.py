@@ -1,5 +1,8 @@
 """Refusals of the few-token product and of the products of 8-bit x, made on the host before any device call."""
 import ctypes
+import os
+import random
+import subprocess
 
 import pytest
 import torch
@@ -152,3 +155,56 @@ def test_matrices_of_another_form_are_named():
                  lambda: mx4.matmul(q, [q], stream=0)):
         with pytest.raises(ValueError, match=r"^need an mxfp4 or nvfp4 matrix, not mxfp8: Mx8Tensor\(16 x 64"):
             call()
+
+
+# Prints the few-token product's plan for each line "tokens D units mx nt ready".
+PLANNER = r"""
+#include "dp_w4_plan.h"
+#include <cstdio>
+int main() {
+  int tokens, D, units, mx, nt, ready;
+  while (std::scanf("%d %d %d %d %d %d", &tokens, &D, &units, &mx, &nt, &ready) == 6) {
+    const w4::Plan p = w4::plan(tokens, D, units, mx, nt, ready);
+    std::printf("%d %d %d %d %d %d %zu\n", p.split, p.split_bits, p.per, p.warps, p.slab, p.slabs,
+                p.smem);
+  }
+}
+"""
+
+
+def test_the_plan_follows_from_the_sizes(tmp_path):
+    """The order of the few-token product's sums is its plan's, which is made without a device:
+    from the sizes.  Every plan covers d and the units, and stays within a CTA's means."""
+    csrc = os.path.join(os.path.dirname(B.__file__), "csrc")
+    (tmp_path / "p.cpp").write_text(PLANNER)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", csrc,
+                    str(tmp_path / "p.cpp"), "-o", str(tmp_path / "p")], check=True)
+    rng = random.Random(5)
+    cases = [(1, 4096, 128), (1, 8192, 2048), (8, 32, 4), (16, 8192, 2048), (32, 1 << 30, 4),
+             (32, 8192, 1 << 26), (1, 1 << 30, 4), (8, 1 << 30, 4), (9, 16384, 4)]
+    for _ in range(3000):
+        cases.append((rng.choice([1, 2, 3, 5, 8, 9, 12, 16, 17, 31, 32]),
+                      32 * int(2 ** rng.uniform(0, 12)), 4 * int(2 ** rng.uniform(0, 14))))
+    lines = []
+    for tokens, D, units in cases:
+        nt = 1 if tokens <= 8 else 2 if tokens <= 16 else 4
+        for mx in (0, 1):
+            lines.append((tokens, D, units, mx, nt, int(tokens > 8)))
+    out = subprocess.run([str(tmp_path / "p")], input="\n".join(" ".join(map(str, c)) for c in lines),
+                         capture_output=True, text=True, check=True).stdout.splitlines()
+    assert len(out) == len(lines)
+    for (tokens, D, units, mx, nt, ready), o in zip(lines, out):
+        split, bits, per, warps, slab, slabs, smem = map(int, o.split())
+        steps = -(-D // 128)
+        assert split == 1 << bits and warps == per * split and 1 <= warps <= 16
+        assert split == 1 or (split <= steps and units * split <= 16 * 152)
+        assert slab >= 1 and split * slabs * slab >= steps and (slabs - 1) * slab < -(-steps // split)
+        assert warps * 32 >= split * tokens or not ready       # a lane copies a token's slab
+        assert smem <= 220 << 10
+        step = 32 * 64 + (128 if mx else 256)
+        ring = warps * (2 if nt == 4 else 3) * step
+        assert smem == ring + (2 if slabs > 1 else 1) * split * tokens * (slab * 256 + 64)
+        if not ready and slabs > 1:
+            assert slab >= 2                    # a slab of one step would not wait for the next
+    with open(os.path.join(csrc, "dp_w4.cu")) as f:
+        assert "sm_count" not in f.read()
