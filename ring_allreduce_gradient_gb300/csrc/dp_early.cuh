@@ -7,6 +7,8 @@
 
 #include "dp_common.cuh"
 
+#include <mutex>
+
 namespace dpk {
 
 // Comes first in such a kernel, before it touches global memory: everything
@@ -31,9 +33,19 @@ __device__ __forceinline__ void stream_order() {
 
 namespace dph {
 
+// Held while such a kernel is launched.  A call whose second kernel reads, before its
+// wait, what its first one has waited for holds it over both: no kernel that another
+// thread launches through this header, and that writes while the next one starts, comes
+// between the two.
+inline std::mutex& early_launches() {
+  static std::mutex mu;
+  return mu;
+}
+
+// With early_launches() held.
 template <typename P>
-cudaError_t launch_early(void (*kernel)(P), const P& p, unsigned grid, unsigned threads,
-                         cudaStream_t s, size_t smem = 0) {
+cudaError_t launch_early_held(void (*kernel)(P), const P& p, unsigned grid, unsigned threads,
+                              cudaStream_t s, size_t smem = 0) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -45,6 +57,13 @@ cudaError_t launch_early(void (*kernel)(P), const P& p, unsigned grid, unsigned 
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename P>
+cudaError_t launch_early(void (*kernel)(P), const P& p, unsigned grid, unsigned threads,
+                         cudaStream_t s, size_t smem = 0) {
+  std::lock_guard<std::mutex> lock(early_launches());
+  return launch_early_held(kernel, p, grid, threads, s, smem);
 }
 
 }  // namespace dph

@@ -53,6 +53,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <mutex>
 
 namespace {
 
@@ -370,7 +371,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_kernel(const __grid_cons
 
   if constexpr (kReady) {
     // The kernel before this one is prepare_kernel, which let this one start when all
-    // before it had ended: the weights may be read already, x not yet.
+    // before it had ended: the weights may be read already, x not yet.  The call's lock
+    // keeps this library's kernels of other threads from between the two; one of another
+    // kind that is put there has ended when this one starts.
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch(c_lo + s);
     stream_order();
@@ -709,10 +712,12 @@ dp_status_t dp_allgather_linear_w4(const void* x, int M, int D, long long ld,
   p.err = dev.err_word;
   p.units = (int)((long long)K * p.tiles_f * 4);
   cudaError_t e = cudaSuccess;
+  std::unique_lock<std::mutex> pair(dph::early_launches(), std::defer_lock);
   if (need) {
+    pair.lock();  // (the product reads weights on the strength of prepare_kernel's wait)
     XParams q{p.x, ld, D, (D + kStep - 1) / kStep, p.x_vec, static_cast<uint16_t*>(workspace),
               reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + prepared_bytes(M, D))};
-    e = dph::launch_early(prepare_kernel, q, (unsigned)M, kXThreads, s);
+    e = dph::launch_early_held(prepare_kernel, q, (unsigned)M, kXThreads, s);
     p.x = q.out;
     p.xexp = q.xexp;
   }

@@ -11,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+from ring_allreduce_gradient_gb300 import binding as B
 from ring_allreduce_gradient_gb300 import mx4
 
 pytestmark = pytest.mark.gpu
@@ -346,3 +347,43 @@ def test_one_token_and_the_same_one_in_a_batch(fmt):
             if D == 128:
                 assert torch.equal(y, alone[:M])
             assert bool(((y - alone[:M]).double().abs() <= 4 * (D + 8) * U * size[:M]).all())
+
+
+def test_weights_rewritten_by_another_thread_on_the_same_stream():
+    """A product of prepared tokens is of the weights before or after the other thread's
+    quantisation, never of some of both: the call's two kernels stay together."""
+    import threading
+    D, F, M, runs = 1024, 8192, 12, 300
+    w = [normal((F, D), i, 0.02).bfloat16() for i in range(2)]
+    q = mx4.quantize(w[0], "nvfp4")
+    x = normal((M, D), 3).bfloat16()
+    want = []
+    for i in range(2):
+        B.dp_mx4_quantize([w[i]], 1, F, D, D, B.DP_BF16, B.DP_NVFP4, False, None, q.codes, q.scales)
+        want.append(mx4.linear_w4(x, [q]))
+    torch.cuda.synchronize()
+    assert not torch.equal(*want)
+    stream = torch.cuda.Stream()
+    got, errors = [], []
+    go = threading.Barrier(2)
+
+    def quantise():
+        try:
+            go.wait()
+            for i in range(2 * runs):
+                B.dp_mx4_quantize([w[i % 2]], 1, F, D, D, B.DP_BF16, B.DP_NVFP4, False, None,
+                                  q.codes, q.scales, stream=stream.cuda_stream)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    other = threading.Thread(target=quantise)
+    other.start()
+    with torch.cuda.stream(stream):
+        go.wait()
+        for _ in range(runs):
+            got.append(mx4.linear_w4(x, [q]))
+    other.join()
+    torch.cuda.synchronize()
+    assert not errors
+    same = [[torch.equal(y, z) for z in want] for y in got]
+    assert all(any(s) for s in same)
