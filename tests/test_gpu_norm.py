@@ -100,6 +100,12 @@ def check_quantised(q, y64, t=1.0, margin=32 * U):
     assert np.all(np.abs(got - y64) <= (64 if q.format == "mxfp8" else 4) * step)
 
 
+@pytest.fixture(autouse=True)
+def no_expired_wait():
+    yield
+    assert B.dp_get_device_error() == B.DP_OK
+
+
 def f64(t):
     return t.double().cpu().numpy()
 

@@ -20,6 +20,12 @@ DEV = torch.device("cuda", 0)
 U = 2.0 ** -24
 
 
+@pytest.fixture(autouse=True)
+def no_expired_wait():
+    yield
+    assert B.dp_get_device_error() == B.DP_OK
+
+
 def f64(t):
     return t.double().cpu().numpy()
 
