@@ -856,12 +856,14 @@ DP_API dp_status_t dp_allgather_linear_mx8_workspace_size(int M, int D, size_t* 
  * NULL for 1) and dp_mx8_quantize define them, from the unrounded y.  y may then
  * be NULL; without a format codes and scales are.
  * Arithmetic in fp32: a thread sums 16 or 32 squares in four chains, the rest is
- * pairwise (the same bits for a row in any call, but for rows that start off 32-byte
- * boundaries).  That holds magnitudes up to 3.2e18; where the sum passes fp32 the
- * mean is infinite, rstd 0, and y 0, or NaN where h * weight, which is formed first,
- * is infinite; in other rows it has to stay within fp32, too.  With an eps below
- * 1e-30, rows below 5e-19 lose bits of rstd and rows below 1e-23 count as zeros (rstd
- * is then infinite if eps is 0).  A row with a NaN is NaN throughout.
+ * pairwise (the same bits for a row in any call with a format, and in any without one
+ * where D is a multiple of 16 and the weight and every buffer's rows start on 32-byte
+ * boundaries; other calls sum in another order).  That holds magnitudes up to 3.2e18;
+ * where the sum passes fp32 the mean is infinite, rstd 0, and y 0, or NaN where
+ * h * weight, which is formed first, is infinite; in other rows it has to stay within
+ * fp32, too.  With an eps below 1e-30, rows below 5e-19 lose bits of rstd and rows
+ * below 1e-23 count as zeros (rstd is then infinite if eps is 0).  A row with a NaN is
+ * NaN throughout.
  * Requires D <= 32768, and D % 32 == 0 with a format; eps >= 0 and finite.
  * M == 0 or D == 0 writes nothing, rstd neither.
  *

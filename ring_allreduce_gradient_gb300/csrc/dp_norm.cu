@@ -14,15 +14,16 @@
 // Both are bound by memory (bf16, residual, 8-bit output: 7.03 bytes an element
 // for about 10 operations; backward with dh: 8 bytes).  A row is held in
 // registers by its warps, 16 G elements a thread, from its load to its store, so
-// it crosses memory once; a thread's sixteen consecutive elements are one or two
+// it crosses memory once (where they suffice, see below); a thread's sixteen consecutive elements are one or two
 // 32-byte loads and half a block of 32 (the other half is its neighbour lane's).
 // Where a CTA takes several rows, the next ones are on their way to shared memory
 // by bulk copies.  Arithmetic is in pairs of fp32, one instruction each.
 //
 // Measured (GB300, launches in a CUDA graph, inputs larger than L2), 8192 x 4096
-// bf16: forward with residual to 8 bits 39.4 us (236 MB: 6.0 TB/s; 58 % of the
-// issue slots), backward with dh 45 us with the sum over 304 sets of rows (268 MB:
-// 6.0 TB/s, 75 % of DRAM under the profiler).  One row of 4096: 2.1 us, 1000 x 768
+// bf16: forward with residual to 8 bits 39.5 us (236 MB: 6.0 TB/s; 58 % of the
+// issue slots), to mxfp4 38, to nvfp4 41.5, plain 28 (134 MB; 44 with the residual),
+// backward with dh 45.5 us with the sum over 304 sets of rows (268 MB: 5.9 TB/s, 75 %
+// of DRAM under the profiler); fp32: 69, 68, 76, 44 (90) and 83 us.  One row of 4096: 2.1 us, 1000 x 768
 // fp32 4.8, 2050 x 1120 to nvfp4 8.7 (first loads, and the two divisors of each block
 // of 16), backward of 1031 x 1601 fp32 11 us (scalar accesses).  What led there: a CTA
 // for each row with scalar fp32 arithmetic 49 and 101 us; pairs of fp32 and
@@ -32,6 +33,16 @@
 // forward (3 stages 41 us, the whole share of the GPU in one turn 40.4), 3 stages and
 // 128 registers backward (80 registers, three CTAs an SM, spill: 60; 456 sets of rows
 // 55.7).
+//
+// Long rows do not fit the registers.  Above D = 8192 a thread has 32 elements (G = 2),
+// in 128 registers, and above 16384 in 64: what does not fit is spilled to local memory
+// (-Xptxas -v, bytes of stores a thread: backward up to 16384 444-1140, above that
+// 1584-2188; forward above 16384 584-1436, below it 108 at most), next to 64 or 128
+// bytes of an array that the thread's share of the row has.  Forward with residual to 8
+// bits / backward with dh, bf16: 8192 x 8192 91 / 93 us (5.2 / 5.8 TB/s), 4096 x 12288
+// 66 / 110 (5.3 / 3.7), 4096 x 16384 81 / 145 (5.8 / 3.7), 2048 x 24576 112 / 299 (3.2 /
+// 1.4), 2048 x 32768 156 / 462 (3.0 / 1.2); fp32: 150 / 160 (5.9 / 6.7), 133 / 195 (4.9 /
+// 4.1), 134 / 259 (6.5 / 4.2), 213 / 455 (3.1 / 1.8), 296 / 634 (3.0 / 1.7).
 
 #include "dp_early.cuh"
 #include "dp_launch.h"
@@ -52,7 +63,9 @@ enum { kPlain = 0, kToMx4 = 1, kToNv4 = 2, kToMx8 = 3 };
 
 // How a row is laid over threads: `warps` of them hold it, rows_cta rows at once
 // in a CTA.  vec: every row of every buffer starts on a 32-byte boundary and D is a
-// multiple of 16.  stages: sets of rows that are on their way to shared memory.
+// multiple of 16.  It is one flag for all of them, and without it every access is of one
+// element and no row comes ahead: 8192 x 4096 to 8 bits takes 228 us with the weight alone
+// off a boundary, against 39.5 (a flag for each buffer has not been built).  stages: sets of rows that are on their way to shared memory.
 struct RowPlan {
   int warps, rows_cta, vec, stages;
 };
@@ -731,6 +744,10 @@ dp_status_t dp_rms_norm(const void* x, long long ldx, const void* residual, long
   // A CTA keeps the weights and has rows ahead over a turn of several sets, as long
   // as there are CTAs enough to even out (8192 x 4096: 48.4 us with turns of one,
   // 41.3 of four, 39.4 of six, 39.5 of nine; 4000 x 768 bf16: 10.6 of one, 8.4 of two).
+  // What that measured is also how full the last round of CTAs is: 456 of them fit at
+  // once, and six make 3.00 rounds of 8192 rows, four 4.49, nine 2.00.  Elsewhere, to 8
+  // bits with residual: 4096 rows of 4096 (1.50 rounds) 4.8 TB/s, 5000 5.4, 6000 (2.20)
+  // 5.1, 10000 5.9, 8192 of 2048 (1.50) 4.6; the turn of 8192 x 4096 has 5.9.
   p.span = (int)std::max(1ll, std::min(6ll, sets / (dev.sm_count * 3)));
   p.err = dev.err_word;
   const int threads = p.plan.warps * p.plan.rows_cta * 32;

@@ -37,8 +37,14 @@
 // either form (5.3 TB/s of weights in nvfp4), eight 62 us, 16 71 us in mxfp4, 32 116
 // us; 4096 x 4096: one token 6.9 us, 16 8.6 us.  What bounds it: one token's bytes
 // alone (no decoding, no products) take 52 us and its instructions alone (the same
-// codes again and again) 50; 16 tokens' instructions 66; 32 tokens' MMAs 138 clocks
-// of a step, against the 87 in which its bytes arrive.  Neither rings of 4 or 5 steps
+// codes again and again) 50.  16 tokens' instructions alone take 66, with nothing full
+// (53 % of the issue slots, 51 % of DRAM, 44 % of the tensor pipe): 2048 units are 14
+// warps on each of 147 SMs, four on half of the schedulers and three on the others,
+// and all wait for four.  32 tokens: MMAs, 138 clocks of a step against the 87 in which
+// its bytes arrive; there 128 registers do not suffice (-Xptxas -v, bytes of spill
+// stores a thread: nvfp4 76, mxfp4 48; 16 tokens in nvfp4 16).  Rows past a shard's
+// end are decoded and multiplied like the others, so shards of fewer than 128 rows
+// cost as much as ones of 128.  Neither rings of 4 or 5 steps
 // nor 28 warps of 72 registers gained anything.  The steps that led here: x
 // converted by each warp for itself 83 us (one token, nvfp4) and 138 us (16, mxfp4);
 // rings half as large, twice the warps 69 and 128; x staged for the CTA 59 and 91; x

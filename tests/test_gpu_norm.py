@@ -602,3 +602,22 @@ def test_a_row_of_nothing_has_no_mean():
     n = norm.rms_norm(torch.zeros(2, 0, device=DEV), torch.ones(0, device=DEV),
                       residual=torch.zeros(2, 0, device=DEV), format="mxfp8")
     assert n.rstd.isnan().all() and n.q.rows == 2 and n.q.cols == 0
+
+
+def test_which_calls_have_the_same_bits():
+    """A row's bits are one in all calls with a format, and in calls without one whose buffers are
+    all on 32-byte boundaries; otherwise sums have another order, within both tolerances."""
+    rng = np.random.default_rng(11)
+    M, D = 40, 1120
+    x, res = matrix(rng, M, D, torch.bfloat16), matrix(rng, M, D, torch.bfloat16)
+    odd = matrix(rng, M, D, torch.bfloat16, ld=D + 3, offset=1)
+    odd.copy_(x)
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(D + 1)).float().to(DEV)
+    w_odd, w = w[1:], w[1:].clone()
+    want = norm.rms_norm(x, w, residual=res)
+    for a, b, fmt in ((x, w, "mxfp8"), (odd, w, "mxfp8"), (x, w_odd, "mxfp4"), (odd, w_odd, "nvfp4")):
+        n = norm.rms_norm(a, b, residual=res, format=fmt, keep=True)
+        assert torch.equal(n.rstd, want.rstd) and torch.equal(n.y, want.y)
+    for a, b in ((odd, w), (x, w_odd), (odd, w_odd)):
+        n = norm.rms_norm(a, b, residual=res)
+        assert bool(((n.rstd - want.rstd).abs() <= 32 * U * want.rstd).all())
